@@ -56,7 +56,10 @@ typedef enum {
     TILES_ERR_TOO_LARGE = -7         /* size beyond a documented maximum */
 } tiles_status;
 
-typedef enum { TILES_F16 = 0, TILES_BF16 = 1, TILES_F32 = 2 } tiles_dtype;
+/* E4M3 (8-bit floating point, 4 exponent and 3 mantissa bits, largest value
+ * 448, no infinities) is a storage type of the block-scaled operators at the
+ * end of this header; the GEMM and the convolution do not take it. */
+typedef enum { TILES_F16 = 0, TILES_BF16 = 1, TILES_F32 = 2, TILES_E4M3 = 3 } tiles_dtype;
 
 /* MMA families of the constraint C3.  MMA, WGMMA and SIMT are the page's
  * instruction-shape table; TCGEN05 is the sm_100/sm_103 tensor-core MMA
@@ -575,6 +578,149 @@ int tiles_selftest_wait_timeout(void* workspace, int64_t limit_ns, void* stream)
  * groups of the launch run normally.  The launch consumes the fault; stage
  * < 0 disarms it.  INVALID_ARG unless 0 < limit_ns <= 1e10. */
 int tiles_selftest_drop_stage(int stage, int64_t limit_ns);
+
+/* ---- Norms, 8-bit products and products grouped by expert -----------------
+ * The operators around the GEMM in a transformer block.  8-bit matrices hold
+ * e4m3 values with fp32 scales: rows of activations carry one scale per row
+ * and 128 columns, weights one scale per 128 x 128 block.  Scale arrays are
+ * indexed through explicit strides (in floats), so either order of rows and
+ * blocks works; blocks stored outermost ([blocks][rows]) load fastest.
+ * Number of blocks of a length n: ceil(n / 128); the last may be short.
+ * A row count of 0 is allowed and does nothing. */
+
+/* h = x + residual;  y = h * (mean(h^2) + eps)^(-1/2) * weight,  row by row.
+ * The sum, the mean and the norm are fp32 and read the sum before it is
+ * rounded into h.  out_dtype is dtype, or E4M3: then
+ *   scale = max(max|y| over the block / 448, 2^-126),  y8 = e4m3(y / scale)
+ * (round to nearest even; a NaN in a row makes its outputs and scales NaN). */
+typedef struct {
+    int64_t rows, cols;               /* rows >= 0, cols >= 1 */
+    const void* x;                    /* device, rows x cols */
+    const void* residual;             /* device, rows x cols, or NULL: h = x */
+    const void* weight;               /* device, cols */
+    void* h;                          /* device, rows x cols; NULL: h is not stored */
+    void* y;                          /* device, rows x cols, out_dtype */
+    float* scales;                    /* device, E4M3 only */
+    int64_t ldx, ldr, ldh, ldy;       /* row pitches, elements */
+    int64_t scale_row, scale_block;   /* scale of (row, block) at row*scale_row + block*scale_block */
+    float eps;
+    int32_t dtype;                    /* of x, residual and h: F16, BF16 or F32 */
+    int32_t weight_dtype;             /* F16, BF16 or F32 */
+    int32_t out_dtype;                /* dtype or E4M3 */
+} tiles_rmsnorm_desc;
+
+/* Pointers need only their element's alignment; rows whose base and pitch
+ * are 16-byte multiples are read in 16-byte pieces.  No workspace: the
+ * kernel waits on nothing. */
+int tiles_rmsnorm(const tiles_rmsnorm_desc* desc, void* stream);
+
+/* Gradients of tiles_rmsnorm at h, with u = mean(h^2) + eps:
+ *   dx_j = dy_j w_j u^(-1/2) - h_j (sum_i dy_i w_i h_i) u^(-3/2) / cols + dh_j
+ *   dweight_j = sum over rows of dy_j h_j u^(-1/2)
+ * dx is the gradient of x and of the residual alike; dh, the gradient that
+ * reaches h past the norm, may be NULL.  dweight is fp32.  The sum over rows
+ * runs in a fixed order for given sizes and device. */
+typedef struct {
+    int64_t rows, cols;
+    const void* dy;
+    const void* h;
+    const void* weight;
+    const void* dh;                   /* or NULL */
+    void* dx;
+    float* dweight;                   /* cols; zeros when rows == 0 */
+    int64_t lddy, ldh, lddh, lddx;    /* row pitches, elements */
+    float eps;
+    int32_t dtype;                    /* of dy, h, dh and dx */
+    int32_t weight_dtype;
+    int32_t pad0;
+} tiles_rmsnorm_grad_desc;
+
+/* Workspace bytes of the gradient: the partial weight gradients of the
+ * blocks that sweep the rows (0 on invalid arguments). */
+size_t tiles_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
+
+int tiles_rmsnorm_grad(const tiles_rmsnorm_grad_desc* desc, void* workspace, size_t ws_bytes,
+                       void* stream);
+
+/* e4m3 values and scales of `batch` row-major matrices, one scale per row and
+ * 128 columns (block_rows 1) or per 128 x 128 block (block_rows 128); the
+ * scale rule of tiles_rmsnorm. */
+typedef struct {
+    int64_t batch, rows, cols;
+    const void* x;
+    void* q;
+    float* scales;
+    int64_t ldx, stride_x;            /* elements */
+    int64_t ldq, stride_q;
+    int64_t scale_row, scale_col, scale_batch;   /* strides between block rows, block columns, items */
+    int32_t dtype;                    /* of x: F16, BF16 or F32 */
+    int32_t block_rows;               /* 1 or 128 */
+} tiles_quantize_desc;
+
+int tiles_quantize_fp8(const tiles_quantize_desc* desc, void* stream);
+
+/* How the weight of a product is stored. */
+typedef enum { TILES_B_KN = 0, TILES_B_NK = 1 } tiles_b_layout;
+
+/* Rows times a weight: dense (groups 0) or grouped by expert.
+ *   dense:    c[i] = a[i] x b             for the m rows of a
+ *   grouped:  c[i] = a[i] x b[g]          for the rows i in [offsets[g], offsets[g+1])
+ * offsets (groups + 1 int32 on the device, ascending) is read by the kernel
+ * only: no copy to the host, so a router's counts can stay on the device.
+ * Rows outside every group are not written; offsets outside [0, m] count as
+ * the nearer end, and a descending pair as an empty group.
+ * in_dtype F16/BF16: a is m x k, b is k x n (TILES_B_KN) or n x k
+ *   (TILES_B_NK: c = a x b^T, the form of the rows' gradient under a KN
+ *   weight), grouped only; fp32 accumulation over all of k.
+ * in_dtype E4M3: b is n x k (TILES_B_NK), and
+ *   c[i][j] = sum over blocks t of as[i][t] * bs[j/128][t] * (sum over k in t of a[i][k] * b[j][k])
+ *   with the inner sums in the tensor core and the outer sum in fp32.
+ * c is F32, F16 or BF16 (round to nearest even).  a and b need 16-byte
+ * aligned bases, row pitches and group strides (TMA); c and the scales only
+ * their element's. */
+typedef struct {
+    int64_t m, n, k;                  /* m >= 0; n, k >= 1 */
+    int64_t groups;                   /* 0: dense; at most 4096 */
+    const int32_t* offsets;           /* device, groups + 1; NULL when dense */
+    const void* a;                    /* device, m x k */
+    const void* b;                    /* device */
+    void* c;                          /* device, m x n */
+    const float* a_scales;            /* E4M3: at row*a_scale_row + block*a_scale_block */
+    const float* b_scales;            /* E4M3: at (j/128)*b_scale_row + block*b_scale_block
+                                         + group*b_scale_group */
+    int64_t lda, ldb, ldc, stride_b;  /* elements; stride_b between groups' weights */
+    int64_t a_scale_row, a_scale_block;
+    int64_t b_scale_row, b_scale_block, b_scale_group;
+    int32_t in_dtype, out_dtype;
+    int32_t b_layout;                 /* tiles_b_layout */
+    int32_t pad0;
+} tiles_product_desc;
+
+/* The dense 8-bit product (in_dtype E4M3, groups 0).  Workspace: at least
+ * tiles_workspace_bytes() (the error word). */
+int tiles_gemm_fp8(const tiles_product_desc* desc, void* workspace, size_t ws_bytes, void* stream);
+
+/* The grouped product (groups >= 1), 16-bit or 8-bit. */
+int tiles_grouped_gemm(const tiles_product_desc* desc, void* workspace, size_t ws_bytes,
+                       void* stream);
+
+/* Weight gradients of the grouped product: dw[g] = a_g^T x dc_g over the rows
+ * of group g (zeros for an empty group), fp32 accumulation. */
+typedef struct {
+    int64_t m;                        /* rows, >= 0 */
+    int64_t k, n;                     /* columns of a and of dc: dw[g] is k x n */
+    int64_t groups;
+    const int32_t* offsets;           /* device, groups + 1 */
+    const void* a;                    /* device, m x k */
+    const void* dc;                   /* device, m x n */
+    void* dw;                         /* device, groups x k x n */
+    int64_t lda, lddc, lddw, stride_dw;
+    int32_t in_dtype;                 /* F16 or BF16 */
+    int32_t out_dtype;                /* F32, F16 or BF16 */
+} tiles_wgrad_desc;
+
+int tiles_grouped_wgrad(const tiles_wgrad_desc* desc, void* workspace, size_t ws_bytes,
+                        void* stream);
 
 #ifdef __cplusplus
 }

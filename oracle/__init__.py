@@ -18,5 +18,7 @@ Contents
             tutorial's problem statement C = A x B).
   conv      H-tile row formulas (tutorial section "H/W 维切分的通用公式") and a
             direct float64 convolution, untiled and H-tiled.
+  operators the norm with its gradients, 8-bit values with block scales, and
+            the dense and grouped products, from their formulas.
   tolerance the pass criterion |C - C_ref| <= 1e-3 * S + ulp_out(C_ref).
 """

@@ -1,5 +1,6 @@
 """tile_size_decision_gb300 — constraint-planned tiled GEMM and H-tiled
-convolution for NVIDIA GB300 (sm_103a).
+convolution for NVIDIA GB300 (sm_103a), with the norms, 8-bit products and
+expert-grouped products that surround the GEMM in a transformer block.
 
 A thin Python binding over libtiles.so (C ABI in include/tiles.h).  The
 binding only marshals arguments: planning (C0-C4), tensor-map encoding and
@@ -25,6 +26,8 @@ __all__ = [
     "conv_workspace",
     "conv_out_shape", "conv_out_hw", "check", "selftest_wait_timeout", "selftest_drop_stage",
     "make_config",
+    "rmsnorm", "rmsnorm_fp8", "rmsnorm_grad", "rmsnorm_grad_workspace", "quantize_fp8",
+    "gemm_fp8", "grouped_gemm", "grouped_gemm_fp8", "grouped_wgrad",
 ]
 
 
@@ -509,3 +512,311 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
     """Arm a planted fault for this thread's next GEMM or TMA convolution
     launch (tiles_selftest_drop_stage); stage < 0 disarms."""
     _check(load().tiles_selftest_drop_stage(stage, limit_ns), "tiles_selftest_drop_stage")
+
+
+# ---- norms, 8-bit products and products grouped by expert ------------------------
+
+
+SCALE_BLOCK = 128     # columns (and weight rows) that share one scale
+
+
+def _rows2(t, name):
+    """Checks a CUDA matrix with unit stride along its rows; its row pitch.  The pitch of
+    a single row is never used: it is reported as whole 16-byte pieces."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _vector(t, n, name):
+    if not t.is_cuda or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous CUDA vector of {n} elements")
+    return t.data_ptr()
+
+
+def _like(t, x, name):
+    """Row pitch of a matrix of x's shape and type (x itself gives both)."""
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must have the shape {tuple(x.shape)}, not {tuple(t.shape)}")
+    if t.dtype != x.dtype:
+        raise TypeError(f"{name} must be {x.dtype}, not {t.dtype}")
+    return _rows2(t, name)
+
+
+def _blocks(n):
+    return (n + SCALE_BLOCK - 1) // SCALE_BLOCK
+
+
+def _empty_fp8(torch, lead, cols, device):
+    """e4m3 rows whose pitch is whole 16-byte pieces, as the products need."""
+    pitch = (cols + 15) // 16 * 16
+    q = torch.empty((*lead, pitch), dtype=torch.float8_e4m3fn, device=device)
+    return q if pitch == cols else q[..., :cols]
+
+
+def _rmsnorm(x, weight, residual, eps, y, scales, h, out_code, stream):
+    rows, cols = x.shape
+    ldx = _rows2(x, "x")
+    code = _dtype_code(x)
+    ldr = _like(residual, x, "residual") if residual is not None else 0
+    ldh = _like(h, x, "h_out") if h is not None else 0
+    wptr = _vector(weight, cols, "weight")
+    sr = sb = 0
+    if scales is not None:
+        if scales.shape != (rows, _blocks(cols)) or scales.dtype != _torch().float32 or \
+                not scales.is_cuda:
+            raise ValueError(f"scales must be a float32 CUDA tensor of shape "
+                             f"{(rows, _blocks(cols))}")
+        sr, sb = scales.stride()
+    d = _abi.RmsnormDesc(rows, cols, x.data_ptr(),
+                         residual.data_ptr() if residual is not None else None, wptr,
+                         h.data_ptr() if h is not None else None, y.data_ptr(),
+                         scales.data_ptr() if scales is not None else None, ldx, ldr, ldh,
+                         _rows2(y, "out"), sr, sb, eps, code, _dtype_code(weight),
+                         code if out_code is None else out_code)
+    _check(load().tiles_rmsnorm(C.byref(d), _stream_handle(stream)), "tiles_rmsnorm")
+
+
+def rmsnorm(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=None):
+    """h = x + residual and y = h * (mean(h^2) + eps)^(-1/2) * weight, row by
+    row of a matrix; returns (y, h) in x's type.  Without a residual h is x
+    itself.  h_out may be the residual (updated in place)."""
+    torch = _torch()
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    if out is not None:
+        _like(out, x, "out")
+    if residual is None:
+        h = x
+    else:
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if h_out is None else h_out
+    _rmsnorm(x, weight, residual, eps, y, None, None if residual is None else h, None, stream)
+    return y, h
+
+
+def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out=None,
+                stream=None):
+    """The norm of rmsnorm with y in 8 bits: returns (q, scales, h), e4m3
+    values and one fp32 scale per row and 128 columns, y ~ q * scale.  New
+    scales are stored block by block (a transposed view, rows x blocks),
+    which the products read fastest."""
+    torch = _torch()
+    rows, cols = x.shape
+    q = _empty_fp8(torch, (rows,), cols, x.device) if out is None else out
+    if q.shape != x.shape or q.dtype != torch.float8_e4m3fn:
+        raise ValueError("out must be float8_e4m3fn of x's shape")
+    if scales is None:
+        scales = torch.empty((_blocks(cols), rows), dtype=torch.float32, device=x.device).t()
+    if residual is None:
+        h = x
+    else:
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if h_out is None else h_out
+    _rmsnorm(x, weight, residual, eps, q, scales, None if residual is None else h, _abi.E4M3,
+             stream)
+    return q, scales, h
+
+
+def rmsnorm_grad_workspace(x):
+    """A workspace for rmsnorm_grad on matrices of x's shape."""
+    torch = _torch()
+    rows, cols = x.shape
+    n = int(load().tiles_rmsnorm_grad_workspace_bytes(rows, cols))
+    if n == 0:
+        raise TilesError(_abi.ERR_INVALID_ARG, "tiles_rmsnorm_grad_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def rmsnorm_grad(dy, h, weight, eps=1e-6, dh=None, dx_out=None, dweight_out=None, workspace=None,
+                 stream=None):
+    """Gradients of rmsnorm at h, given those of y (dy) and, where h is used
+    past the norm, of h (dh): returns (dx, dweight).  dx, in h's type, is the
+    gradient of x and of the residual alike; dweight is fp32."""
+    torch = _torch()
+    rows, cols = h.shape
+    ldh = _rows2(h, "h")
+    lddy = _like(dy, h, "dy")
+    lddh = _like(dh, h, "dh") if dh is not None else 0
+    dx = torch.empty(h.shape, dtype=h.dtype, device=h.device) if dx_out is None else dx_out
+    dw = torch.empty(cols, dtype=torch.float32, device=h.device) if dweight_out is None \
+        else dweight_out
+    if dw.dtype != torch.float32:
+        raise TypeError("dweight_out must be float32")
+    d = _abi.RmsnormGradDesc(rows, cols, dy.data_ptr(), h.data_ptr(),
+                             _vector(weight, cols, "weight"),
+                             dh.data_ptr() if dh is not None else None, dx.data_ptr(),
+                             _vector(dw, cols, "dweight_out"), lddy, ldh, lddh,
+                             _like(dx, h, "dx_out"), eps, _dtype_code(h), _dtype_code(weight), 0)
+    ws, wsb = _workspace_args(workspace)
+    _check(load().tiles_rmsnorm_grad(C.byref(d), ws, wsb, _stream_handle(stream)),
+           "tiles_rmsnorm_grad")
+    return dx, dw
+
+
+def _workspace_args(workspace):
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def quantize_fp8(x, block_rows=1, stream=None):
+    """e4m3 values and fp32 scales of x (a matrix, or a batch of them): one
+    scale per row and 128 columns (block_rows 1: activations; the scales are
+    stored block by block, as a view rows x blocks) or per 128 x 128
+    (block_rows 128: weights)."""
+    torch = _torch()
+    if not x.is_cuda or x.dim() not in (2, 3):
+        raise ValueError("x must be a CUDA matrix or a batch of them")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("x must have unit stride in its last dimension")
+    if block_rows not in (1, SCALE_BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    *lead, rows, cols = x.shape
+    batch = lead[0] if lead else 1
+    q = _empty_fp8(torch, (*lead, rows), cols, x.device)
+    nb = _blocks(cols)
+    if block_rows == 1:
+        scales = torch.empty((*lead, nb, rows), dtype=torch.float32,
+                             device=x.device).transpose(-1, -2)
+    else:
+        scales = torch.empty((*lead, _blocks(rows), nb), dtype=torch.float32, device=x.device)
+    d = _abi.QuantizeDesc(batch, rows, cols, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                          x.stride(-2) if rows > 1 else max(x.stride(-2), cols),
+                          x.stride(0) if lead else 0, max(q.stride(-2), cols),
+                          q.stride(0) if lead else 0, scales.stride(-2), scales.stride(-1),
+                          scales.stride(0) if lead else 0, _dtype_code(x), block_rows)
+    _check(load().tiles_quantize_fp8(C.byref(d), _stream_handle(stream)), "tiles_quantize_fp8")
+    return q, scales
+
+
+def _out_rows(out, rows, cols, out_dtype, like):
+    if out is None:
+        return _alloc_out((rows, cols), like, out_dtype)
+    if out.shape != (rows, cols):
+        raise ValueError(f"out must have the shape {(rows, cols)}")
+    return out
+
+
+def _weight(b, groups, name="b"):
+    """Row pitch and group stride of a weight (grouped: 3-D)."""
+    if b.dim() != (3 if groups else 2):
+        raise ValueError(f"{name} must have {3 if groups else 2} dimensions")
+    if not b.is_cuda or (b.shape[-1] > 1 and b.stride(-1) != 1):
+        raise ValueError(f"{name} must be a CUDA tensor with unit stride in its last dimension")
+    ld = b.stride(-2) if b.shape[-2] > 1 else (b.shape[-1] + 15) // 16 * 16
+    return ld, b.stride(0) if groups else 0
+
+
+def _offsets(offsets, groups):
+    torch = _torch()
+    if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.shape != (groups + 1,) or \
+            offsets.stride(0) != 1:
+        raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {groups + 1} elements")
+    return offsets.data_ptr()
+
+
+def _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype, workspace, stream, where):
+    torch = _torch()
+    grouped = offsets is not None
+    lda = _rows2(a, "a")
+    ldb, stride_b = _weight(b, grouped)
+    m, k = a.shape
+    n = b.shape[-2]
+    if a.dtype != torch.float8_e4m3fn or b.dtype != torch.float8_e4m3fn:
+        raise TypeError("a and b must be float8_e4m3fn")
+    if b.shape[-1] != k:
+        raise ValueError(f"shape mismatch: {tuple(a.shape)} x {tuple(b.shape)}^T")
+    groups = b.shape[0] if grouped else 0
+    kb = _blocks(k)
+    want = (groups, _blocks(n), kb) if grouped else (_blocks(n), kb)
+    for s, shape, name in ((a_scales, (m, kb), "a_scales"), (b_scales, want, "b_scales")):
+        if s.shape != shape or s.dtype != torch.float32 or not s.is_cuda:
+            raise ValueError(f"{name} must be a float32 CUDA tensor of shape {shape}")
+    if out is None and out_dtype is None:
+        out_dtype = "bf16"
+    out = _out_rows(out, m, n, out_dtype, a)
+    sbs = b_scales.stride()
+    d = _abi.ProductDesc(m, n, k, groups, _offsets(offsets, groups) if grouped else None,
+                         a.data_ptr(), b.data_ptr(), out.data_ptr(), a_scales.data_ptr(),
+                         b_scales.data_ptr(), lda, ldb, _rows2(out, "out"), stride_b,
+                         a_scales.stride(0), a_scales.stride(1), sbs[-2], sbs[-1],
+                         sbs[0] if grouped else 0, _abi.E4M3, _dtype_code(out), _abi.B_NK, 0)
+    ws, wsb = _workspace_args(workspace)
+    fn = load().tiles_grouped_gemm if grouped else load().tiles_gemm_fp8
+    _check(fn(C.byref(d), ws, wsb, _stream_handle(stream)), where)
+    return out
+
+
+def gemm_fp8(a, a_scales, b, b_scales, out=None, out_dtype=None, workspace=None, stream=None):
+    """out[i][j] = sum over blocks t of 128 of a_scales[i][t] * b_scales[j//128][t]
+    * (a[i] . b[j] within t): e4m3 rows (m x k, as rmsnorm_fp8 and
+    quantize_fp8 give them) times an e4m3 weight stored n x k.  out is bf16
+    unless out_dtype ("f32", "f16", "bf16") says otherwise."""
+    return _product_fp8(a, a_scales, b, b_scales, None, out, out_dtype, workspace, stream,
+                        "tiles_gemm_fp8")
+
+
+def grouped_gemm_fp8(a, a_scales, b, b_scales, offsets, out=None, out_dtype=None, workspace=None,
+                     stream=None):
+    """gemm_fp8 with a weight per group (b: groups x n x k): rows offsets[g] ..
+    offsets[g+1] - 1 of a meet b[g].  offsets is an int32 CUDA vector that
+    only the kernel reads.  Rows outside every group are not written."""
+    return _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype, workspace, stream,
+                        "tiles_grouped_gemm")
+
+
+def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspace=None,
+                 stream=None):
+    """out[i] = a[i] @ b[g] for the rows i of group g, offsets[g] <= i <
+    offsets[g+1]: fp16/bf16 rows (m x k) and weights (groups x k x n).  With
+    trans_b the weights are groups x n x k and out[i] = a[i] @ b[g]^T, which
+    is the gradient of the rows when a is that of the products.  offsets is
+    an int32 CUDA vector that only the kernel reads.  Rows outside every
+    group are not written."""
+    lda = _rows2(a, "a")
+    ldb, stride_b = _weight(b, True)
+    m, k = a.shape
+    groups, bk, n = (b.shape[0], b.shape[2], b.shape[1]) if trans_b else b.shape
+    if bk != k:
+        raise ValueError(f"shape mismatch: {tuple(a.shape)} x {tuple(b.shape)}"
+                         f"{'^T' if trans_b else ''}")
+    if b.dtype != a.dtype:
+        raise TypeError("a and b must share a dtype")
+    out = _out_rows(out, m, n, out_dtype, a)
+    d = _abi.ProductDesc(m, n, k, groups, _offsets(offsets, groups), a.data_ptr(), b.data_ptr(),
+                         out.data_ptr(), None, None, lda, ldb, _rows2(out, "out"), stride_b, 0, 0,
+                         0, 0, 0, _dtype_code(a), _dtype_code(out),
+                         _abi.B_NK if trans_b else _abi.B_KN, 0)
+    ws, wsb = _workspace_args(workspace)
+    _check(load().tiles_grouped_gemm(C.byref(d), ws, wsb, _stream_handle(stream)),
+           "tiles_grouped_gemm")
+    return out
+
+
+def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stream=None):
+    """out[g] = a_g^T @ dc_g over the rows of group g: the weight gradients
+    (groups x k x n) of out = grouped_gemm(a, w, offsets), given dc.  An
+    empty group's gradient is zero."""
+    torch = _torch()
+    lda, lddc = _rows2(a, "a"), _rows2(dc, "dc")
+    m, k = a.shape
+    n = dc.shape[1]
+    if dc.shape[0] != m:
+        raise ValueError("a and dc must have the same rows")
+    if dc.dtype != a.dtype:
+        raise TypeError("a and dc must share a dtype")
+    groups = offsets.shape[0] - 1
+    if out is None:
+        out = _alloc_out((groups, k, n), a, out_dtype)
+    if out.shape != (groups, k, n):
+        raise ValueError(f"out must have the shape {(groups, k, n)}")
+    ldw, stride_dw = _weight(out, True, "out")
+    d = _abi.WgradDesc(m, k, n, groups, _offsets(offsets, groups), a.data_ptr(), dc.data_ptr(),
+                       out.data_ptr(), lda, lddc, ldw, stride_dw, _dtype_code(a), _dtype_code(out))
+    ws, wsb = _workspace_args(workspace)
+    _check(load().tiles_grouped_wgrad(C.byref(d), ws, wsb, _stream_handle(stream)),
+           "tiles_grouped_wgrad")
+    return out

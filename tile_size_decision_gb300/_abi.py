@@ -24,7 +24,7 @@ ERR_TIMEOUT = -6
 ERR_TOO_LARGE = -7
 
 # tiles_dtype
-F16, BF16, F32 = 0, 1, 2
+F16, BF16, F32, E4M3 = 0, 1, 2, 3
 DTYPE_CODES = {"f16": F16, "bf16": BF16, "f32": F32}
 
 # tiles_instr
@@ -133,6 +133,42 @@ class ConvDesc(C.Structure):
 LAYOUT_NCHW, LAYOUT_NHWC = 0, 1
 
 
+def _fields(spec):
+    """Structure fields from "type name name ...; type name ..." text."""
+    kinds = {"i64": C.c_int64, "i32": C.c_int32, "f32": C.c_float, "ptr": C.c_void_p}
+    return [(name, kinds[part.split()[0]]) for part in spec.split(";")
+            for name in part.split()[1:]]
+
+
+class RmsnormDesc(C.Structure):
+    _fields_ = _fields("i64 rows cols; ptr x residual weight h y scales; i64 ldx ldr ldh ldy "
+                       "scale_row scale_block; f32 eps; i32 dtype weight_dtype out_dtype")
+
+
+class RmsnormGradDesc(C.Structure):
+    _fields_ = _fields("i64 rows cols; ptr dy h weight dh dx dweight; i64 lddy ldh lddh lddx; "
+                       "f32 eps; i32 dtype weight_dtype pad0")
+
+
+class QuantizeDesc(C.Structure):
+    _fields_ = _fields("i64 batch rows cols; ptr x q scales; i64 ldx stride_x ldq stride_q "
+                       "scale_row scale_col scale_batch; i32 dtype block_rows")
+
+
+class ProductDesc(C.Structure):
+    _fields_ = _fields("i64 m n k groups; ptr offsets a b c a_scales b_scales; i64 lda ldb ldc "
+                       "stride_b a_scale_row a_scale_block b_scale_row b_scale_block "
+                       "b_scale_group; i32 in_dtype out_dtype b_layout pad0")
+
+
+class WgradDesc(C.Structure):
+    _fields_ = _fields("i64 m k n groups; ptr offsets a dc dw; i64 lda lddc lddw stride_dw; "
+                       "i32 in_dtype out_dtype")
+
+
+B_KN, B_NK = 0, 1
+
+
 # Every exported entry point: name -> (restype, argtypes).
 SIGNATURES = {
     "tiles_status_string": (C.c_char_p, [C.c_int]),
@@ -185,6 +221,14 @@ SIGNATURES = {
     "tiles_check": (C.c_int, [C.c_void_p, C.c_void_p]),
     "tiles_selftest_wait_timeout": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p]),
     "tiles_selftest_drop_stage": (C.c_int, [C.c_int, C.c_int64]),
+    "tiles_rmsnorm": (C.c_int, [C.POINTER(RmsnormDesc), C.c_void_p]),
+    "tiles_rmsnorm_grad_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "tiles_rmsnorm_grad": (C.c_int, [C.POINTER(RmsnormGradDesc), C.c_void_p, C.c_size_t,
+                                     C.c_void_p]),
+    "tiles_quantize_fp8": (C.c_int, [C.POINTER(QuantizeDesc), C.c_void_p]),
+    "tiles_gemm_fp8": (C.c_int, [C.POINTER(ProductDesc), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_grouped_gemm": (C.c_int, [C.POINTER(ProductDesc), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_grouped_wgrad": (C.c_int, [C.POINTER(WgradDesc), C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 _lib = None

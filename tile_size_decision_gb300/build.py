@@ -46,6 +46,10 @@ def units():
         ("conv_sm103a.cu", "conv_sm103a.o", []),
         ("conv_tma_sm103a.cu", "conv_tma_sm103a.o", []),
         ("host_pipeline.cu", "host_pipeline.o", []),
+        ("norm_sm103a.cu", "norm_sm103a.o", []),
+        ("stream_sm103a.cu", "stream_sm103a.o", []),
+        ("wgrad_sm103a.cu", "wgrad_sm103a.o", []),
+        ("product_api.cu", "product_api.o", []),
     ]
     for bn, cg in GEMM_VARIANTS:
         out.append(("gemm_sm103a.cu", f"gemm_bn{bn}_cg{cg}.o",

@@ -1,0 +1,107 @@
+// What the product kernels (dense 8-bit, grouped 16- and 8-bit, and the
+// grouped weight gradient) share: their arguments, the lookup of a tile among
+// ragged groups, and their host-side launches.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "gemm_sm103a.cuh"
+#include "launch_util.h"
+
+namespace tiles {
+
+constexpr int kScaleBlock = 128;      // columns (and weight rows) per scale
+constexpr int kMaxGroups = 4096;
+
+// Operand kinds of the products.
+constexpr int kWeight16KN = 0;        // 16-bit, b is k x n (MN-major weight)
+constexpr int kWeight16NK = 1;        // 16-bit, b is n x k (K-major weight)
+constexpr int kWeight8NK = 2;         // e4m3, b is n x k, block scales
+
+struct ProductArgs {
+    int32_t m, n, k;
+    int32_t groups;                   // 0: dense
+    const int32_t* offsets;
+    int32_t n_blocks, k_blocks;       // of the kernel's tile
+    int32_t split;                    // CTAs along K (a cluster)
+    void* c;
+    int64_t ldc;
+    int32_t c_dtype;
+    uint32_t idesc;
+    const float* sa;
+    const float* sb;
+    int64_t sa_row, sa_block, sb_row, sb_block, sb_group;
+    int32_t* err;
+    uint64_t wait_limit_ns;
+    int32_t drop_stage;               // test hook (-1: none)
+};
+
+// Rows [row0, end) of one tile of `group`.
+struct RowTile { int group, row0, end; };
+
+__device__ __forceinline__ int clamp_offset(int v, int m) { return min(max(v, 0), m); }
+
+// Tile `want` among the groups' tiles of `tile_rows` rows, in group order; a
+// warp looks at 32 groups at a time.  False past the last tile.
+__device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int groups, int m,
+                                              int tile_rows, int want, RowTile* out) {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+        const int g = g0 + lane;
+        int lo = 0, hi = 0;
+        if (g < groups) {
+            lo = clamp_offset(offsets[g], m);
+            hi = clamp_offset(offsets[g + 1], m);
+        }
+        const int tiles = hi > lo ? (hi - lo + tile_rows - 1) / tile_rows : 0;
+        int upto = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += t;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, want < base + upto);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            const int first = base + __shfl_sync(0xffffffffu, upto - tiles, src);
+            out->group = g0 + src;
+            out->row0 = __shfl_sync(0xffffffffu, lo, src) + (want - first) * tile_rows;
+            out->end = __shfl_sync(0xffffffffu, hi, src);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
+// One value in the output's type.
+__device__ __forceinline__ void store_one(void* c, int64_t at, float v, int dtype) {
+    if (dtype == TILES_F32) static_cast<float*>(c)[at] = v;
+    else if (dtype == TILES_F16) static_cast<__half*>(c)[at] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(c)[at] = __float2bfloat16_rn(v);
+}
+
+// The few-rows kernel: tile_rows in {16, 32, 64, 128}; units is the number
+// of (row tile, weight block) pairs launched.
+int launch_stream(int kind, int tile_rows, const CUtensorMap& weight, const CUtensorMap& rows,
+                  const ProductArgs& args, int64_t units, cudaStream_t st);
+
+struct WgradArgs {
+    int32_t m, k, n, groups;
+    const int32_t* offsets;
+    int32_t k_blocks, n_blocks;
+    void* dw;
+    int64_t lddw, stride_dw;
+    int32_t out_dtype;
+    uint32_t idesc;
+    int32_t* err;
+    uint64_t wait_limit_ns;
+    int32_t drop_stage;
+};
+
+int launch_wgrad(const CUtensorMap& a, const CUtensorMap& dc, const WgradArgs& args,
+                 cudaStream_t st);
+
+}  // namespace tiles

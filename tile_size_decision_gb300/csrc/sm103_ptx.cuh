@@ -61,6 +61,18 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t saddr, uint32_t rank) {
     return r;
 }
 
+// A 32-bit value from the shared memory of a CTA of the cluster.
+__device__ __forceinline__ float ld_shared_cluster(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// Barrier `id` (1 .. 15) among `threads` threads of the block.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // ---- mbarrier --------------------------------------------------------------
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -283,6 +295,18 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32acc(bool bf16, bool b_mn_maj
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The instruction descriptor with either operand's order given (0 = K-major,
+// 1 = MN-major), and that of kind::f8f6f4 with e4m3 operands (format 0, both
+// K-major): the fields sit at the same bits.
+__host__ __device__ constexpr uint32_t idesc_f16_f32acc_majors(bool bf16, bool a_mn, bool b_mn,
+                                                               int m, int n) {
+    return idesc_f16_f32acc(bf16, b_mn, m, n) | ((a_mn ? 1u : 0u) << 15);
+}
+
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32acc(int m, int n) {
+    return idesc_f16_f32acc(false, false, m, n);
+}
+
 // ---- tcgen05 MMA -----------------------------------------------------------
 
 // D[tmem] (+)= A[smem] x B[smem], kind::f16.  accumulate == 0 overwrites D.
@@ -303,6 +327,24 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
             "{\n\t.reg .pred p;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// The same with 8-bit operands (kind::f8f6f4, K = 32 elements).
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
@@ -362,6 +404,19 @@ __device__ __forceinline__ void tmem_ld_32cols(uint32_t taddr, uint32_t (&r)[32]
           "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
           "=r"(r[31])
+        : "r"(taddr));
+}
+
+// The same for 16 columns, into r[first .. first + 15].
+template <int N>
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[N], int first) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[first]), "=r"(r[first + 1]), "=r"(r[first + 2]), "=r"(r[first + 3]),
+          "=r"(r[first + 4]), "=r"(r[first + 5]), "=r"(r[first + 6]), "=r"(r[first + 7]),
+          "=r"(r[first + 8]), "=r"(r[first + 9]), "=r"(r[first + 10]), "=r"(r[first + 11]),
+          "=r"(r[first + 12]), "=r"(r[first + 13]), "=r"(r[first + 14]), "=r"(r[first + 15])
         : "r"(taddr));
 }
 
