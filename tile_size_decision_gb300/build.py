@@ -48,7 +48,8 @@ def units():
         ("host_pipeline.cu", "host_pipeline.o", []),
         ("norm_sm103a.cu", "norm_sm103a.o", []),
         ("stream_sm103a.cu", "stream_sm103a.o", []),
-        ("wgrad_sm103a.cu", "wgrad_sm103a.o", []),
+        ("pair_sm103a.cu", "pair_sm103a.o", []),
+        ("pair8_sm103a.cu", "pair8_sm103a.o", []),
         ("product_api.cu", "product_api.o", []),
     ]
     for bn, cg in GEMM_VARIANTS:

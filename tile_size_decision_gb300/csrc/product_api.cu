@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "product_sm103a.cuh"
@@ -83,6 +84,21 @@ int check_product(const tiles_product_desc* d, bool grouped) {
     return TILES_OK;
 }
 
+// CTA pairs resident at once, asked of the runtime once per device.
+int resident_pairs(int sms, int* pairs) {
+    static std::atomic<int> known[64];
+    int d = 0;
+    const cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return fail(TILES_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    int n = d < 64 ? known[d].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        n = pair_max_groups(sms);
+        if (d < 64) known[d].store(n, std::memory_order_relaxed);
+    }
+    *pairs = n;
+    return TILES_OK;
+}
+
 int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_bytes, void* stream) {
     int s = check_product(d, grouped);
     if (s != TILES_OK) return s;
@@ -117,11 +133,51 @@ int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_b
     args.drop_stage = planted.stage;
     if (planted.stage >= 0) args.wait_limit_ns = planted.limit_ns;
 
-    // Rows a tile: what an average group has, up to 128.
     const int64_t mean = (d->m + groups - 1) / groups;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    CUtensorMap tw, ta;
+    const int64_t stride_b = groups > 1 ? d->stride_b : d->ldb;
+    args.k_blocks = static_cast<int32_t>((d->k + bk - 1) / bk);
+    // More rows a group than the few-rows kernel's largest tile: CTA pairs.
+    const bool use_pair = mean > 128;
+    const bool kn = kind == kWeight16KN;
+    if (use_pair) {
+        int pairs = 0;
+        if ((s = resident_pairs(sms, &pairs)) != TILES_OK) return s;
+        args.tile_cols = 256;
+        if (fp8 && !grouped) {
+            // The width whose units fill the rounds of the pairs best: a
+            // K block of a unit takes 2 clocks per column of MMA, or the time
+            // to fill 128 rows and half the columns at 64 B/clk.
+            int64_t best = INT64_MAX;
+            for (int nt = 256; nt >= 32; nt -= 32) {
+                const int64_t units = (d->n + nt - 1) / nt * ((d->m + 255) / 256);
+                const int64_t cost = (units + pairs - 1) / pairs * std::max(2 * nt, 256 + nt);
+                if (cost < best) { best = cost; args.tile_cols = nt; }
+            }
+        }
+        args.n_blocks = static_cast<int32_t>((d->n + args.tile_cols - 1) / args.tile_cols);
+        const int64_t row_tiles = grouped ? d->m / 256 + std::min(groups, d->m) : (d->m + 255) / 256;
+        const int64_t units = row_tiles * args.n_blocks;
+        if (units > INT32_MAX / 2) return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
+        args.idesc = fp8 ? ptx::idesc_e4m3_f32acc(256, 0)
+                         : ptx::idesc_f16_f32acc_majors(d->in_dtype == TILES_BF16, kn, false, 256, 0);
+        s = encode_box(&tw, map_type(d->in_dtype), d->b, kn ? d->n : d->k, kn ? d->k : d->n, groups,
+                       d->ldb * eb, stride_b * eb, kn ? 64 : bk, kn ? 64 : fp8 ? 32 : 128);
+        if (s != TILES_OK) return s;
+        s = encode_box(&ta, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
+                       fp8 ? 128 : 32);
+        if (s != TILES_OK) return s;
+        return launch_status(fp8 ? launch_pair8(tw, ta, args, static_cast<int>(units), st)
+                                 : launch_pair(kind, tw, ta, args, static_cast<int>(units), st),
+                             grouped ? "grouped product" : "8-bit product");
+    }
+    s = encode_box(&tw, map_type(d->in_dtype), d->b, kn ? d->n : d->k, kn ? d->k : d->n, groups,
+                   d->ldb * eb, stride_b * eb, kn ? 64 : bk, kn ? 64 : 128);
+    if (s != TILES_OK) return s;
+    // Rows a tile: what an average group has, up to 128.
     const int tile_rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
     args.n_blocks = static_cast<int32_t>((d->n + 127) / 128);
-    args.k_blocks = static_cast<int32_t>((d->k + bk - 1) / bk);
     // Row tiles: exact when dense; grouped, every group may end inside one.
     const int64_t row_tiles = grouped ? d->m / tile_rows + std::min(groups, d->m)
                                       : (d->m + tile_rows - 1) / tile_rows;
@@ -133,22 +189,12 @@ int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_b
         args.split *= 2;
     if (units * args.split > INT32_MAX) return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
     args.idesc = fp8 ? ptx::idesc_e4m3_f32acc(128, tile_rows)
-                     : ptx::idesc_f16_f32acc_majors(d->in_dtype == TILES_BF16, kind == kWeight16KN,
-                                                    false, 128, tile_rows);
-    CUtensorMap tw, ta;
-    const int64_t sb = groups > 1 ? d->stride_b : (kind == kWeight16KN ? d->k : d->n) * d->ldb;
-    if (kind == kWeight16KN)
-        s = encode_box(&tw, map_type(d->in_dtype), d->b, d->n, d->k, groups, d->ldb * eb, sb * eb,
-                       64, 64);
-    else
-        s = encode_box(&tw, map_type(d->in_dtype), d->b, d->k, d->n, groups, d->ldb * eb, sb * eb,
-                       bk, 128);
-    if (s != TILES_OK) return s;
+                     : ptx::idesc_f16_f32acc_majors(d->in_dtype == TILES_BF16, kn, false, 128,
+                                                    tile_rows);
     s = encode_box(&ta, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
                    tile_rows);
     if (s != TILES_OK) return s;
-    return launch_status(launch_stream(kind, tile_rows, tw, ta, args, units,
-                                       static_cast<cudaStream_t>(stream)),
+    return launch_status(launch_stream(kind, tile_rows, tw, ta, args, units, st),
                          grouped ? "grouped product" : "8-bit product");
 }
 
@@ -192,17 +238,23 @@ int tiles_grouped_wgrad(const tiles_wgrad_desc* d, void* ws, size_t ws_bytes, vo
     if (d->groups * ((d->k + 127) / 128) > INT32_MAX / ((d->n + 127) / 128))
         return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
     if ((s = check_workspace(ws, ws_bytes)) != TILES_OK) return s;
-    WgradArgs args{};
+    int sms = 0, pairs = 0;
+    if ((s = current_sm_count(&sms)) != TILES_OK) return s;
+    if ((s = resident_pairs(sms, &pairs)) != TILES_OK) return s;
+    // The tile of the products with other names: dc is the weight side, the
+    // columns of a are the rows, and the group's rows the contraction.
+    ProductArgs args{};
     args.m = static_cast<int32_t>(d->m);
-    args.k = static_cast<int32_t>(d->k);
     args.n = static_cast<int32_t>(d->n);
+    args.k = static_cast<int32_t>(d->k);
     args.groups = static_cast<int32_t>(d->groups);
     args.offsets = d->offsets;
-    args.dw = d->dw;
-    args.lddw = d->lddw;
-    args.stride_dw = d->stride_dw;
-    args.out_dtype = d->out_dtype;
-    args.idesc = ptx::idesc_f16_f32acc(d->in_dtype == TILES_BF16, false, 0, 0);
+    args.n_blocks = static_cast<int32_t>((d->n + 255) / 256);
+    args.c = d->dw;
+    args.ldc = d->lddw;
+    args.stride_c = d->stride_dw;
+    args.c_dtype = d->out_dtype;
+    args.idesc = ptx::idesc_f16_f32acc_majors(d->in_dtype == TILES_BF16, true, true, 256, 0);
     args.err = static_cast<int32_t*>(ws);
     args.wait_limit_ns = kWaitLimitNs;
     const PlantedFault planted = take_planted_fault();
@@ -212,14 +264,16 @@ int tiles_grouped_wgrad(const tiles_wgrad_desc* d, void* ws, size_t ws_bytes, vo
     // only have to be valid.
     const bool none = d->m == 0;
     alignas(16) static const char nothing[16] = {};
-    CUtensorMap ta, tb;
+    CUtensorMap tw, ta;
+    s = encode_box(&tw, map_type(d->in_dtype), none ? nothing : d->dc, d->n, none ? 1 : d->m, 1,
+                   d->lddc * 2, d->lddc * 2, 64, 64);
+    if (s != TILES_OK) return s;
     s = encode_box(&ta, map_type(d->in_dtype), none ? nothing : d->a, d->k, none ? 1 : d->m, 1,
                    d->lda * 2, d->lda * 2, 64, 64);
     if (s != TILES_OK) return s;
-    s = encode_box(&tb, map_type(d->in_dtype), none ? nothing : d->dc, d->n, none ? 1 : d->m, 1,
-                   d->lddc * 2, d->lddc * 2, 64, 64);
-    if (s != TILES_OK) return s;
-    return launch_status(launch_wgrad(ta, tb, args, static_cast<cudaStream_t>(stream)),
+    const int64_t units = d->groups * ((d->k + 255) / 256) * args.n_blocks;
+    return launch_status(launch_pair(kWeightGrad, tw, ta, args, static_cast<int>(units),
+                                     static_cast<cudaStream_t>(stream)),
                          "grouped weight gradient");
 }
 

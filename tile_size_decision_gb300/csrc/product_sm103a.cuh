@@ -18,13 +18,16 @@ constexpr int kMaxGroups = 4096;
 constexpr int kWeight16KN = 0;        // 16-bit, b is k x n (MN-major weight)
 constexpr int kWeight16NK = 1;        // 16-bit, b is n x k (K-major weight)
 constexpr int kWeight8NK = 2;         // e4m3, b is n x k, block scales
+constexpr int kWeightGrad = 3;        // 16-bit weight gradient (the large-tile kernel's form)
 
 struct ProductArgs {
     int32_t m, n, k;
     int32_t groups;                   // 0: dense
     const int32_t* offsets;
     int32_t n_blocks, k_blocks;       // of the kernel's tile
-    int32_t split;                    // CTAs along K (a cluster)
+    int32_t split;                    // few rows: CTAs along K (a cluster)
+    int32_t tile_cols;                // 8-bit pairs: weight rows a tile, a multiple of 32
+    int64_t stride_c;                 // weight gradient: elements between groups' results
     void* c;
     int64_t ldc;
     int32_t c_dtype;
@@ -76,6 +79,43 @@ __device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int groups
     return false;
 }
 
+// The same lookup for increasing `want`: a warp keeps the 32 groups it is at
+// in registers, so that a step costs a vote and shuffles.
+struct RowTileCursor {
+    int base = 0, g0 = -32;           // tiles before the chunk; its first group
+    int lo = 0, hi = 0, upto = 0, tiles = 0, total = 0;
+
+    __device__ __forceinline__ bool seek(const int32_t* offsets, int groups, int m, int tile_rows,
+                                         int want, RowTile* out) {
+        const int lane = threadIdx.x & 31;
+        while (want >= base + total) {
+            g0 += 32;
+            if (g0 >= groups) { g0 = groups; total = 0; return false; }
+            base += total;
+            const int g = g0 + lane;
+            lo = hi = 0;
+            if (g < groups) {
+                lo = clamp_offset(offsets[g], m);
+                hi = clamp_offset(offsets[g + 1], m);
+            }
+            tiles = hi > lo ? (hi - lo + tile_rows - 1) / tile_rows : 0;
+            upto = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += t;
+            }
+            total = __shfl_sync(0xffffffffu, upto, 31);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, want < base + upto)) - 1;
+        const int first = base + __shfl_sync(0xffffffffu, upto - tiles, src);
+        out->group = g0 + src;
+        out->row0 = __shfl_sync(0xffffffffu, lo, src) + (want - first) * tile_rows;
+        out->end = __shfl_sync(0xffffffffu, hi, src);
+        return true;
+    }
+};
+
 // One value in the output's type.
 __device__ __forceinline__ void store_one(void* c, int64_t at, float v, int dtype) {
     if (dtype == TILES_F32) static_cast<float*>(c)[at] = v;
@@ -88,20 +128,15 @@ __device__ __forceinline__ void store_one(void* c, int64_t at, float v, int dtyp
 int launch_stream(int kind, int tile_rows, const CUtensorMap& weight, const CUtensorMap& rows,
                   const ProductArgs& args, int64_t units, cudaStream_t st);
 
-struct WgradArgs {
-    int32_t m, k, n, groups;
-    const int32_t* offsets;
-    int32_t k_blocks, n_blocks;
-    void* dw;
-    int64_t lddw, stride_dw;
-    int32_t out_dtype;
-    uint32_t idesc;
-    int32_t* err;
-    uint64_t wait_limit_ns;
-    int32_t drop_stage;
-};
-
-int launch_wgrad(const CUtensorMap& a, const CUtensorMap& dc, const WgradArgs& args,
-                 cudaStream_t st);
+// The 16-bit kernel on CTA pairs: tiles of 256 weight columns by up to 256
+// rows (weight gradient: dc's columns by a's); units is an upper bound.
+int launch_pair(int kind, const CUtensorMap& weight, const CUtensorMap& rows,
+                const ProductArgs& args, int units, cudaStream_t st);
+// The 8-bit kernel on CTA pairs: tiles of 256 rows by args.tile_cols weight
+// rows; units is an upper bound.
+int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const ProductArgs& args,
+                 int units, cudaStream_t st);
+// CTA pairs resident at once on the current device.
+int pair_max_groups(int sms);
 
 }  // namespace tiles

@@ -95,7 +95,6 @@ __global__ void __launch_bounds__(kThreads)
         ptx::tmem_relinquish<1>();
     }
     ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
     if (warp == 2) {
         RowTile rt{0, row_tile * NT, args.m};
         bool found = true;
@@ -111,6 +110,9 @@ __global__ void __launch_bounds__(kThreads)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    // Only now: the next kernel's blocks must not take the tensor memory that
+    // this block still waits for.
+    ptx::grid_launch_dependents();
 
     const uint32_t tmem = bar->tmem_base;
     const int group = bar->group, row0 = bar->row0, end = bar->end;
