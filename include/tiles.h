@@ -635,8 +635,9 @@ typedef struct {
     int32_t pad0;
 } tiles_rmsnorm_grad_desc;
 
-/* Workspace bytes of the gradient: the partial weight gradients of the
- * blocks that sweep the rows (0 on invalid arguments). */
+/* Workspace bytes of the gradient: the 256-byte header that every workspace
+ * has (this call leaves it alone) and the partial weight gradients of the
+ * blocks that sweep the rows (0 on invalid arguments).  16-byte aligned. */
 size_t tiles_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols);
 
 int tiles_rmsnorm_grad(const tiles_rmsnorm_grad_desc* desc, void* workspace, size_t ws_bytes,

@@ -515,6 +515,10 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
 
 
 # ---- norms, 8-bit products and products grouped by expert ------------------------
+#
+# These calls are short (a decoding step's norm takes a few microseconds on
+# the GPU), so the binding checks what the caller passes and nothing that it
+# allocates itself.
 
 
 SCALE_BLOCK = 128     # columns (and weight rows) that share one scale
@@ -528,19 +532,20 @@ def _rows2(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    return ld if rows > 1 else (cols + 15) // 16 * 16
 
 
 def _vector(t, n, name):
-    if not t.is_cuda or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if not t.is_cuda or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous CUDA vector of {n} elements")
     return t.data_ptr()
 
 
 def _like(t, x, name):
-    """Row pitch of a matrix of x's shape and type (x itself gives both)."""
+    """Row pitch of a matrix of x's shape and type."""
     if t.shape != x.shape:
         raise ValueError(f"{name} must have the shape {tuple(x.shape)}, not {tuple(t.shape)}")
     if t.dtype != x.dtype:
@@ -552,34 +557,29 @@ def _blocks(n):
     return (n + SCALE_BLOCK - 1) // SCALE_BLOCK
 
 
+def _scale_strides(s, shape, name):
+    if s.shape != shape or s.dtype != _torch().float32 or not s.is_cuda:
+        raise ValueError(f"{name} must be a float32 CUDA tensor of shape {shape}")
+    return s.stride()
+
+
 def _empty_fp8(torch, lead, cols, device):
     """e4m3 rows whose pitch is whole 16-byte pieces, as the products need."""
+    if cols % 16 == 0:
+        return torch.empty((*lead, cols), dtype=torch.float8_e4m3fn, device=device)
     pitch = (cols + 15) // 16 * 16
-    q = torch.empty((*lead, pitch), dtype=torch.float8_e4m3fn, device=device)
-    return q if pitch == cols else q[..., :cols]
+    return torch.empty((*lead, pitch), dtype=torch.float8_e4m3fn, device=device)[..., :cols]
 
 
-def _rmsnorm(x, weight, residual, eps, y, scales, h, out_code, stream):
-    rows, cols = x.shape
-    ldx = _rows2(x, "x")
-    code = _dtype_code(x)
-    ldr = _like(residual, x, "residual") if residual is not None else 0
-    ldh = _like(h, x, "h_out") if h is not None else 0
-    wptr = _vector(weight, cols, "weight")
-    sr = sb = 0
-    if scales is not None:
-        if scales.shape != (rows, _blocks(cols)) or scales.dtype != _torch().float32 or \
-                not scales.is_cuda:
-            raise ValueError(f"scales must be a float32 CUDA tensor of shape "
-                             f"{(rows, _blocks(cols))}")
-        sr, sb = scales.stride()
-    d = _abi.RmsnormDesc(rows, cols, x.data_ptr(),
-                         residual.data_ptr() if residual is not None else None, wptr,
-                         h.data_ptr() if h is not None else None, y.data_ptr(),
-                         scales.data_ptr() if scales is not None else None, ldx, ldr, ldh,
-                         _rows2(y, "out"), sr, sb, eps, code, _dtype_code(weight),
-                         code if out_code is None else out_code)
-    _check(load().tiles_rmsnorm(C.byref(d), _stream_handle(stream)), "tiles_rmsnorm")
+def _residual_args(torch, x, residual, h_out):
+    """(h, pointers and pitches of the residual and of h)."""
+    if residual is None:
+        return x, None, 0, None, 0
+    ldr = _like(residual, x, "residual")
+    if h_out is None:
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return h, residual.data_ptr(), ldr, h.data_ptr(), x.shape[1]
+    return h_out, residual.data_ptr(), ldr, h_out.data_ptr(), _like(h_out, x, "h_out")
 
 
 def rmsnorm(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=None):
@@ -587,15 +587,19 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=Non
     row of a matrix; returns (y, h) in x's type.  Without a residual h is x
     itself.  h_out may be the residual (updated in place)."""
     torch = _torch()
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    if out is not None:
-        _like(out, x, "out")
-    if residual is None:
-        h = x
+    ldx = _rows2(x, "x")
+    rows, cols = x.shape
+    code = _dtype_code(x)
+    if out is None:
+        out, ldy = torch.empty(x.shape, dtype=x.dtype, device=x.device), cols
     else:
-        h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if h_out is None else h_out
-    _rmsnorm(x, weight, residual, eps, y, None, None if residual is None else h, None, stream)
-    return y, h
+        ldy = _like(out, x, "out")
+    h, pr, ldr, ph, ldh = _residual_args(torch, x, residual, h_out)
+    d = _abi.RmsnormDesc(rows, cols, x.data_ptr(), pr, _vector(weight, cols, "weight"), ph,
+                         out.data_ptr(), None, ldx, ldr, ldh, ldy, 0, 0, eps, code,
+                         _dtype_code(weight), code)
+    _check(load().tiles_rmsnorm(C.byref(d), _stream_handle(stream)), "tiles_rmsnorm")
+    return out, h
 
 
 def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out=None,
@@ -605,29 +609,38 @@ def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out
     scales are stored block by block (a transposed view, rows x blocks),
     which the products read fastest."""
     torch = _torch()
+    ldx = _rows2(x, "x")
     rows, cols = x.shape
-    q = _empty_fp8(torch, (rows,), cols, x.device) if out is None else out
-    if q.shape != x.shape or q.dtype != torch.float8_e4m3fn:
-        raise ValueError("out must be float8_e4m3fn of x's shape")
-    if scales is None:
-        scales = torch.empty((_blocks(cols), rows), dtype=torch.float32, device=x.device).t()
-    if residual is None:
-        h = x
+    nb = (cols + SCALE_BLOCK - 1) // SCALE_BLOCK
+    if out is None:
+        out = _empty_fp8(torch, (rows,), cols, x.device)
+        ldy = (cols + 15) // 16 * 16
     else:
-        h = torch.empty(x.shape, dtype=x.dtype, device=x.device) if h_out is None else h_out
-    _rmsnorm(x, weight, residual, eps, q, scales, None if residual is None else h, _abi.E4M3,
-             stream)
-    return q, scales, h
+        if out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
+            raise ValueError("out must be float8_e4m3fn of x's shape")
+        ldy = _rows2(out, "out")
+    if scales is None:
+        scales = torch.empty_strided((rows, nb), (1, max(rows, 1)), dtype=torch.float32,
+                                     device=x.device)
+        sr, sb = 1, rows
+    else:
+        sr, sb = _scale_strides(scales, (rows, nb), "scales")
+    h, pr, ldr, ph, ldh = _residual_args(torch, x, residual, h_out)
+    d = _abi.RmsnormDesc(rows, cols, x.data_ptr(), pr, _vector(weight, cols, "weight"), ph,
+                         out.data_ptr(), scales.data_ptr(), ldx, ldr, ldh, ldy, sr, sb, eps,
+                         _dtype_code(x), _dtype_code(weight), _abi.E4M3)
+    _check(load().tiles_rmsnorm(C.byref(d), _stream_handle(stream)), "tiles_rmsnorm")
+    return out, scales, h
 
 
 def rmsnorm_grad_workspace(x):
-    """A workspace for rmsnorm_grad on matrices of x's shape."""
+    """A zeroed workspace for rmsnorm_grad on matrices of x's shape."""
     torch = _torch()
     rows, cols = x.shape
     n = int(load().tiles_rmsnorm_grad_workspace_bytes(rows, cols))
     if n == 0:
         raise TilesError(_abi.ERR_INVALID_ARG, "tiles_rmsnorm_grad_workspace_bytes")
-    return torch.empty(n, dtype=torch.uint8, device=x.device)
+    return torch.zeros(n, dtype=torch.uint8, device=x.device)
 
 
 def rmsnorm_grad(dy, h, weight, eps=1e-6, dh=None, dx_out=None, dweight_out=None, workspace=None,
@@ -636,24 +649,27 @@ def rmsnorm_grad(dy, h, weight, eps=1e-6, dh=None, dx_out=None, dweight_out=None
     past the norm, of h (dh): returns (dx, dweight).  dx, in h's type, is the
     gradient of x and of the residual alike; dweight is fp32."""
     torch = _torch()
-    rows, cols = h.shape
     ldh = _rows2(h, "h")
+    rows, cols = h.shape
     lddy = _like(dy, h, "dy")
     lddh = _like(dh, h, "dh") if dh is not None else 0
-    dx = torch.empty(h.shape, dtype=h.dtype, device=h.device) if dx_out is None else dx_out
-    dw = torch.empty(cols, dtype=torch.float32, device=h.device) if dweight_out is None \
-        else dweight_out
-    if dw.dtype != torch.float32:
+    if dx_out is None:
+        dx_out, lddx = torch.empty(h.shape, dtype=h.dtype, device=h.device), cols
+    else:
+        lddx = _like(dx_out, h, "dx_out")
+    if dweight_out is None:
+        dweight_out = torch.empty(cols, dtype=torch.float32, device=h.device)
+    elif dweight_out.dtype != torch.float32:
         raise TypeError("dweight_out must be float32")
     d = _abi.RmsnormGradDesc(rows, cols, dy.data_ptr(), h.data_ptr(),
                              _vector(weight, cols, "weight"),
-                             dh.data_ptr() if dh is not None else None, dx.data_ptr(),
-                             _vector(dw, cols, "dweight_out"), lddy, ldh, lddh,
-                             _like(dx, h, "dx_out"), eps, _dtype_code(h), _dtype_code(weight), 0)
+                             dh.data_ptr() if dh is not None else None, dx_out.data_ptr(),
+                             _vector(dweight_out, cols, "dweight_out"), lddy, ldh, lddh, lddx, eps,
+                             _dtype_code(h), _dtype_code(weight), 0)
     ws, wsb = _workspace_args(workspace)
     _check(load().tiles_rmsnorm_grad(C.byref(d), ws, wsb, _stream_handle(stream)),
            "tiles_rmsnorm_grad")
-    return dx, dw
+    return dx_out, dweight_out
 
 
 def _workspace_args(workspace):
@@ -693,59 +709,60 @@ def quantize_fp8(x, block_rows=1, stream=None):
 
 
 def _out_rows(out, rows, cols, out_dtype, like):
+    """The output matrix (new, or the caller's, checked) and its row pitch."""
     if out is None:
-        return _alloc_out((rows, cols), like, out_dtype)
+        return _alloc_out((rows, cols), like, out_dtype), cols
     if out.shape != (rows, cols):
         raise ValueError(f"out must have the shape {(rows, cols)}")
-    return out
+    return out, _rows2(out, "out")
 
 
-def _weight(b, groups, name="b"):
+def _weight(b, grouped, name="b"):
     """Row pitch and group stride of a weight (grouped: 3-D)."""
-    if b.dim() != (3 if groups else 2):
-        raise ValueError(f"{name} must have {3 if groups else 2} dimensions")
-    if not b.is_cuda or (b.shape[-1] > 1 and b.stride(-1) != 1):
+    if b.dim() != (3 if grouped else 2):
+        raise ValueError(f"{name} must have {3 if grouped else 2} dimensions")
+    st, shape = b.stride(), b.shape
+    if not b.is_cuda or (st[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be a CUDA tensor with unit stride in its last dimension")
-    ld = b.stride(-2) if b.shape[-2] > 1 else (b.shape[-1] + 15) // 16 * 16
-    return ld, b.stride(0) if groups else 0
+    ld = st[-2] if shape[-2] > 1 else (shape[-1] + 15) // 16 * 16
+    return ld, st[0] if grouped else 0
 
 
 def _offsets(offsets, groups):
-    torch = _torch()
-    if offsets.dtype != torch.int32 or not offsets.is_cuda or offsets.shape != (groups + 1,) or \
-            offsets.stride(0) != 1:
+    if offsets.dtype != _torch().int32 or not offsets.is_cuda or \
+            offsets.shape != (groups + 1,) or offsets.stride(0) != 1:
         raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {groups + 1} elements")
     return offsets.data_ptr()
 
 
 def _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype, workspace, stream, where):
-    torch = _torch()
+    fp8 = _torch().float8_e4m3fn
     grouped = offsets is not None
     lda = _rows2(a, "a")
     ldb, stride_b = _weight(b, grouped)
     m, k = a.shape
     n = b.shape[-2]
-    if a.dtype != torch.float8_e4m3fn or b.dtype != torch.float8_e4m3fn:
+    if a.dtype != fp8 or b.dtype != fp8:
         raise TypeError("a and b must be float8_e4m3fn")
     if b.shape[-1] != k:
         raise ValueError(f"shape mismatch: {tuple(a.shape)} x {tuple(b.shape)}^T")
-    groups = b.shape[0] if grouped else 0
-    kb = _blocks(k)
-    want = (groups, _blocks(n), kb) if grouped else (_blocks(n), kb)
-    for s, shape, name in ((a_scales, (m, kb), "a_scales"), (b_scales, want, "b_scales")):
-        if s.shape != shape or s.dtype != torch.float32 or not s.is_cuda:
-            raise ValueError(f"{name} must be a float32 CUDA tensor of shape {shape}")
+    kb, nb = _blocks(k), _blocks(n)
+    sar, sab = _scale_strides(a_scales, (m, kb), "a_scales")
+    if grouped:
+        groups = b.shape[0]
+        sbg, sbr, sbb = _scale_strides(b_scales, (groups, nb, kb), "b_scales")
+        off, fn = _offsets(offsets, groups), load().tiles_grouped_gemm
+    else:
+        groups = sbg = 0
+        sbr, sbb = _scale_strides(b_scales, (nb, kb), "b_scales")
+        off, fn = None, load().tiles_gemm_fp8
     if out is None and out_dtype is None:
         out_dtype = "bf16"
-    out = _out_rows(out, m, n, out_dtype, a)
-    sbs = b_scales.stride()
-    d = _abi.ProductDesc(m, n, k, groups, _offsets(offsets, groups) if grouped else None,
-                         a.data_ptr(), b.data_ptr(), out.data_ptr(), a_scales.data_ptr(),
-                         b_scales.data_ptr(), lda, ldb, _rows2(out, "out"), stride_b,
-                         a_scales.stride(0), a_scales.stride(1), sbs[-2], sbs[-1],
-                         sbs[0] if grouped else 0, _abi.E4M3, _dtype_code(out), _abi.B_NK, 0)
+    out, ldc = _out_rows(out, m, n, out_dtype, a)
+    d = _abi.ProductDesc(m, n, k, groups, off, a.data_ptr(), b.data_ptr(), out.data_ptr(),
+                         a_scales.data_ptr(), b_scales.data_ptr(), lda, ldb, ldc, stride_b, sar,
+                         sab, sbr, sbb, sbg, _abi.E4M3, _dtype_code(out), _abi.B_NK, 0)
     ws, wsb = _workspace_args(workspace)
-    fn = load().tiles_grouped_gemm if grouped else load().tiles_gemm_fp8
     _check(fn(C.byref(d), ws, wsb, _stream_handle(stream)), where)
     return out
 
@@ -785,11 +802,10 @@ def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspa
                          f"{'^T' if trans_b else ''}")
     if b.dtype != a.dtype:
         raise TypeError("a and b must share a dtype")
-    out = _out_rows(out, m, n, out_dtype, a)
+    out, ldc = _out_rows(out, m, n, out_dtype, a)
     d = _abi.ProductDesc(m, n, k, groups, _offsets(offsets, groups), a.data_ptr(), b.data_ptr(),
-                         out.data_ptr(), None, None, lda, ldb, _rows2(out, "out"), stride_b, 0, 0,
-                         0, 0, 0, _dtype_code(a), _dtype_code(out),
-                         _abi.B_NK if trans_b else _abi.B_KN, 0)
+                         out.data_ptr(), None, None, lda, ldb, ldc, stride_b, 0, 0, 0, 0, 0,
+                         _dtype_code(a), _dtype_code(out), _abi.B_NK if trans_b else _abi.B_KN, 0)
     ws, wsb = _workspace_args(workspace)
     _check(load().tiles_grouped_gemm(C.byref(d), ws, wsb, _stream_handle(stream)),
            "tiles_grouped_gemm")
@@ -800,7 +816,6 @@ def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stre
     """out[g] = a_g^T @ dc_g over the rows of group g: the weight gradients
     (groups x k x n) of out = grouped_gemm(a, w, offsets), given dc.  An
     empty group's gradient is zero."""
-    torch = _torch()
     lda, lddc = _rows2(a, "a"), _rows2(dc, "dc")
     m, k = a.shape
     n = dc.shape[1]
@@ -810,10 +825,11 @@ def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stre
         raise TypeError("a and dc must share a dtype")
     groups = offsets.shape[0] - 1
     if out is None:
-        out = _alloc_out((groups, k, n), a, out_dtype)
-    if out.shape != (groups, k, n):
-        raise ValueError(f"out must have the shape {(groups, k, n)}")
-    ldw, stride_dw = _weight(out, True, "out")
+        out, ldw, stride_dw = _alloc_out((groups, k, n), a, out_dtype), n, k * n
+    else:
+        if out.shape != (groups, k, n):
+            raise ValueError(f"out must have the shape {(groups, k, n)}")
+        ldw, stride_dw = _weight(out, True, "out")
     d = _abi.WgradDesc(m, k, n, groups, _offsets(offsets, groups), a.data_ptr(), dc.data_ptr(),
                        out.data_ptr(), lda, lddc, ldw, stride_dw, _dtype_code(a), _dtype_code(out))
     ws, wsb = _workspace_args(workspace)

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "tiles_internal.h"
@@ -23,6 +24,21 @@ inline int launch_status(int e, const char* what) {
     if (e == cudaSuccess) return TILES_OK;
     return fail(TILES_ERR_CUDA, "%s launch failed: %s", what,
                 cudaGetErrorString(static_cast<cudaError_t>(e)));
+}
+
+// Opts `kernel` into `bytes` of dynamic shared memory on the current device;
+// remembered per device in the caller's `done` (one flag word per kernel), so
+// that repeated launches ask the runtime nothing.
+template <typename K>
+cudaError_t opt_in_smem(K* kernel, int bytes, std::atomic<uint64_t>* done) {
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = d < 64 ? uint64_t(1) << d : 0;
+    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // A launch with programmatic serialization (the kernel waits for its

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "launch_util.h"
 #include "sm103_ptx.cuh"
@@ -159,6 +160,48 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* slot, int turn) {
     }
 }
 
+// ---- rows on their way in ----------------------------------------------------
+//
+// Rows whose pieces are 16-byte aligned come in through asynchronous copies,
+// kRing rows deep.  A thread copies exactly the pieces it will read (its
+// 8-element vectors of N matrices), so its own copy groups order them: no
+// barrier, and no registers held by loads in flight.
+constexpr int kRing = 3;
+
+template <typename T, int N, int VPT>
+struct RowRing {
+    static constexpr int PIECES = static_cast<int>(sizeof(T)) / 2;   // 16-byte pieces of a vector
+    static constexpr int STAGE = N * VPT * PIECES;                   // pieces per thread and row
+    uint4* at;                                                       // + piece * threads
+
+    static size_t bytes(int threads) {
+        return static_cast<size_t>(kRing) * STAGE * threads * 16;
+    }
+    // Start the copies of matrix n's vectors for ring slot `slot`.
+    __device__ __forceinline__ void copy(int slot, int n, const T* row, int step, int tid,
+                                         int threads, int cols) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = j * step + tid * 8;
+            if (c < cols)
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p)
+                    ptx::cp_async_16(at + ((slot * N + n) * VPT * PIECES + j * PIECES + p) * threads,
+                                     reinterpret_cast<const uint4*>(row + c) + p);
+        }
+    }
+    __device__ __forceinline__ void read(int slot, int n, int j, bool in, int threads,
+                                         float (&v)[8]) const {
+        union { uint4 q[PIECES]; T e[8]; } u;
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p)
+            u.q[p] = in ? at[((slot * N + n) * VPT * PIECES + j * PIECES + p) * threads]
+                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_float(u.e[i]);
+    }
+};
+
 struct NormArgs {
     int64_t rows, cols;
     const void* x;
@@ -247,6 +290,74 @@ __global__ void __launch_bounds__(kMaxThreads)
             if (h) store8<T, VEC>(h, c0 + threadIdx.x * 8, a.cols, v);
             emit(c0 + threadIdx.x * 8, v, rstd);
         }
+    }
+}
+
+// The same with the rows' pieces 16-byte aligned: the block takes rows
+// blockIdx.x, + gridDim.x, ... (times blockDim.y), the next two of them on
+// their way in while one is worked on.
+template <typename T, int VPT, bool FP8>
+__global__ void __launch_bounds__(kMaxThreads)
+    rmsnorm_ring_kernel(const NormArgs a) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float slots[64];
+    const int threads = blockDim.x * blockDim.y;
+    RowRing<T, 2, VPT> ring{ring_smem + threadIdx.y * blockDim.x + threadIdx.x};
+    const int step = blockDim.x * 8, tid = threadIdx.x, cols = static_cast<int>(a.cols);
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < a.rows) {
+            ring.copy(slot, 0, static_cast<const T*>(a.x) + row * a.ldx, step, tid, threads, cols);
+            if (a.residual)
+                ring.copy(slot, 1, static_cast<const T*>(a.residual) + row * a.ldr, step, tid, threads,
+                          cols);
+        }
+        ptx::cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(row0 + i * stride, i);
+    int slot = 0, turn = 0;
+    for (int64_t row = row0; row < a.rows; row += stride, turn ^= 1) {
+        const int refill = slot == 0 ? kRing - 1 : slot - 1;
+        fetch(row + (kRing - 1) * stride, refill);
+        ptx::cp_async_wait_groups<kRing - 1>();
+        float v[VPT][8], sum[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = j * step + tid * 8;
+            ring.read(slot, 0, j, c < cols, threads, v[j]);
+            if (a.residual) {
+                float q[8];
+                ring.read(slot, 1, j, c < cols, threads, q);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] += q[i];
+            }
+            if (a.h) store8<T, true>(static_cast<T*>(a.h) + row * a.ldh, c, cols, v[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[0] += v[j][i] * v[j][i];
+        }
+        row_sum(sum, slots, turn);
+        const float rstd = rsqrtf(sum[0] / static_cast<float>(cols) + a.eps);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = j * step + tid * 8;
+            float w[8], y[8];
+            load8_any<true>(a.weight, a.weight_dtype, c, cols, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = c < cols ? v[j][i] * rstd * w[i] : 0.0f;
+            if constexpr (FP8) {
+                const float s = block_scale(block_amax(y));
+                store8_e4m3<true>(static_cast<uint8_t*>(a.y) + row * a.ldy, c, cols, y, 1.0f / s);
+                if ((tid & 15) == 0 && c < cols)
+                    a.scales[row * a.scale_row + c / kBlock * a.scale_block] = s;
+            } else {
+                store8<T, true>(static_cast<T*>(a.y) + row * a.ldy, c, cols, y);
+            }
+        }
+        if (++slot == kRing) slot = 0;
     }
 }
 
@@ -372,6 +483,110 @@ __global__ void __launch_bounds__(512)
     }
 }
 
+// The same with the rows' pieces 16-byte aligned and the whole row in one
+// block (gridDim.y == 1), the next two rows on their way in.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(512)
+    rmsnorm_grad_ring_kernel(const GradArgs a) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float slots[128];
+    __shared__ float side[7][VPT * 256];           // blockDim.y > 1: the other warps' parts
+    const int threads = blockDim.x * blockDim.y;
+    RowRing<T, 3, VPT> ring{ring_smem + threadIdx.y * blockDim.x + threadIdx.x};
+    const int step = blockDim.x * 8, tid = threadIdx.x, cols = static_cast<int>(a.cols);
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < a.rows) {
+            ring.copy(slot, 0, static_cast<const T*>(a.dy) + row * a.lddy, step, tid, threads, cols);
+            ring.copy(slot, 1, static_cast<const T*>(a.h) + row * a.ldh, step, tid, threads, cols);
+            if (a.dh)
+                ring.copy(slot, 2, static_cast<const T*>(a.dh) + row * a.lddh, step, tid, threads, cols);
+        }
+        ptx::cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(row0 + i * stride, i);
+    float dw[VPT][8], w[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        load8_any<true>(a.weight, a.weight_dtype, j * step + tid * 8, cols, w[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
+    }
+    const float inv_n = 1.0f / static_cast<float>(cols);
+    int slot = 0, turn = 0;
+    for (int64_t row = row0; row < a.rows; row += stride, turn ^= 1) {
+        const int refill = slot == 0 ? kRing - 1 : slot - 1;
+        fetch(row + (kRing - 1) * stride, refill);
+        ptx::cp_async_wait_groups<kRing - 1>();
+        float s[2] = {0.0f, 0.0f};                 // sum h^2, sum dy w h
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float g[8], h[8];
+            const bool in = j * step + tid * 8 < cols;
+            ring.read(slot, 0, j, in, threads, g);
+            ring.read(slot, 1, j, in, threads, h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[0] += h[i] * h[i];
+                s[1] += g[i] * w[j][i] * h[i];
+            }
+        }
+        row_sum(s, slots, turn);
+        const float rstd = rsqrtf(s[0] * inv_n + a.eps);
+        const float back = s[1] * inv_n * rstd * rstd * rstd;
+        T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float g[8], h[8], o[8];
+            const int c = j * step + tid * 8;
+            ring.read(slot, 0, j, c < cols, threads, g);
+            ring.read(slot, 1, j, c < cols, threads, h);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g[i] *= rstd;
+                o[i] = g[i] * w[j][i] - h[i] * back;
+                dw[j][i] += g[i] * h[i];
+            }
+            if (a.dh) {
+                float q[8];
+                ring.read(slot, 2, j, c < cols, threads, q);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] += q[i];
+            }
+            store8<T, true>(dx, c, cols, o);
+        }
+        if (++slot == kRing) slot = 0;
+    }
+    if (blockDim.y > 1) {                          // then blockDim.x == 32: one warp a row
+        if (threadIdx.y > 0)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) side[threadIdx.y - 1][(j * 8 + i) * 32 + tid] = dw[j][i];
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+        for (int y = 0; y < static_cast<int>(blockDim.y) - 1; ++y)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dw[j][i] += side[y][(j * 8 + i) * 32 + tid];
+    }
+    float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = j * step + tid * 8;
+        if (c < cols)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+                *reinterpret_cast<float4*>(out + c + i) =
+                    make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
+    }
+}
+
 // dweight[c] = the sum of the partials of column c: 32 columns a block, 32
 // threads a column, each over every 32nd partial, added in a fixed order.
 __global__ void __launch_bounds__(1024) reduce_partials_kernel(const float* partials, int64_t cols,
@@ -468,6 +683,28 @@ bool element_aligned(const void* p, int elem_bytes) {
     return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(elem_bytes - 1)) == 0;
 }
 
+#ifndef NTH
+#define NTH 1536
+#endif
+constexpr int kRingBytesMost = 96 * 1024;            // two blocks an SM
+
+template <typename T, int VPT, bool FP8>
+int launch_norm_ring(const NormArgs& a, int sms, cudaStream_t st) {
+    const int64_t vectors = (a.cols + 7) / 8;
+    const int threads = static_cast<int>((vectors + 32 * VPT - 1) / (32 * VPT) * 32);
+    const int per_block = threads == 32 ? 8 : 1;
+    const size_t smem = RowRing<T, 2, VPT>::bytes(threads * per_block);
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(rmsnorm_ring_kernel<T, VPT, FP8>, kRingBytesMost, &opted);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    // As many blocks as an SM holds (threads and shared memory).
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(
+        NTH / (threads * per_block), 220 * 1024 / static_cast<int64_t>(smem + 1024)));
+    const int64_t need = (a.rows + per_block - 1) / per_block;
+    const dim3 grid(static_cast<unsigned>(std::min(need, sms * per_sm)));
+    return launch(rmsnorm_ring_kernel<T, VPT, FP8>, grid, dim3(threads, per_block), smem, st, a);
+}
+
 template <typename T, bool VEC, bool FP8>
 int launch_norm(const NormArgs& a, cudaStream_t st) {
     const int64_t vectors = (a.cols + 7) / 8;
@@ -491,12 +728,23 @@ int launch_norm(const NormArgs& a, cudaStream_t st) {
 }
 
 template <typename T>
-int launch_norm_any(const NormArgs& a, bool vec, bool fp8, cudaStream_t st) {
+int launch_norm_any(const NormArgs& a, bool vec, bool fp8, int sms, cudaStream_t st) {
+    const int64_t vectors = (a.cols + 7) / 8;
+    int v = 2; if (getenv("VPT")) v = atoi(getenv("VPT"));
+    if (vec && vectors <= 2048 && v && RowRing<T, 2, 2>::bytes((vectors + 63) / 64 * 32) <= kRingBytesMost) {
+        if (v == 2) return fp8 ? launch_norm_ring<T, 2, true>(a, sms, st) : launch_norm_ring<T, 2, false>(a, sms, st);
+        if (v == 4) return fp8 ? launch_norm_ring<T, 4, true>(a, sms, st) : launch_norm_ring<T, 4, false>(a, sms, st);
+        if (v == 1) return fp8 ? launch_norm_ring<T, 1, true>(a, sms, st) : launch_norm_ring<T, 1, false>(a, sms, st);
+    }
     if (vec) return fp8 ? launch_norm<T, true, true>(a, st) : launch_norm<T, true, false>(a, st);
     return fp8 ? launch_norm<T, false, true>(a, st) : launch_norm<T, false, false>(a, st);
 }
 
-constexpr int kGradVpt = 2;
+#ifndef GV
+#define GV 2
+#define GC 512
+#endif
+constexpr int kGradVpt = GV;
 
 struct GradGeometry { int threads, per_block, blocks, spans; };
 
@@ -510,7 +758,7 @@ GradGeometry grad_geometry(int64_t rows, int64_t cols, int sms) {
     g.spans = static_cast<int>((vectors + kGradVpt * g.threads - 1) / (kGradVpt * g.threads));
     g.per_block = g.threads == 32 ? 8 : 1;
     const int64_t resident =
-        static_cast<int64_t>(sms) * std::min(8, 1024 / (g.threads * g.per_block));
+        static_cast<int64_t>(sms) * std::max(1, std::min(8, GC / (g.threads * g.per_block)));
     g.blocks = static_cast<int>(
         std::max<int64_t>(1, std::min((rows + g.per_block - 1) / g.per_block, resident)));
     return g;
@@ -519,6 +767,14 @@ GradGeometry grad_geometry(int64_t rows, int64_t cols, int sms) {
 template <typename T>
 int launch_grad(const GradArgs& a, bool vec, const GradGeometry& g, cudaStream_t st) {
     const dim3 grid(g.blocks, g.spans), block(g.threads, g.per_block);
+    const size_t smem = RowRing<T, 3, kGradVpt>::bytes(g.threads * g.per_block);
+    if (vec && g.spans == 1 && smem <= kRingBytesMost && !getenv("NORING")) {
+        static std::atomic<uint64_t> opted{0};
+        const cudaError_t e =
+            opt_in_smem(rmsnorm_grad_ring_kernel<T, kGradVpt>, kRingBytesMost, &opted);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        return launch(rmsnorm_grad_ring_kernel<T, kGradVpt>, grid, block, smem, st, a);
+    }
     return vec ? launch(rmsnorm_grad_kernel<T, kGradVpt, true>, grid, block, 0, st, a)
                : launch(rmsnorm_grad_kernel<T, kGradVpt, false>, grid, block, 0, st, a);
 }
@@ -596,10 +852,12 @@ int tiles_rmsnorm(const tiles_rmsnorm_desc* d, void* stream) {
                      whole16(d->weight, 0, 1) &&
                      (fp8 ? whole8(d->y, d->ldy) : whole16(d->y, d->ldy, eb));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    if ((s = current_sm_count(&sms)) != TILES_OK) return s;
     int e;
-    if (d->dtype == TILES_BF16) e = launch_norm_any<__nv_bfloat16>(a, vec, fp8, st);
-    else if (d->dtype == TILES_F16) e = launch_norm_any<__half>(a, vec, fp8, st);
-    else e = launch_norm_any<float>(a, vec, fp8, st);
+    if (d->dtype == TILES_BF16) e = launch_norm_any<__nv_bfloat16>(a, vec, fp8, sms, st);
+    else if (d->dtype == TILES_F16) e = launch_norm_any<__half>(a, vec, fp8, sms, st);
+    else e = launch_norm_any<float>(a, vec, fp8, sms, st);
     return launch_status(e, "norm");
 }
 
@@ -608,7 +866,7 @@ size_t tiles_rmsnorm_grad_workspace_bytes(int64_t rows, int64_t cols) {
     int sms = 0;
     if (current_sm_count(&sms) != TILES_OK) return 0;
     const GradGeometry g = grad_geometry(rows, cols, sms);
-    return std::max<size_t>(kConvMinWorkspaceBytes, static_cast<size_t>(g.blocks) * cols * 4);
+    return kConvMinWorkspaceBytes + static_cast<size_t>(g.blocks) * cols * 4;
 }
 
 int tiles_rmsnorm_grad(const tiles_rmsnorm_grad_desc* d, void* ws, size_t ws_bytes, void* stream) {
@@ -630,15 +888,16 @@ int tiles_rmsnorm_grad(const tiles_rmsnorm_grad_desc* d, void* ws, size_t ws_byt
     if (d->dh && (s = check_matrix("dh", d->dh, d->lddh, d->cols, eb)) != TILES_OK) return s;
     if ((s = check_matrix("dx", d->dx, d->lddx, d->cols, eb)) != TILES_OK) return s;
     if (!ws) return fail(TILES_ERR_INVALID_ARG, "the norm gradient needs a workspace");
-    if (reinterpret_cast<uintptr_t>(ws) & 3u)
-        return fail(TILES_ERR_MISALIGNED, "the workspace must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(ws) & 15u)
+        return fail(TILES_ERR_MISALIGNED, "the workspace must be 16-byte aligned");
     int sms = 0;
     if ((s = current_sm_count(&sms)) != TILES_OK) return s;
     const GradGeometry g = grad_geometry(d->rows, d->cols, sms);
-    const size_t need = static_cast<size_t>(g.blocks) * d->cols * 4;
+    const size_t need = kConvMinWorkspaceBytes + static_cast<size_t>(g.blocks) * d->cols * 4;
     if (ws_bytes < need)
         return fail(TILES_ERR_INVALID_ARG, "the norm gradient needs %zu workspace bytes", need);
-    GradArgs a{d->rows, d->cols, d->dy, d->h, d->weight, d->dh, d->dx, static_cast<float*>(ws),
+    GradArgs a{d->rows, d->cols, d->dy, d->h, d->weight, d->dh, d->dx,
+               reinterpret_cast<float*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes),
                d->lddy, d->ldh, d->lddh, d->lddx, d->eps, d->weight_dtype};
     const bool vec = d->cols % 8 == 0 && whole16(d->dy, d->lddy, eb) && whole16(d->h, d->ldh, eb) &&
                      whole16(d->dh, d->lddh, eb) && whole16(d->dx, d->lddx, eb) &&

@@ -350,8 +350,8 @@ int pair_max_groups(int sms) {
 
 int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const ProductArgs& args,
                  int units, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        pair8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(pair8_kernel, kSmemBytes, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
     return launch_cluster(pair8_kernel, 2, dim3(static_cast<unsigned>(2 * units)), dim3(kThreads),
                           kSmemBytes, st, weight, rows, args);

@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int KIND>
 int launch_kind(const CUtensorMap& w, const CUtensorMap& a, const ProductArgs& args, int units,
                 cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        pair_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(pair_kernel<KIND>, kSmemBytes, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
     return launch_cluster(pair_kernel<KIND>, 2, dim3(static_cast<unsigned>(2 * units)),
                           dim3(kThreads), kSmemBytes, st, w, a, args);

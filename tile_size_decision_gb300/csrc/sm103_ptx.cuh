@@ -504,7 +504,7 @@ __device__ __forceinline__ void st_matrix_x4_trans(uint32_t saddr, uint32_t r0, 
 
 // {d.x, d.y} += {a.x * b.x, a.y * b.y}, fused, in one instruction.
 __device__ __forceinline__ void fma_pair(uint64_t& d, uint64_t a, uint64_t b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+    asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
 __device__ __forceinline__ uint64_t pack_pair(uint32_t lo, uint32_t hi) {
@@ -564,6 +564,17 @@ __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gmem_src
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem_dst)),
                  "l"(gmem_src)
                  : "memory");
+}
+
+// Close this thread's copies since the last call into a group, and wait
+// until at most N of its groups are in flight.
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait_groups() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void cp_async_wait_all() {

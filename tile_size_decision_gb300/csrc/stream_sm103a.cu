@@ -317,8 +317,8 @@ template <int KIND, int NT>
 int launch_one(const CUtensorMap& w, const CUtensorMap& a, const ProductArgs& args, int64_t units,
                cudaStream_t st) {
     using L = StreamLayout<KIND, NT>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        stream_kernel<KIND, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_BYTES);
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(stream_kernel<KIND, NT>, L::SMEM_BYTES, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
     return launch_cluster(stream_kernel<KIND, NT>, args.split,
                           dim3(static_cast<unsigned>(units * args.split)), dim3(kThreads),
