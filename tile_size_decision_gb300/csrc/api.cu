@@ -485,6 +485,23 @@ int encode_box(CUtensorMap* map, CUtensorMapDataType type, const void* base, uin
     return TILES_OK;
 }
 
+bool encode_out_boxes(CUtensorMap* map, int dtype, void* base, uint64_t d0, uint64_t d1,
+                      uint64_t d2, uint64_t pitch1, uint64_t pitch2) {
+    auto fn = encode_fn();
+    const uint64_t eb = dtype == TILES_F32 ? 4 : 2;
+    if (!fn || !aligned16(base) || pitch1 * eb % 16 || pitch2 * eb % 16) return false;
+    const CUtensorMapDataType t = dtype == TILES_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                  : dtype == TILES_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    cuuint64_t dims[3] = {d0, d1, d2};
+    cuuint64_t strides[2] = {pitch1 * eb, pitch2 * eb};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(64 / eb), 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, t, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int current_sm_count(int* sms) {
     static std::atomic<int> known[64];
     int d = 0;

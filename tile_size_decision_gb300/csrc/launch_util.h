@@ -82,4 +82,10 @@ int encode_box(CUtensorMap* map, CUtensorMapDataType type, const void* base, uin
                uint64_t d1, uint64_t d2, uint64_t pitch1_bytes, uint64_t pitch2_bytes,
                uint32_t box0, uint32_t box1);
 
+// The map through which whole 32-row x 64-byte boxes of an output leave (a
+// [d2][d1][d0] array of F32, F16 or BF16, element pitches, 64-byte swizzle).
+// False where TMA cannot address it (base or pitches not 16-byte multiples).
+bool encode_out_boxes(CUtensorMap* map, int dtype, void* base, uint64_t d0, uint64_t d1,
+                      uint64_t d2, uint64_t pitch1, uint64_t pitch2);
+
 }  // namespace tiles

@@ -24,8 +24,8 @@
 namespace tiles {
 namespace {
 
-constexpr int kScaleSlots = 8;
-constexpr int kScaleBatch = 4;                        // K blocks whose scales are fetched at once
+constexpr int kScaleSlots = kSideSlots;
+constexpr int kScaleLag = 10;                         // K blocks whose scales are on their way in
 constexpr int kSlotFloats = 128 + 8;                  // 128 rows, 8 chunks of 32 columns
 constexpr int kScaleBytes = kScaleSlots * kSlotFloats * 4;
 constexpr int kSmemBytes = kStages * kStageBytes + kStagingBytes + kScaleBytes + kBarrierBytes +
@@ -34,8 +34,8 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 static_assert(kScaleBytes % 16 == 0, "the barriers follow the scales");
 constexpr int BK = 128;
 // Registers a thread: the epilogue holds 128 sums.  The block is launched
-// with 168 (384 x 168 = 64512), and 128 x 104 + 256 x 200 is the same total.
-constexpr int kServiceRegisters = 104, kEpilogueRegisters = 200;
+// with 168 (384 x 168 = 64512), and 128 x 72 + 256 x 216 is the same total.
+constexpr int kServiceRegisters = 72, kEpilogueRegisters = 216;
 static_assert(128 * kServiceRegisters + 256 * kEpilogueRegisters <= kThreads * 168, "registers");
 
 struct Unit {
@@ -67,7 +67,7 @@ struct Units {
 
 __global__ void __launch_bounds__(kThreads, 1)
     pair8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
-                 const ProductArgs args) {
+                 const __grid_constant__ CUtensorMap tmC, const ProductArgs args) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t* base = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -149,8 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             do {
                 const uint32_t idesc = args.idesc | static_cast<uint32_t>(un.width >> 3) << 17;
                 for (int b = 0; b < blocks; ++b) {
-                    const bool ok = ptx::mbar_wait(&bar->acc_empty[acc], acc_phase ^ 1u, abort, limit) &&
-                                    ptx::mbar_wait(&bar->full[stage], phase, abort, limit);
+                    // The accumulator comes last: its return is what a K block
+                    // usually waits for.
+                    const bool ok = ptx::mbar_wait(&bar->full[stage], phase, abort, limit) &&
+                                    ptx::mbar_wait(&bar->acc_empty[acc], acc_phase ^ 1u, abort, limit);
                     if (!__all_sync(0xffffffffu, ok)) {
                         failed = true;
                         break;
@@ -180,44 +182,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- scales ----------------
-            uint32_t slot = 0, phase = 0;
+            // Asynchronous copies into the ring, kScaleLag K blocks ahead of
+            // the slot that is handed on (across units).  Scales of rows past
+            // the end are not copied: their sums are never written.
+            uint32_t slot = 0, phase = 0, done = 0;
+            int pending = 0;
             do {
                 const int row0 = un.row0 + static_cast<int>(rank) * 128 + lane;
-                const float* sa = args.sa;
+                const float* sa = args.sa + row0 * args.sa_row;
                 // Lane c < 8: the weight's scale of column chunk c.
                 const float* sb = args.sb + un.group * args.sb_group +
                                   (min(un.n0 + (lane & 7) * 32, args.n - 1) / kScaleBlock) * args.sb_row;
-                for (int b0 = 0; b0 < blocks && !failed; b0 += kScaleBatch) {
-                    float r[kScaleBatch][4], w[kScaleBatch];
-#pragma unroll
-                    for (int j = 0; j < kScaleBatch; ++j) {
-                        const int64_t b = min(b0 + j, blocks - 1);
-                        w[j] = sb[b * args.sb_block];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = row0 + i * 32;
-                            r[j][i] = row < un.end ? sa[row * args.sa_row + b * args.sa_block] : 0.0f;
-                        }
+                for (int b = 0; b < blocks; ++b) {
+                    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->side_empty[slot], phase ^ 1u,
+                                                                abort, limit))) {
+                        failed = true;
+                        break;
                     }
+                    float* to = scales + slot * kSlotFloats + lane;
 #pragma unroll
-                    for (int j = 0; j < kScaleBatch; ++j) {
-                        if (b0 + j >= blocks || failed) continue;
-                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bar->side_empty[slot],
-                                                                    phase ^ 1u, abort, limit))) {
-                            failed = true;
-                            continue;
-                        }
-                        float* to = scales + slot * kSlotFloats;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) to[i * 32 + lane] = r[j][i];
-                        if (lane < 8) to[128 + lane] = w[j];
+                    for (int i = 0; i < 4; ++i)
+                        if (row0 + i * 32 < un.end) ptx::cp_async_4(to + i * 32, sa + i * 32 * args.sa_row);
+                    if (lane < 8) ptx::cp_async_4(to + 128, sb);
+                    ptx::cp_async_commit();
+                    sa += args.sa_block;
+                    sb += args.sb_block;
+                    if (++slot == kScaleSlots) { slot = 0; phase ^= 1u; }
+                    if (++pending > kScaleLag) {
+                        ptx::cp_async_wait_groups<kScaleLag>();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&bar->side_full[slot]);
-                        if (++slot == kScaleSlots) { slot = 0; phase ^= 1u; }
+                        if (lane == 0) ptx::mbar_arrive(&bar->side_full[done]);
+                        done = (done + 1) % kScaleSlots;
+                        --pending;
                     }
                 }
             } while (!failed && walk.next(bar, abort, limit, &failed) &&
                      units.get(walk.unit, args, &un));
+            ptx::cp_async_wait_groups<0>();
+            __syncwarp();
+            for (; pending > 0; --pending) {
+                if (lane == 0) ptx::mbar_arrive(&bar->side_full[done]);
+                done = (done + 1) % kScaleSlots;
+            }
             if (failed && lane == 0) raise_error(args.err, abort, kErrEpilogue);
         }
     } else {
@@ -225,13 +231,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::registers_inc<kEpilogueRegisters>();
         const int quarter = warp & 3, set = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        uint8_t* box_ptr = staging + (warp - 4) * 32 * kStagePitch;
-        const uint32_t box = ptx::smem_addr(box_ptr) + lane * kStagePitch;
+        uint8_t* box = staging + (warp - 4) * kBoxBytes;
         const bool f16 = args.c_dtype == TILES_F16;
-        const int out_bytes = args.c_dtype == TILES_F32 ? 4 : 2;
-        const bool vec = (reinterpret_cast<uintptr_t>(args.c) & 15u) == 0 &&
-                         args.ldc * out_bytes % 16 == 0;
+        // One 64-byte row of the box, from 16 words.
+        auto fill = [&](const uint32_t (&w)[16]) {
+            box_begin();
+            const uint32_t at = ptx::smem_addr(box);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                ptx::st_shared_v4(at + box_piece(lane, q), w[4 * q], w[4 * q + 1], w[4 * q + 2],
+                                  w[4 * q + 3]);
+        };
         uint32_t acc = 0, acc_phase = 0, slot = 0, slot_phase = 0;
+        // The leader's acc_empty barriers.
+        const uint32_t acc_empty = ptx::map_to_cta(ptx::smem_addr(&bar->acc_empty[0]), 0);
         do {
             // This thread's row: columns 64 * (2h + set) + 32q + .. in
             // sum[2h + q], as pairs.
@@ -254,25 +267,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) ptx::mbar_arrive(&bar->side_empty[slot]);
                 ptx::tc_fence_after();
+                // 16 columns at a time, the next ones' load in flight while
+                // these are added.  (Columns past the width hold old sums
+                // that nothing reads.)
                 const uint32_t t = tmem + lanes + acc * kMaxWidth + set * 64;
+                auto column = [](int i) { return (i >> 2) * 128 + (i & 3) * 16; };
+                constexpr int parts = 8;
+                uint32_t v[2][16];
+                if (parts > 0) {
+                    ptx::tmem_ld_16cols(t, v[0], 0);
+                    ptx::tmem_ld_wait();
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = (j >> 1) * 128 + (j & 1) * 32;   // + 64 * set
-                    if (col + set * 64 < un.width) {
-                        uint32_t v[32];
-                        ptx::tmem_ld_32cols(t + col, v);
-                        const float s = row_scale * w[j];
+                for (int i = 0; i < 8; ++i) {
+                    if (i < parts) {
+                        if (i + 1 < parts) {
+                            ptx::tmem_ld_16cols(t + column(i + 1), v[(i + 1) & 1], 0);
+                        } else {
+                            // All read: back to the MMA before the last sums.
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive_remote(acc_empty + acc * 8);
+                        }
+                        const float s = row_scale * w[i >> 1];
                         const uint64_t ss = ptx::pack_pair(__float_as_uint(s), __float_as_uint(s));
-                        ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            ptx::fma_pair(sum[j][i], ptx::pack_pair(v[2 * i], v[2 * i + 1]), ss);
+                        for (int q = 0; q < 8; ++q)
+                            ptx::fma_pair(sum[i >> 1][(i & 1) * 8 + q],
+                                          ptx::pack_pair(v[i & 1][2 * q], v[i & 1][2 * q + 1]), ss);
+                        if (i + 1 < parts) ptx::tmem_ld_wait_for(v[(i + 1) & 1]);
                     }
                 }
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    ptx::mbar_arrive_remote(ptx::map_to_cta(ptx::smem_addr(&bar->acc_empty[acc]), 0));
                 if (++slot == kScaleSlots) { slot = 0; slot_phase ^= 1u; }
                 acc ^= 1u;
                 if (acc == 0) acc_phase ^= 1u;
@@ -286,36 +311,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int cols = min(args.n, un.n0 + un.width) - col0;
                 if (rows <= 0 || cols <= 0) break;
                 const int64_t out0 = static_cast<int64_t>(row0) * args.ldc + col0;
-                uint32_t v[32];
+                uint32_t v[2][16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ptx::unpack_pair(sum[j][i], v[2 * i], v[2 * i + 1]);
+                for (int i = 0; i < 16; ++i)
+                    ptx::unpack_pair(sum[j][i], v[i >> 3][2 * (i & 7)], v[i >> 3][2 * (i & 7) + 1]);
                 if (args.c_dtype == TILES_F32) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        __syncwarp();
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            ptx::st_shared_v4(box + q * 16, v[h * 16 + 4 * q], v[h * 16 + 4 * q + 1],
-                                              v[h * 16 + 4 * q + 2], v[h * 16 + 4 * q + 3]);
-                        __syncwarp();
-                        copy_staging(box_ptr, static_cast<float*>(args.c) + out0 + h * 16, args.ldc,
-                                     rows, cols - h * 16, vec);
+                        fill(v[h]);
+                        if (cols > h * 16)
+                            box_end(&tmC, args.tma_store, box, col0 + h * 16, row0, 0,
+                                    static_cast<float*>(args.c) + out0 + h * 16, args.ldc, rows,
+                                    cols - h * 16, false);
                     }
                 } else {
-                    __syncwarp();
+                    uint32_t p[16];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        ptx::st_shared_v4(box + q * 16, pack16(v[8 * q], v[8 * q + 1], f16),
-                                          pack16(v[8 * q + 2], v[8 * q + 3], f16),
-                                          pack16(v[8 * q + 4], v[8 * q + 5], f16),
-                                          pack16(v[8 * q + 6], v[8 * q + 7], f16));
-                    __syncwarp();
-                    copy_staging(box_ptr, static_cast<uint16_t*>(args.c) + out0, args.ldc, rows, cols,
-                                 vec);
+                    for (int i = 0; i < 16; ++i)
+                        p[i] = pack16(v[i >> 3][2 * (i & 7)], v[i >> 3][2 * (i & 7) + 1], f16);
+                    fill(p);
+                    box_end(&tmC, args.tma_store, box, col0, row0, 0,
+                            static_cast<uint16_t*>(args.c) + out0, args.ldc, rows, cols, false);
                 }
             }
         } while (walk.next(bar, abort, limit, &failed) && units.get(walk.unit, args, &un));
         if (failed && lane == 0) raise_error(args.err, abort, kErrEpilogue);
+        box_begin();                                       // the last box has been read
     }
     pair_teardown(tmem);
 }
@@ -348,13 +369,13 @@ int pair_max_groups(int sms) {
     return clusters;
 }
 
-int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const ProductArgs& args,
-                 int units, cudaStream_t st) {
+int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const CUtensorMap& out,
+                 const ProductArgs& args, int units, cudaStream_t st) {
     static std::atomic<uint64_t> opted{0};
     const cudaError_t e = opt_in_smem(pair8_kernel, kSmemBytes, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
     return launch_cluster(pair8_kernel, 2, dim3(static_cast<unsigned>(2 * units)), dim3(kThreads),
-                          kSmemBytes, st, weight, rows, args);
+                          kSmemBytes, st, weight, rows, out, args);
 }
 
 }  // namespace tiles

@@ -76,7 +76,7 @@ struct Units {
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
-                const ProductArgs args) {
+                const __grid_constant__ CUtensorMap tmC, const ProductArgs args) {
     constexpr bool GRAD = KIND == kWeightGrad;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The weight gradient's stages are completed by both CTAs (the producers,
     // or the warps that clear a ragged end).  Walkers: both TMA warps, every
     // epilogue warp, the MMA warp, and the clearing warps.
-    pair_setup(bar, GRAD ? 2 : 1, 2 + 16 + 1 + (GRAD ? 2 : 0), 1, &tmW, &tmA);
+    pair_setup(bar, GRAD ? 2 : 1, 2 + 16 + 1 + (GRAD ? 2 : 0), 8, &tmW, &tmA);
 
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
@@ -264,13 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- epilogue ----------------
         const int quarter = warp & 3, set = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        uint8_t* box_ptr = staging + (warp - 4) * 32 * kStagePitch;
-        const uint32_t box = ptx::smem_addr(box_ptr);
+        uint8_t* box = staging + (warp - 4) * kBoxBytes;
         const bool f16 = args.c_dtype == TILES_F16;
-        const int out_bytes = args.c_dtype == TILES_F32 ? 4 : 2;
-        const bool vec = (reinterpret_cast<uintptr_t>(args.c) & 15u) == 0 &&
-                         args.ldc * out_bytes % 16 == 0 &&
-                         (!GRAD || args.stride_c * out_bytes % 16 == 0);
         // One chunk of 32 columns of this warp's 32 lanes leaves: v0 holds
         // lanes 0-15, v1 lanes 16-31, in the fragment layout.
         auto emit = [&](const uint32_t (&v0)[16], const uint32_t (&v1)[16], int col) {
@@ -299,18 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 return;
             }
-            __syncwarp();                                  // the box's last readers are done
+            box_begin();
             // Matrix q of a store is lanes 8q .. 8q+7; lane t addresses row
             // t%8 of matrix t/8.
-            const uint32_t to = box + (lane & 7) * kStagePitch + (lane >> 3) * 16;
+            const uint32_t to = ptx::smem_addr(box);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                ptx::st_matrix_x4_trans(to + i * 8 * kStagePitch, pack16(v0[4 * i], v0[4 * i + 1], f16),
+                ptx::st_matrix_x4_trans(to + box_piece(i * 8 + (lane & 7), lane >> 3),
+                                        pack16(v0[4 * i], v0[4 * i + 1], f16),
                                         pack16(v0[4 * i + 2], v0[4 * i + 3], f16),
                                         pack16(v1[4 * i], v1[4 * i + 1], f16),
                                         pack16(v1[4 * i + 2], v1[4 * i + 3], f16));
-            __syncwarp();
-            copy_staging(box_ptr, static_cast<uint16_t*>(args.c) + out0, args.ldc, rows, cols, vec);
+            box_end(&tmC, args.tma_store, box, f0, row0, GRAD ? un.group : 0,
+                    static_cast<uint16_t*>(args.c) + out0, args.ldc, rows, cols, GRAD);
         };
         uint32_t acc = 0, acc_phase = 0;
         do {
@@ -336,34 +332,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                ptx::mbar_arrive_remote(ptx::map_to_cta(ptx::smem_addr(&bar->acc_empty[acc]), 0));
+            if (lane == 0) hand_back(&bar->acc_empty[acc], leader);
             acc ^= 1u;
             if (acc == 0) acc_phase ^= 1u;
         } while (walk.next(bar, abort, limit, &failed) && units.get(walk.unit, args, &un));
         if (failed && lane == 0) raise_error(args.err, abort, kErrEpilogue);
+        box_begin();                                       // the last box has been read
     }
     pair_teardown(tmem);
 }
 
 template <int KIND>
-int launch_kind(const CUtensorMap& w, const CUtensorMap& a, const ProductArgs& args, int units,
-                cudaStream_t st) {
+int launch_kind(const CUtensorMap& w, const CUtensorMap& a, const CUtensorMap& c,
+                const ProductArgs& args, int units, cudaStream_t st) {
     static std::atomic<uint64_t> opted{0};
     const cudaError_t e = opt_in_smem(pair_kernel<KIND>, kSmemBytes, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
     return launch_cluster(pair_kernel<KIND>, 2, dim3(static_cast<unsigned>(2 * units)),
-                          dim3(kThreads), kSmemBytes, st, w, a, args);
+                          dim3(kThreads), kSmemBytes, st, w, a, c, args);
 }
 
 }  // namespace
 
 int launch_pair(int kind, const CUtensorMap& weight, const CUtensorMap& rows,
-                const ProductArgs& args, int units, cudaStream_t st) {
+                const CUtensorMap& out, const ProductArgs& args, int units, cudaStream_t st) {
     switch (kind) {
-        case kWeight16KN: return launch_kind<kWeight16KN>(weight, rows, args, units, st);
-        case kWeight16NK: return launch_kind<kWeight16NK>(weight, rows, args, units, st);
-        default: return launch_kind<kWeightGrad>(weight, rows, args, units, st);
+        case kWeight16KN: return launch_kind<kWeight16KN>(weight, rows, out, args, units, st);
+        case kWeight16NK: return launch_kind<kWeight16NK>(weight, rows, out, args, units, st);
+        default: return launch_kind<kWeightGrad>(weight, rows, out, args, units, st);
     }
 }
 

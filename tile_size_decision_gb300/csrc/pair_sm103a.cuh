@@ -15,15 +15,17 @@ constexpr int kStageBytes = 2 * kHalfBytes;
 constexpr int kAtomBytes = 64 * 128;
 constexpr int kBoxRows = 32;                          // rows per TMA box of the MMA's N operand
 constexpr int kMaxWidth = 256;                        // TMEM columns of a tile
-// Epilogue staging, per warp: 32 rows of 64 bytes, padded so that eight
-// 16-byte accesses to successive rows hit distinct banks.
-constexpr int kStagePitch = 80;
-constexpr int kStagingBytes = 8 * 32 * kStagePitch;
+// Epilogue staging, per warp: a box of 32 rows of 64 bytes in the 64-byte
+// swizzle of a tensor map (16-byte piece q of row r sits at q ^ (r/2 % 4)), so
+// that eight accesses to successive rows hit distinct banks.
+constexpr int kBoxBytes = 32 * 64;
+constexpr int kStagingBytes = 8 * kBoxBytes;
 constexpr int kBarrierBytes = 768;
+constexpr int kSideSlots = 16;
 
 struct PairBarriers {
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
-    uint64_t side_full[8], side_empty[8];             // scales (8-bit), ragged ends (gradient)
+    uint64_t side_full[kSideSlots], side_empty[kSideSlots];   // scales (8-bit), ragged ends (gradient)
     uint64_t drain;
     uint64_t next_full[2], next_empty[2];
     ulonglong2 next[2];                               // answers about the next unit
@@ -82,11 +84,17 @@ struct Asker {
     }
 };
 
+// An accumulator goes back to the leader's MMA warp (lane 0 of a warp).
+__device__ __forceinline__ void hand_back(uint64_t* acc_empty, bool leader) {
+    if (leader) ptx::mbar_arrive(acc_empty);
+    else ptx::mbar_arrive_remote(ptx::map_to_cta(ptx::smem_addr(acc_empty), 0));
+}
+
 // Set-up of a pair: barriers and tensor memory.  stage_arrivals: arrivals that
 // complete a stage's full barrier; walkers: warps of the pair that walk the
-// units; side_readers: arrivals on a side slot's empty barrier.
+// units; readers: epilogue warps of a CTA.
 __device__ __forceinline__ void pair_setup(PairBarriers* bar, int stage_arrivals, int walkers,
-                                           int side_readers, const CUtensorMap* a,
+                                           int readers, const CUtensorMap* a,
                                            const CUtensorMap* b) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -95,13 +103,13 @@ __device__ __forceinline__ void pair_setup(PairBarriers* bar, int stage_arrivals
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bar->acc_full[i], 1);
-            ptx::mbar_init(&bar->acc_empty[i], 16);       // every epilogue warp of the pair
+            ptx::mbar_init(&bar->acc_empty[i], 2 * readers);
             ptx::mbar_init(&bar->next_full[i], 1);
             ptx::mbar_init(&bar->next_empty[i], walkers);
         }
-        for (int s = 0; s < 8; ++s) {
+        for (int s = 0; s < kSideSlots; ++s) {
             ptx::mbar_init(&bar->side_full[s], 1);
-            ptx::mbar_init(&bar->side_empty[s], side_readers);
+            ptx::mbar_init(&bar->side_empty[s], readers);
         }
         ptx::mbar_init(&bar->drain, 1);
         bar->abort = 0;
@@ -133,26 +141,48 @@ __device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi, bool f16) {
     return f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
 
-// The 32 rows x 64 bytes of a warp's staging leave for rows of `pitch` bytes
-// at `out`, as 16-byte pieces where `vec` and the piece is whole, else
-// element by element; rows and cols are what may be written.
+__device__ __forceinline__ uint32_t box_piece(int row, int piece) {
+    return static_cast<uint32_t>(row * 64 + ((piece ^ (row >> 1 & 3)) << 4));
+}
+
+// The previous box has left: the warp may write the next.
+__device__ __forceinline__ void box_begin() {
+    if ((threadIdx.x & 31) == 0) ptx::bulk_wait_read_all();
+    __syncwarp();
+}
+
+// The warp's box leaves for columns x .. and rows y .. of item z of c: whole
+// boxes through one TMA store (clipped at the tensor's edges), a ragged
+// group's last rows, or a c that TMA cannot address, through the registers.
+// `out` is the box's first element, and rows x cols what may be written.
 template <typename E>
-__device__ __forceinline__ void copy_staging(const uint8_t* box, E* out, int64_t ld, int rows,
-                                             int cols, bool vec) {
+__device__ __forceinline__ void box_end(const CUtensorMap* map, bool tma, const uint8_t* box, int x,
+                                        int y, int z, E* out, int64_t ld, int rows, int cols,
+                                        bool whole_rows) {
     constexpr int PER = 16 / static_cast<int>(sizeof(E));
     const int lane = threadIdx.x & 31;
-    const int piece = (lane & 3) * PER;
+    if (tma && (whole_rows || rows >= 32)) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            ptx::tma_store_3d(map, box, x, y, z);
+            ptx::bulk_commit_group();
+        }
+        return;
+    }
+    __syncwarp();
+    const int first = (lane & 3) * PER;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2);
         if (r >= rows) break;
-        const uint8_t* from = box + r * kStagePitch + (lane & 3) * 16;
-        E* at = out + r * ld + piece;
-        if (vec && piece + PER <= cols) {
+        const uint8_t* from = box + box_piece(r, lane & 3);
+        E* at = out + r * ld + first;
+        if (tma && first + PER <= cols) {
             *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(from);
         } else {
             for (int j = 0; j < PER; ++j)
-                if (piece + j < cols) at[j] = reinterpret_cast<const E*>(from)[j];
+                if (first + j < cols) at[j] = reinterpret_cast<const E*>(from)[j];
         }
     }
 }

@@ -168,8 +168,10 @@ int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_b
         s = encode_box(&ta, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
                        fp8 ? 128 : 32);
         if (s != TILES_OK) return s;
-        return launch_status(fp8 ? launch_pair8(tw, ta, args, static_cast<int>(units), st)
-                                 : launch_pair(kind, tw, ta, args, static_cast<int>(units), st),
+        CUtensorMap tc{};
+        args.tma_store = encode_out_boxes(&tc, d->out_dtype, d->c, d->n, d->m, 1, d->ldc, d->ldc);
+        return launch_status(fp8 ? launch_pair8(tw, ta, tc, args, static_cast<int>(units), st)
+                                 : launch_pair(kind, tw, ta, tc, args, static_cast<int>(units), st),
                              grouped ? "grouped product" : "8-bit product");
     }
     s = encode_box(&tw, map_type(d->in_dtype), d->b, kn ? d->n : d->k, kn ? d->k : d->n, groups,
@@ -272,7 +274,10 @@ int tiles_grouped_wgrad(const tiles_wgrad_desc* d, void* ws, size_t ws_bytes, vo
                    d->lda * 2, d->lda * 2, 64, 64);
     if (s != TILES_OK) return s;
     const int64_t units = d->groups * ((d->k + 255) / 256) * args.n_blocks;
-    return launch_status(launch_pair(kWeightGrad, tw, ta, args, static_cast<int>(units),
+    CUtensorMap tc{};
+    args.tma_store = encode_out_boxes(&tc, d->out_dtype, d->dw, d->n, d->k, d->groups, d->lddw,
+                                      d->groups > 1 ? d->stride_dw : d->lddw);
+    return launch_status(launch_pair(kWeightGrad, tw, ta, tc, args, static_cast<int>(units),
                                      static_cast<cudaStream_t>(stream)),
                          "grouped weight gradient");
 }

@@ -27,6 +27,7 @@ struct ProductArgs {
     int32_t n_blocks, k_blocks;       // of the kernel's tile
     int32_t split;                    // few rows: CTAs along K (a cluster)
     int32_t tile_cols;                // 8-bit pairs: weight rows a tile, a multiple of 32
+    int32_t tma_store;                // pairs: c leaves through TMA stores (its map is valid)
     int64_t stride_c;                 // weight gradient: elements between groups' results
     void* c;
     int64_t ldc;
@@ -131,11 +132,11 @@ int launch_stream(int kind, int tile_rows, const CUtensorMap& weight, const CUte
 // The 16-bit kernel on CTA pairs: tiles of 256 weight columns by up to 256
 // rows (weight gradient: dc's columns by a's); units is an upper bound.
 int launch_pair(int kind, const CUtensorMap& weight, const CUtensorMap& rows,
-                const ProductArgs& args, int units, cudaStream_t st);
+                const CUtensorMap& out, const ProductArgs& args, int units, cudaStream_t st);
 // The 8-bit kernel on CTA pairs: tiles of 256 rows by args.tile_cols weight
 // rows; units is an upper bound.
-int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const ProductArgs& args,
-                 int units, cudaStream_t st);
+int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const CUtensorMap& out,
+                 const ProductArgs& args, int units, cudaStream_t st);
 // CTA pairs resident at once on the current device.
 int pair_max_groups(int sms);
 

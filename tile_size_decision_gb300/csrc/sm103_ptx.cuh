@@ -504,7 +504,7 @@ __device__ __forceinline__ void st_matrix_x4_trans(uint32_t saddr, uint32_t r0, 
 
 // {d.x, d.y} += {a.x * b.x, a.y * b.y}, fused, in one instruction.
 __device__ __forceinline__ void fma_pair(uint64_t& d, uint64_t a, uint64_t b) {
-    asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
 __device__ __forceinline__ uint64_t pack_pair(uint32_t lo, uint32_t hi) {
@@ -529,6 +529,16 @@ __device__ __forceinline__ void tmem_ld_8cols(uint32_t taddr, uint32_t& r0, uint
 
 __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// The same, and no use of r moves ahead of it: the compiler does not know
+// that a load's registers are filled only then, and copies of them made
+// early (to pair them for fma_pair, say) double the instructions.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // Warp-collective store of 32 consecutive fp32 columns into the warp's 32
@@ -562,6 +572,13 @@ __device__ __forceinline__ void tmem_st_wait() {
 
 __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gmem_src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem_dst)),
+                 "l"(gmem_src)
+                 : "memory");
+}
+
+// The same for 4 bytes.
+__device__ __forceinline__ void cp_async_4(void* smem_dst, const void* gmem_src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(smem_dst)),
                  "l"(gmem_src)
                  : "memory");
 }
