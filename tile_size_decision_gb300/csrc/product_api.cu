@@ -99,6 +99,66 @@ int resident_pairs(int sms, int* pairs) {
     return TILES_OK;
 }
 
+// How a product runs: on CTA pairs, or with the few-rows kernel; the rows and
+// columns of a tile, and the CTAs along K.
+struct Choice { bool pair; int rows, cols, split; };
+
+// The cheaper by a model in nanoseconds, whose constants were measured on a
+// GB300 (times of single products, 8 to 1024 rows, weights of 512^2 to
+// 4096^2).  A kernel takes a fixed time, then the larger of
+//   - its rounds over the resident blocks x K blocks x the time of one, and
+//   - its bytes at the measured copy rate, times how far it stays from it.
+// Few rows (two blocks an SM): 330 / 360 / 530 ns a K block of 128 for tiles of
+// 16 / 32 / 64 rows in 8 bits, 250 / 280 / 360 ns a K block of 64 in 16 bits.
+// Pairs: 460 ns in 8 bits (whatever the tile's width: the hand-over of the
+// sums bounds it), 330 ns in 16 bits.  Both sides of the choice, 4096 x 4096
+// in 8 bits: 64 rows 8.1 us against 18.4 on pairs, 256 rows 13.3 against 18.4,
+// 1024 rows 37.8 against 20.2; 8 groups of 2048 x 2048 in 16 bits: 8 rows a
+// group 12.3 against 13.3, 128 rows 21.3 against 16.0.  Tiles of 128 rows never
+// won: 8-bit sums of 128 rows leave room for one block an SM.
+Choice choose(int kind, int64_t m, int64_t n, int64_t k, int64_t groups, int sms, int pairs) {
+    const bool fp8 = kind == kWeight8NK;
+    const int64_t kb = (k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+    // Row tiles: grouped, half a tile a group more than the rows fill, at
+    // least one for every group that can have rows.
+    auto row_tiles = [&](int64_t rows) {
+        if (groups == 0) return (m + rows - 1) / rows;
+        return std::max(std::min(groups, m), m / rows + groups / 2);
+    };
+    const int64_t eb = fp8 ? 1 : 2;
+    const int64_t weights = groups == 0 ? 1 : std::min(groups, m);
+    const double dram_ns = static_cast<double>((weights * n * k + m * k) * eb + 2 * m * n) / 6786.0;
+    Choice best{};
+    double best_ns = 0;
+    auto offer = [&](const Choice& c, double ns) {
+        if (best_ns == 0 || ns < best_ns) { best = c; best_ns = ns; }
+    };
+    const struct { int rows; double ns8, ns16, far; } few[] = {
+        {16, 330, 250, 1.0}, {32, 360, 280, 1.15}, {64, 530, 360, 1.35}};
+    for (const auto& f : few) {
+        const int64_t units = row_tiles(f.rows) * ((n + 127) / 128);
+        // CTAs along K: while the units leave SMs without a block, at least
+        // two K blocks a CTA.
+        int split = 1;
+        while (split < 8 && units * split < sms && kb >= split * 4) split *= 2;
+        const int64_t rounds = (units * split + 2 * sms - 1) / (2 * sms);
+        const double ns = std::max(static_cast<double>(rounds * ((kb + split - 1) / split)) *
+                                       (fp8 ? f.ns8 : f.ns16) + (split > 1 ? 20.0 * f.rows : 0),
+                                   dram_ns * f.far);
+        offer(Choice{false, f.rows, 128, split}, 3000 + ns);
+    }
+    // 8-bit pairs: the narrowest tile that takes the fewest rounds.
+    int64_t fewest = INT64_MAX;
+    int cols = 256;
+    for (int c = 256; c >= (fp8 ? 64 : 256); c -= 32) {
+        const int64_t rounds = (row_tiles(256) * ((n + c - 1) / c) + pairs - 1) / pairs;
+        if (rounds <= fewest) { fewest = rounds; cols = c; }
+    }
+    offer(Choice{true, 256, cols, 1},
+          4000 + std::max(static_cast<double>(fewest * kb) * (fp8 ? 460 : 330), dram_ns * 1.05));
+    return best;
+}
+
 int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_bytes, void* stream) {
     int s = check_product(d, grouped);
     if (s != TILES_OK) return s;
@@ -133,71 +193,44 @@ int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_b
     args.drop_stage = planted.stage;
     if (planted.stage >= 0) args.wait_limit_ns = planted.limit_ns;
 
-    const int64_t mean = (d->m + groups - 1) / groups;
+    int pairs = 0;
+    if ((s = resident_pairs(sms, &pairs)) != TILES_OK) return s;
+    const Choice choice = choose(kind, d->m, d->n, d->k, grouped ? d->groups : 0, sms, pairs);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    CUtensorMap tw, ta;
+    const char* what = grouped ? "grouped product" : "8-bit product";
+    const bool kn = kind == kWeight16KN;
     const int64_t stride_b = groups > 1 ? d->stride_b : d->ldb;
     args.k_blocks = static_cast<int32_t>((d->k + bk - 1) / bk);
-    // More rows a group than the few-rows kernel's largest tile: CTA pairs.
-    const bool use_pair = mean > 128;
-    const bool kn = kind == kWeight16KN;
-    if (use_pair) {
-        int pairs = 0;
-        if ((s = resident_pairs(sms, &pairs)) != TILES_OK) return s;
-        args.tile_cols = 256;
-        if (fp8 && !grouped) {
-            // The width whose units fill the rounds of the pairs best: a
-            // K block of a unit takes 2 clocks per column of MMA, or the time
-            // to fill 128 rows and half the columns at 64 B/clk.
-            int64_t best = INT64_MAX;
-            for (int nt = 256; nt >= 32; nt -= 32) {
-                const int64_t units = (d->n + nt - 1) / nt * ((d->m + 255) / 256);
-                const int64_t cost = (units + pairs - 1) / pairs * std::max(2 * nt, 256 + nt);
-                if (cost < best) { best = cost; args.tile_cols = nt; }
-            }
-        }
-        args.n_blocks = static_cast<int32_t>((d->n + args.tile_cols - 1) / args.tile_cols);
-        const int64_t row_tiles = grouped ? d->m / 256 + std::min(groups, d->m) : (d->m + 255) / 256;
-        const int64_t units = row_tiles * args.n_blocks;
-        if (units > INT32_MAX / 2) return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
-        args.idesc = fp8 ? ptx::idesc_e4m3_f32acc(256, 0)
-                         : ptx::idesc_f16_f32acc_majors(d->in_dtype == TILES_BF16, kn, false, 256, 0);
-        s = encode_box(&tw, map_type(d->in_dtype), d->b, kn ? d->n : d->k, kn ? d->k : d->n, groups,
-                       d->ldb * eb, stride_b * eb, kn ? 64 : bk, kn ? 64 : fp8 ? 32 : 128);
-        if (s != TILES_OK) return s;
-        s = encode_box(&ta, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
-                       fp8 ? 128 : 32);
-        if (s != TILES_OK) return s;
-        CUtensorMap tc{};
-        args.tma_store = encode_out_boxes(&tc, d->out_dtype, d->c, d->n, d->m, 1, d->ldc, d->ldc);
-        return launch_status(fp8 ? launch_pair8(tw, ta, tc, args, static_cast<int>(units), st)
-                                 : launch_pair(kind, tw, ta, tc, args, static_cast<int>(units), st),
-                             grouped ? "grouped product" : "8-bit product");
-    }
-    s = encode_box(&tw, map_type(d->in_dtype), d->b, kn ? d->n : d->k, kn ? d->k : d->n, groups,
-                   d->ldb * eb, stride_b * eb, kn ? 64 : bk, kn ? 64 : 128);
-    if (s != TILES_OK) return s;
-    // Rows a tile: what an average group has, up to 128.
-    const int tile_rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
-    args.n_blocks = static_cast<int32_t>((d->n + 127) / 128);
+    args.n_blocks = static_cast<int32_t>((d->n + choice.cols - 1) / choice.cols);
     // Row tiles: exact when dense; grouped, every group may end inside one.
-    const int64_t row_tiles = grouped ? d->m / tile_rows + std::min(groups, d->m)
-                                      : (d->m + tile_rows - 1) / tile_rows;
+    const int64_t row_tiles = grouped ? d->m / choice.rows + std::min(groups, d->m)
+                                      : (d->m + choice.rows - 1) / choice.rows;
     const int64_t units = row_tiles * args.n_blocks;
-    // CTAs along K: while the units leave SMs without a block, at least two
-    // K blocks a CTA.
-    args.split = 1;
-    while (args.split < 8 && units * args.split < sms && args.k_blocks >= args.split * 4)
-        args.split *= 2;
-    if (units * args.split > INT32_MAX) return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
-    args.idesc = fp8 ? ptx::idesc_e4m3_f32acc(128, tile_rows)
-                     : ptx::idesc_f16_f32acc_majors(d->in_dtype == TILES_BF16, kn, false, 128,
-                                                    tile_rows);
-    s = encode_box(&ta, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
-                   tile_rows);
+    if (units > INT32_MAX / 16) return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
+    // Boxes: one operand of a stage (MN-major: 64-column atoms), except the
+    // MMA's N operand of a pair, whose tile ends anywhere (32 rows).
+    const bool pair = choice.pair;
+    CUtensorMap tw, ta;
+    s = encode_box(&tw, map_type(d->in_dtype), d->b, kn ? d->n : d->k, kn ? d->k : d->n, groups,
+                   d->ldb * eb, stride_b * eb, kn ? 64 : bk, kn ? 64 : pair && fp8 ? 32 : 128);
     if (s != TILES_OK) return s;
-    return launch_status(launch_stream(kind, tile_rows, tw, ta, args, units, st),
-                         grouped ? "grouped product" : "8-bit product");
+    s = encode_box(&ta, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
+                   !pair ? choice.rows : fp8 ? 128 : 32);
+    if (s != TILES_OK) return s;
+    const int mma_rows = pair ? 256 : 128, mma_cols = pair ? 0 : choice.rows;
+    args.idesc = fp8 ? ptx::idesc_e4m3_f32acc(mma_rows, mma_cols)
+                     : ptx::idesc_f16_f32acc_majors(d->in_dtype == TILES_BF16, kn, false, mma_rows,
+                                                    mma_cols);
+    if (!pair) {
+        args.split = choice.split;
+        return launch_status(launch_stream(kind, choice.rows, tw, ta, args, units, st), what);
+    }
+    args.tile_cols = choice.cols;
+    CUtensorMap tc{};
+    args.tma_store = encode_out_boxes(&tc, d->out_dtype, d->c, d->n, d->m, 1, d->ldc, d->ldc);
+    return launch_status(fp8 ? launch_pair8(tw, ta, tc, args, static_cast<int>(units), st)
+                             : launch_pair(kind, tw, ta, tc, args, static_cast<int>(units), st),
+                         what);
 }
 
 }  // namespace
@@ -240,9 +273,6 @@ int tiles_grouped_wgrad(const tiles_wgrad_desc* d, void* ws, size_t ws_bytes, vo
     if (d->groups * ((d->k + 127) / 128) > INT32_MAX / ((d->n + 127) / 128))
         return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
     if ((s = check_workspace(ws, ws_bytes)) != TILES_OK) return s;
-    int sms = 0, pairs = 0;
-    if ((s = current_sm_count(&sms)) != TILES_OK) return s;
-    if ((s = resident_pairs(sms, &pairs)) != TILES_OK) return s;
     // The tile of the products with other names: dc is the weight side, the
     // columns of a are the rows, and the group's rows the contraction.
     ProductArgs args{};

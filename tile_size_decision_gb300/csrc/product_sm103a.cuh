@@ -124,7 +124,7 @@ __device__ __forceinline__ void store_one(void* c, int64_t at, float v, int dtyp
     else static_cast<__nv_bfloat16*>(c)[at] = __float2bfloat16_rn(v);
 }
 
-// The few-rows kernel: tile_rows in {16, 32, 64, 128}; units is the number
+// The few-rows kernel: tile_rows in {16, 32, 64}; units is the number
 // of (row tile, weight block) pairs launched.
 int launch_stream(int kind, int tile_rows, const CUtensorMap& weight, const CUtensorMap& rows,
                   const ProductArgs& args, int64_t units, cudaStream_t st);

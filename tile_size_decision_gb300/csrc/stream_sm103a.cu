@@ -38,7 +38,7 @@ static_assert(sizeof(Barriers) <= kSmemBarrierBytes, "barrier block too large");
 
 template <int KIND, int NT>
 struct StreamLayout {
-    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 4 : 3;
+    static constexpr int STAGES = NT == 16 ? 6 : NT == 32 ? 5 : 4;
     static constexpr int ROWS_BYTES = NT * kRowBytes;
     static constexpr int STAGE_BYTES = kWeightBytes + ROWS_BYTES;
     static constexpr int SCALE_BYTES = KIND == kWeight8NK ? NT * kScaleChunk * 4 : 0;
@@ -51,6 +51,34 @@ struct StreamLayout {
     static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two blocks per SM");
     static_assert(2 * TMEM_COLS <= 512, "two blocks' tensor memory");
 };
+
+// Columns rank * NT/S .. of the cluster's partial tiles, added in rank order
+// and stored: this thread's weight column, at `mine` in every CTA.  A read from
+// another CTA's shared memory takes a third of a microsecond, so 32 of them
+// are in flight at once.
+template <int S, int NT>
+__device__ __forceinline__ void add_shares(uint32_t mine, int rank, int rows, void* c, int64_t at,
+                                           int64_t ldc, bool in, int dtype) {
+    constexpr int PER = NT / S, BATCH = 32 / S < PER ? 32 / S : PER;
+    uint32_t from[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) from[s] = ptx::map_to_cta(mine, s);
+    for (int c0 = rank * PER; c0 < (rank + 1) * PER && c0 < rows; c0 += BATCH) {
+        float x[S][BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                x[s][j] = ptx::ld_shared_cluster(from[s] + static_cast<uint32_t>(c0 + j) * 512u);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            float v = x[0][j];
+#pragma unroll
+            for (int s = 1; s < S; ++s) v += x[s][j];
+            if (in && c0 + j < rows) store_one(c, at + (c0 + j) * ldc, v, dtype);
+        }
+    }
+}
 
 template <int KIND, int NT>
 __global__ void __launch_bounds__(kThreads)
@@ -215,13 +243,19 @@ __global__ void __launch_bounds__(kThreads)
                     // Every epilogue warp passes here as often, also after
                     // an expired wait, so the barriers always pair up.
                     ptx::named_barrier(1, 128);
-                    const int count = min(kScaleChunk, kb1 - kb) * NT;
-                    for (int i = t; i < count; i += 128) {
-                        const int b = kb + i / NT, row = row0 + i % NT;
-                        scales[i] = row < end ? args.sa[row * args.sa_row + b * args.sa_block] *
-                                                    sb[b * args.sb_block]
-                                              : 0.0f;
+                    // (All loads first: one at a time they took a microsecond
+                    // each.)
+                    constexpr int EACH = kScaleChunk * NT / 128;
+                    float r[EACH], w[EACH];
+#pragma unroll
+                    for (int j = 0; j < EACH; ++j) {
+                        const int i = j * 128 + t, row = row0 + i % NT;
+                        const int64_t b = min(kb + i / NT, args.k_blocks - 1);
+                        r[j] = row < end ? args.sa[row * args.sa_row + b * args.sa_block] : 0.0f;
+                        w[j] = sb[b * args.sb_block];
                     }
+#pragma unroll
+                    for (int j = 0; j < EACH; ++j) scales[j * 128 + t] = r[j] * w[j];
                     ptx::named_barrier(1, 128);
                 }
                 if (ok) ok = __all_sync(0xffffffffu,
@@ -292,16 +326,12 @@ __global__ void __launch_bounds__(kThreads)
         if (warp >= 2 && !*abort) {
             const int f = (warp & 3) * 32 + lane;
             const uint32_t mine = ptx::smem_addr(base) + static_cast<uint32_t>(f) * 4u;
-            for (int c = rank; c < NT; c += split) {
-                if (row0 + c >= end) break;
-                float v = 0.0f;
-                for (int s = 0; s < split; ++s)
-                    v += ptx::ld_shared_cluster(ptx::map_to_cta(mine, s) +
-                                                static_cast<uint32_t>(c) * 512u);
-                if (n0 + f < args.n)
-                    store_one(args.c, static_cast<int64_t>(row0 + c) * args.ldc + n0 + f, v,
-                              args.c_dtype);
-            }
+            const int rows = end - row0, col = n0 + f;
+            void* c = args.c;
+            const int64_t at = static_cast<int64_t>(row0) * args.ldc + col;
+            if (split == 2) add_shares<2, NT>(mine, rank, rows, c, at, args.ldc, col < args.n, args.c_dtype);
+            else if (split == 4) add_shares<4, NT>(mine, rank, rows, c, at, args.ldc, col < args.n, args.c_dtype);
+            else add_shares<8, NT>(mine, rank, rows, c, at, args.ldc, col < args.n, args.c_dtype);
         }
         ptx::cluster_sync();                        // no CTA leaves while another reads from it
     }
@@ -331,8 +361,7 @@ int launch_rows(int tile_rows, const CUtensorMap& w, const CUtensorMap& a, const
     switch (tile_rows) {
         case 16: return launch_one<KIND, 16>(w, a, args, units, st);
         case 32: return launch_one<KIND, 32>(w, a, args, units, st);
-        case 64: return launch_one<KIND, 64>(w, a, args, units, st);
-        default: return launch_one<KIND, 128>(w, a, args, units, st);
+        default: return launch_one<KIND, 64>(w, a, args, units, st);
     }
 }
 
