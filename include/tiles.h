@@ -2,7 +2,9 @@
  * tiles.h — C ABI of libtiles: a tile-size planner (constraints C0-C4) and
  * the GB300 (sm_103a) kernels it drives: a tiled dense GEMM C = A x B with
  * fp16/bf16 inputs and fp32 accumulation, optionally batched, and an NCHW
- * conv2d run as an implicit GEMM tiled over the output height.
+ * conv2d run as an implicit GEMM tiled over the output height; and the
+ * operators that surround the GEMM in a transformer block: root-mean-square
+ * norms, 8-bit products with block scales, and products grouped by expert.
  *
  * Sources of the operations (pages of the tile-size-decision material):
  *   - constraint procedure: page "04-tile-size-decision/tile_decision.py"
@@ -586,13 +588,15 @@ int tiles_selftest_drop_stage(int stage, int64_t limit_ns);
  * indexed through explicit strides (in floats), so either order of rows and
  * blocks works; blocks stored outermost ([blocks][rows]) load fastest.
  * Number of blocks of a length n: ceil(n / 128); the last may be short.
- * A row count of 0 is allowed and does nothing. */
+ * A row count of 0 is allowed and does nothing.  An output may not overlap an
+ * input, except where a norm's h is stored over x or over the residual. */
 
 /* h = x + residual;  y = h * (mean(h^2) + eps)^(-1/2) * weight,  row by row.
  * The sum, the mean and the norm are fp32 and read the sum before it is
  * rounded into h.  out_dtype is dtype, or E4M3: then
  *   scale = max(max|y| over the block / 448, 2^-126),  y8 = e4m3(y / scale)
- * (round to nearest even; a NaN in a row makes its outputs and scales NaN). */
+ * (round to nearest even, saturating at 448; a NaN in a row makes its outputs
+ * and scales NaN; the quotients are within an ulp or two of fp32's). */
 typedef struct {
     int64_t rows, cols;               /* rows >= 0, cols >= 1 */
     const void* x;                    /* device, rows x cols */

@@ -214,3 +214,17 @@ def test_null_descriptors(lib):
     for fn in (lib.tiles_gemm_fp8, lib.tiles_grouped_gemm, lib.tiles_grouped_wgrad):
         assert fn(None, None, 0, None) == _abi.ERR_INVALID_ARG
     assert lib.tiles_rmsnorm_grad_workspace_bytes(4, 0) == 0
+
+
+@pytest.mark.parametrize("packer,desc", [
+    ("_NORM", _abi.RmsnormDesc), ("_NORM_GRAD", _abi.RmsnormGradDesc),
+    ("_PRODUCT", _abi.ProductDesc), ("_WGRAD", _abi.WgradDesc)])
+def test_packed_descriptors_are_the_structures(packer, desc):
+    # The binding packs a descriptor's fields in order; every field must land
+    # on its own in the structure the header declares.
+    import tile_size_decision_gb300 as T
+    packer = getattr(T, packer)
+    assert packer.size == C.sizeof(desc)
+    values = [i + 1 for i in range(len(desc._fields_))]
+    d = desc.from_buffer_copy(packer.pack(*values))
+    assert [getattr(d, name) for name, _ in desc._fields_] == values

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 from . import _abi
 from ._abi import TilesError, check as _check
@@ -516,90 +517,136 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
 
 # ---- norms, 8-bit products and products grouped by expert ------------------------
 #
-# These calls are short (a decoding step's norm takes a few microseconds on
-# the GPU), so the binding checks what the caller passes and nothing that it
-# allocates itself.
+# These calls are short: a decoding step's norm or product takes a few
+# microseconds on the GPU, less than a dozen Python calls take.  So each one
+# checks its arguments in one expression and packs its descriptor directly;
+# only where that fails does _refuse look for what is wrong.
 
 
 SCALE_BLOCK = 128     # columns (and weight rows) that share one scale
 
-
-def _rows2(t, name):
-    """Checks a CUDA matrix with unit stride along its rows; its row pitch.  The pitch of
-    a single row is never used: it is reported as whole 16-byte pieces."""
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    rows, cols = t.shape
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
-    return ld if rows > 1 else (cols + 15) // 16 * 16
+# The descriptors of include/tiles.h, field by field (_abi has their names).
+_NORM = struct.Struct("2q6Q6qf3i")
+_NORM_GRAD = struct.Struct("2q6Q4qf3i")
+_PRODUCT = struct.Struct("4q6Q9q4i")
+_WGRAD = struct.Struct("4q4Q4q2i")
 
 
-def _vector(t, n, name):
-    if not t.is_cuda or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous CUDA vector of {n} elements")
-    return t.data_ptr()
+def _codes():
+    """Codes of the floating types, by torch dtype."""
+    _torch()
+    if _DTYPE_CODES is None:
+        _dtype_code(_torch().empty(0))
+    return _DTYPE_CODES
 
 
-def _like(t, x, name):
-    """Row pitch of a matrix of x's shape and type."""
-    if t.shape != x.shape:
-        raise ValueError(f"{name} must have the shape {tuple(x.shape)}, not {tuple(t.shape)}")
-    if t.dtype != x.dtype:
-        raise TypeError(f"{name} must be {x.dtype}, not {t.dtype}")
-    return _rows2(t, name)
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _RAW_STREAM is None:
+        _stream_handle(None)
+    return _RAW_STREAM()
+
+
+def _workspace_args(workspace):
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _blocks(n):
     return (n + SCALE_BLOCK - 1) // SCALE_BLOCK
 
 
-def _scale_strides(s, shape, name):
-    if s.shape != shape or s.dtype != _torch().float32 or not s.is_cuda:
-        raise ValueError(f"{name} must be a float32 CUDA tensor of shape {shape}")
-    return s.stride()
+def _refuse(*rules):
+    """Raises for the first (name, tensor, shape, dtype) that is not a CUDA tensor
+    of that shape and type with unit stride in its last dimension (shape:
+    any where None; dtype: a type or several)."""
+    for name, t, shape, dtype in rules:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have unit stride in its last dimension")
+        kinds = dtype if isinstance(dtype, (tuple, set)) else (dtype,)
+        if t.dtype not in kinds:
+            raise TypeError(f"{name} must be {' or '.join(sorted(map(str, kinds)))}, not {t.dtype}")
+    raise ValueError("unsupported arguments")
 
 
-def _empty_fp8(torch, lead, cols, device):
-    """e4m3 rows whose pitch is whole 16-byte pieces, as the products need."""
-    if cols % 16 == 0:
-        return torch.empty((*lead, cols), dtype=torch.float8_e4m3fn, device=device)
-    pitch = (cols + 15) // 16 * 16
-    return torch.empty((*lead, pitch), dtype=torch.float8_e4m3fn, device=device)[..., :cols]
+def _matrix(t, name):
+    """Shape and strides of a matrix; the pitch of a single row, which nothing
+    uses, as whole 16-byte pieces."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix")
+    rows, cols = shape
+    ld, unit = t.stride()
+    return rows, cols, (ld if rows > 1 else (cols + 15) // 16 * 16), (1 if cols <= 1 else unit)
 
 
-def _residual_args(torch, x, residual, h_out):
-    """(h, pointers and pitches of the residual and of h)."""
-    if residual is None:
-        return x, None, 0, None, 0
-    ldr = _like(residual, x, "residual")
-    if h_out is None:
-        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        return h, residual.data_ptr(), ldr, h.data_ptr(), x.shape[1]
-    return h_out, residual.data_ptr(), ldr, h_out.data_ptr(), _like(h_out, x, "h_out")
+def _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, fp8):
+    torch = _TORCH or _torch()
+    codes = _DTYPE_CODES or _codes()
+    rows, cols, ldx, unit = _matrix(x, "x")
+    shape, dtype, device = x.shape, x.dtype, x.device
+    code, wcode = codes.get(dtype), codes.get(weight.dtype)
+    given = out is not None
+    if given:
+        _, _, ldy, uy = _matrix(out, "out")
+    elif fp8:
+        ldy = (cols + 15) // 16 * 16          # whole 16-byte pieces, as the products need
+        out = torch.empty((rows, ldy), dtype=torch.float8_e4m3fn, device=device)
+        if ldy != cols:
+            out = out[:, :cols]
+    else:
+        out, ldy = torch.empty(shape, dtype=dtype, device=device), cols
+    ps = sr = sb = 0
+    if fp8:
+        nb = (cols + 127) // 128
+        if scales is None:
+            sr, sb = 1, rows or 1             # stored block by block: the products' fastest order
+            scales = torch.empty_strided((rows, nb), (sr, sb), dtype=torch.float32, device=device)
+        else:
+            if scales.shape != (rows, nb) or scales.dtype != torch.float32 or not scales.is_cuda:
+                raise ValueError(f"scales must be a float32 CUDA tensor of shape {(rows, nb)}")
+            sr, sb = scales.stride()
+        ps = scales.data_ptr()
+    h, pr, ldr, ph, ldh, ok = x, 0, 0, 0, 0, True
+    if residual is not None:
+        _, _, ldr, ur = _matrix(residual, "residual")
+        ok = ur == 1 and residual.shape == shape and residual.dtype == dtype and residual.is_cuda
+        if h_out is None:
+            h, ldh = torch.empty(shape, dtype=dtype, device=device), cols
+        else:
+            h = h_out
+            _, _, ldh, uh = _matrix(h, "h_out")
+            ok = ok and uh == 1 and h.shape == shape and h.dtype == dtype and h.is_cuda
+        pr, ph = residual.data_ptr(), h.data_ptr()
+    if given:
+        ok = ok and uy == 1 and out.shape == shape and out.is_cuda and \
+            out.dtype == (torch.float8_e4m3fn if fp8 else dtype)
+    if not (ok and unit == 1 and x.is_cuda and weight.is_cuda and code is not None and
+            wcode is not None and weight.shape == (cols,) and (cols == 1 or weight.stride(0) == 1)):
+        _refuse(("x", x, None, set(codes)), ("weight", weight, (cols,), set(codes)),
+                ("residual", residual, shape, dtype),
+                ("h_out", h_out, shape, dtype),
+                ("out", out if given else None, shape, torch.float8_e4m3fn if fp8 else dtype))
+    d = _NORM.pack(rows, cols, x.data_ptr(), pr, weight.data_ptr(), ph, out.data_ptr(), ps, ldx, ldr,
+                   ldh, ldy, sr, sb, eps, code, wcode, _abi.E4M3 if fp8 else code)
+    _check(load().tiles_rmsnorm(d, _raw_stream(stream)), "tiles_rmsnorm")
+    return out, scales, h
 
 
 def rmsnorm(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=None):
     """h = x + residual and y = h * (mean(h^2) + eps)^(-1/2) * weight, row by
     row of a matrix; returns (y, h) in x's type.  Without a residual h is x
     itself.  h_out may be the residual (updated in place)."""
-    torch = _torch()
-    ldx = _rows2(x, "x")
-    rows, cols = x.shape
-    code = _dtype_code(x)
-    if out is None:
-        out, ldy = torch.empty(x.shape, dtype=x.dtype, device=x.device), cols
-    else:
-        ldy = _like(out, x, "out")
-    h, pr, ldr, ph, ldh = _residual_args(torch, x, residual, h_out)
-    d = _abi.RmsnormDesc(rows, cols, x.data_ptr(), pr, _vector(weight, cols, "weight"), ph,
-                         out.data_ptr(), None, ldx, ldr, ldh, ldy, 0, 0, eps, code,
-                         _dtype_code(weight), code)
-    _check(load().tiles_rmsnorm(C.byref(d), _stream_handle(stream)), "tiles_rmsnorm")
-    return out, h
+    y, _, h = _rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
+    return y, h
 
 
 def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out=None,
@@ -608,29 +655,7 @@ def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out
     values and one fp32 scale per row and 128 columns, y ~ q * scale.  New
     scales are stored block by block (a transposed view, rows x blocks),
     which the products read fastest."""
-    torch = _torch()
-    ldx = _rows2(x, "x")
-    rows, cols = x.shape
-    nb = (cols + SCALE_BLOCK - 1) // SCALE_BLOCK
-    if out is None:
-        out = _empty_fp8(torch, (rows,), cols, x.device)
-        ldy = (cols + 15) // 16 * 16
-    else:
-        if out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
-            raise ValueError("out must be float8_e4m3fn of x's shape")
-        ldy = _rows2(out, "out")
-    if scales is None:
-        scales = torch.empty_strided((rows, nb), (1, max(rows, 1)), dtype=torch.float32,
-                                     device=x.device)
-        sr, sb = 1, rows
-    else:
-        sr, sb = _scale_strides(scales, (rows, nb), "scales")
-    h, pr, ldr, ph, ldh = _residual_args(torch, x, residual, h_out)
-    d = _abi.RmsnormDesc(rows, cols, x.data_ptr(), pr, _vector(weight, cols, "weight"), ph,
-                         out.data_ptr(), scales.data_ptr(), ldx, ldr, ldh, ldy, sr, sb, eps,
-                         _dtype_code(x), _dtype_code(weight), _abi.E4M3)
-    _check(load().tiles_rmsnorm(C.byref(d), _stream_handle(stream)), "tiles_rmsnorm")
-    return out, scales, h
+    return _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, True)
 
 
 def rmsnorm_grad_workspace(x):
@@ -648,34 +673,41 @@ def rmsnorm_grad(dy, h, weight, eps=1e-6, dh=None, dx_out=None, dweight_out=None
     """Gradients of rmsnorm at h, given those of y (dy) and, where h is used
     past the norm, of h (dh): returns (dx, dweight).  dx, in h's type, is the
     gradient of x and of the residual alike; dweight is fp32."""
-    torch = _torch()
-    ldh = _rows2(h, "h")
-    rows, cols = h.shape
-    lddy = _like(dy, h, "dy")
-    lddh = _like(dh, h, "dh") if dh is not None else 0
-    if dx_out is None:
-        dx_out, lddx = torch.empty(h.shape, dtype=h.dtype, device=h.device), cols
+    torch = _TORCH or _torch()
+    codes = _DTYPE_CODES or _codes()
+    rows, cols, ldh, unit = _matrix(h, "h")
+    shape, dtype = h.shape, h.dtype
+    code, wcode = codes.get(dtype), codes.get(weight.dtype)
+    _, _, lddy, ud = _matrix(dy, "dy")
+    lddh = pdh = 0
+    ok = True
+    if dh is not None:
+        _, _, lddh, u = _matrix(dh, "dh")
+        ok = u == 1 and dh.shape == shape and dh.dtype == dtype and dh.is_cuda
+        pdh = dh.data_ptr()
+    dx, dw = dx_out, dweight_out
+    if dx is None:
+        dx, lddx = torch.empty(shape, dtype=dtype, device=h.device), cols
     else:
-        lddx = _like(dx_out, h, "dx_out")
-    if dweight_out is None:
-        dweight_out = torch.empty(cols, dtype=torch.float32, device=h.device)
-    elif dweight_out.dtype != torch.float32:
-        raise TypeError("dweight_out must be float32")
-    d = _abi.RmsnormGradDesc(rows, cols, dy.data_ptr(), h.data_ptr(),
-                             _vector(weight, cols, "weight"),
-                             dh.data_ptr() if dh is not None else None, dx_out.data_ptr(),
-                             _vector(dweight_out, cols, "dweight_out"), lddy, ldh, lddh, lddx, eps,
-                             _dtype_code(h), _dtype_code(weight), 0)
+        _, _, lddx, u = _matrix(dx, "dx_out")
+        ok = ok and u == 1 and dx.shape == shape and dx.dtype == dtype and dx.is_cuda
+    if dw is None:
+        dw = torch.empty(cols, dtype=torch.float32, device=h.device)
+    else:
+        ok = ok and dw.shape == (cols,) and dw.dtype == torch.float32 and dw.is_cuda and \
+            (cols == 1 or dw.stride(0) == 1)
+    if not (ok and unit == 1 and ud == 1 and h.is_cuda and dy.is_cuda and weight.is_cuda and
+            code is not None and wcode is not None and dy.shape == shape and dy.dtype == dtype and
+            weight.shape == (cols,) and (cols == 1 or weight.stride(0) == 1)):
+        _refuse(("h", h, None, set(codes)), ("dy", dy, shape, dtype),
+                ("weight", weight, (cols,), set(codes)), ("dh", dh, shape, dtype),
+                ("dx_out", dx_out, shape, dtype),
+                ("dweight_out", dweight_out, (cols,), torch.float32))
+    d = _NORM_GRAD.pack(rows, cols, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), pdh,
+                        dx.data_ptr(), dw.data_ptr(), lddy, ldh, lddh, lddx, eps, code, wcode, 0)
     ws, wsb = _workspace_args(workspace)
-    _check(load().tiles_rmsnorm_grad(C.byref(d), ws, wsb, _stream_handle(stream)),
-           "tiles_rmsnorm_grad")
-    return dx_out, dweight_out
-
-
-def _workspace_args(workspace):
-    if workspace is None:
-        return None, 0
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load().tiles_rmsnorm_grad(d, ws, wsb, _raw_stream(stream)), "tiles_rmsnorm_grad")
+    return dx, dw
 
 
 def quantize_fp8(x, block_rows=1, stream=None):
@@ -692,7 +724,8 @@ def quantize_fp8(x, block_rows=1, stream=None):
         raise ValueError("block_rows must be 1 or 128")
     *lead, rows, cols = x.shape
     batch = lead[0] if lead else 1
-    q = _empty_fp8(torch, (*lead, rows), cols, x.device)
+    pitch = (cols + 15) // 16 * 16
+    q = torch.empty((*lead, rows, pitch), dtype=torch.float8_e4m3fn, device=x.device)[..., :cols]
     nb = _blocks(cols)
     if block_rows == 1:
         scales = torch.empty((*lead, nb, rows), dtype=torch.float32,
@@ -701,70 +734,78 @@ def quantize_fp8(x, block_rows=1, stream=None):
         scales = torch.empty((*lead, _blocks(rows), nb), dtype=torch.float32, device=x.device)
     d = _abi.QuantizeDesc(batch, rows, cols, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
                           x.stride(-2) if rows > 1 else max(x.stride(-2), cols),
-                          x.stride(0) if lead else 0, max(q.stride(-2), cols),
-                          q.stride(0) if lead else 0, scales.stride(-2), scales.stride(-1),
-                          scales.stride(0) if lead else 0, _dtype_code(x), block_rows)
+                          x.stride(0) if lead else 0, pitch, q.stride(0) if lead else 0,
+                          scales.stride(-2), scales.stride(-1), scales.stride(0) if lead else 0,
+                          _dtype_code(x), block_rows)
     _check(load().tiles_quantize_fp8(C.byref(d), _stream_handle(stream)), "tiles_quantize_fp8")
     return q, scales
 
 
-def _out_rows(out, rows, cols, out_dtype, like):
-    """The output matrix (new, or the caller's, checked) and its row pitch."""
-    if out is None:
-        return _alloc_out((rows, cols), like, out_dtype), cols
-    if out.shape != (rows, cols):
-        raise ValueError(f"out must have the shape {(rows, cols)}")
-    return out, _rows2(out, "out")
-
-
-def _weight(b, grouped, name="b"):
-    """Row pitch and group stride of a weight (grouped: 3-D)."""
-    if b.dim() != (3 if grouped else 2):
+def _weight(b, grouped, name):
+    """Shape (..., rows, cols), row pitch, group stride and unit stride of a weight."""
+    shape, st = b.shape, b.stride()
+    if len(shape) != (3 if grouped else 2):
         raise ValueError(f"{name} must have {3 if grouped else 2} dimensions")
-    st, shape = b.stride(), b.shape
-    if not b.is_cuda or (st[-1] != 1 and shape[-1] > 1):
-        raise ValueError(f"{name} must be a CUDA tensor with unit stride in its last dimension")
-    ld = st[-2] if shape[-2] > 1 else (shape[-1] + 15) // 16 * 16
-    return ld, st[0] if grouped else 0
-
-
-def _offsets(offsets, groups):
-    if offsets.dtype != _torch().int32 or not offsets.is_cuda or \
-            offsets.shape != (groups + 1,) or offsets.stride(0) != 1:
-        raise ValueError(f"offsets must be a contiguous int32 CUDA vector of {groups + 1} elements")
-    return offsets.data_ptr()
+    cols = shape[-1]
+    ld = st[-2] if shape[-2] > 1 else (cols + 15) // 16 * 16
+    return shape, ld, (st[0] if grouped else 0), (1 if cols <= 1 else st[-1])
 
 
 def _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype, workspace, stream, where):
-    fp8 = _torch().float8_e4m3fn
+    torch = _TORCH or _torch()
+    codes = _DTYPE_CODES or _codes()
     grouped = offsets is not None
-    lda = _rows2(a, "a")
-    ldb, stride_b = _weight(b, grouped)
-    m, k = a.shape
-    n = b.shape[-2]
-    if a.dtype != fp8 or b.dtype != fp8:
-        raise TypeError("a and b must be float8_e4m3fn")
-    if b.shape[-1] != k:
-        raise ValueError(f"shape mismatch: {tuple(a.shape)} x {tuple(b.shape)}^T")
-    kb, nb = _blocks(k), _blocks(n)
-    sar, sab = _scale_strides(a_scales, (m, kb), "a_scales")
+    m, k, lda, ua = _matrix(a, "a")
+    bshape, ldb, stride_b, ub = _weight(b, grouped, "b")
+    n = bshape[-2]
+    kb, nb = (k + 127) // 128, (n + 127) // 128
+    sbs = b_scales.stride()
     if grouped:
-        groups = b.shape[0]
-        sbg, sbr, sbb = _scale_strides(b_scales, (groups, nb, kb), "b_scales")
-        off, fn = _offsets(offsets, groups), load().tiles_grouped_gemm
+        groups = bshape[0]
+        scales_shape, sbg, off = (groups, nb, kb), sbs[0], offsets.data_ptr()
+        ok = offsets.shape == (groups + 1,) and offsets.dtype == torch.int32 and \
+            offsets.is_cuda and offsets.stride(0) == 1
     else:
-        groups = sbg = 0
-        sbr, sbb = _scale_strides(b_scales, (nb, kb), "b_scales")
-        off, fn = None, load().tiles_gemm_fp8
-    if out is None and out_dtype is None:
-        out_dtype = "bf16"
-    out, ldc = _out_rows(out, m, n, out_dtype, a)
-    d = _abi.ProductDesc(m, n, k, groups, off, a.data_ptr(), b.data_ptr(), out.data_ptr(),
-                         a_scales.data_ptr(), b_scales.data_ptr(), lda, ldb, ldc, stride_b, sar,
-                         sab, sbr, sbb, sbg, _abi.E4M3, _dtype_code(out), _abi.B_NK, 0)
+        groups = sbg = off = 0
+        scales_shape, ok = (nb, kb), True
+    given = out is not None
+    if given:
+        _, _, ldc, u = _matrix(out, "out")
+        ok = ok and u == 1 and out.shape == (m, n) and out.is_cuda and out.dtype in codes
+    else:
+        dt = out_dtype if isinstance(out_dtype, torch.dtype) else \
+            _TYPES(torch)["bf16" if out_dtype is None else out_dtype]
+        out, ldc = torch.empty((m, n), dtype=dt, device=a.device), n
+    fp8 = torch.float8_e4m3fn
+    if not (ok and ua == 1 and ub == 1 and a.dtype == fp8 and b.dtype == fp8 and a.is_cuda and
+            b.is_cuda and bshape[-1] == k and a_scales.shape == (m, kb) and
+            b_scales.shape == scales_shape and a_scales.dtype == torch.float32 and
+            b_scales.dtype == torch.float32 and a_scales.is_cuda and b_scales.is_cuda):
+        for s, shape, name in ((a_scales, (m, kb), "a_scales"), (b_scales, scales_shape, "b_scales")):
+            if s.shape != shape or s.dtype != torch.float32 or not s.is_cuda:
+                raise ValueError(f"{name} must be a float32 CUDA tensor of shape {shape}")
+        _refuse(("a", a, None, fp8), ("b", b, (*bshape[:-1], k), fp8),
+                ("offsets", offsets, (groups + 1,), torch.int32),
+                ("out", out if given else None, (m, n), set(codes)))
+    sar, sab = a_scales.stride()
+    d = _PRODUCT.pack(m, n, k, groups, off, a.data_ptr(), b.data_ptr(), out.data_ptr(),
+                      a_scales.data_ptr(), b_scales.data_ptr(), lda, ldb, ldc, stride_b, sar, sab,
+                      sbs[-2], sbs[-1], sbg, _abi.E4M3, codes[out.dtype], _abi.B_NK, 0)
     ws, wsb = _workspace_args(workspace)
-    _check(fn(C.byref(d), ws, wsb, _stream_handle(stream)), where)
+    fn = load().tiles_grouped_gemm if grouped else load().tiles_gemm_fp8
+    _check(fn(d, ws, wsb, _raw_stream(stream)), where)
     return out
+
+
+_TYPE_NAMES = None
+
+
+def _TYPES(torch):
+    """Types by the names that out_dtype takes."""
+    global _TYPE_NAMES
+    if _TYPE_NAMES is None:
+        _TYPE_NAMES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+    return _TYPE_NAMES
 
 
 def gemm_fp8(a, a_scales, b, b_scales, out=None, out_dtype=None, workspace=None, stream=None):
@@ -793,22 +834,34 @@ def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspa
     is the gradient of the rows when a is that of the products.  offsets is
     an int32 CUDA vector that only the kernel reads.  Rows outside every
     group are not written."""
-    lda = _rows2(a, "a")
-    ldb, stride_b = _weight(b, True)
-    m, k = a.shape
-    groups, bk, n = (b.shape[0], b.shape[2], b.shape[1]) if trans_b else b.shape
-    if bk != k:
-        raise ValueError(f"shape mismatch: {tuple(a.shape)} x {tuple(b.shape)}"
-                         f"{'^T' if trans_b else ''}")
-    if b.dtype != a.dtype:
-        raise TypeError("a and b must share a dtype")
-    out, ldc = _out_rows(out, m, n, out_dtype, a)
-    d = _abi.ProductDesc(m, n, k, groups, _offsets(offsets, groups), a.data_ptr(), b.data_ptr(),
-                         out.data_ptr(), None, None, lda, ldb, ldc, stride_b, 0, 0, 0, 0, 0,
-                         _dtype_code(a), _dtype_code(out), _abi.B_NK if trans_b else _abi.B_KN, 0)
+    torch = _TORCH or _torch()
+    codes = _DTYPE_CODES or _codes()
+    m, k, lda, ua = _matrix(a, "a")
+    bshape, ldb, stride_b, ub = _weight(b, True, "b")
+    groups, bk, n = (bshape[0], bshape[2], bshape[1]) if trans_b else bshape
+    dtype = a.dtype
+    given, ok = out is not None, True
+    if given:
+        _, _, ldc, u = _matrix(out, "out")
+        ok = u == 1 and out.shape == (m, n) and out.is_cuda and out.dtype in codes
+    else:
+        dt = dtype if out_dtype is None else \
+            out_dtype if isinstance(out_dtype, torch.dtype) else _TYPES(torch)[out_dtype]
+        out, ldc = torch.empty((m, n), dtype=dt, device=a.device), n
+    if not (ok and ua == 1 and ub == 1 and bk == k and b.dtype == dtype and dtype in codes and
+            a.is_cuda and b.is_cuda and offsets.shape == (groups + 1,) and offsets.is_cuda and
+            offsets.dtype == torch.int32 and offsets.stride(0) == 1):
+        if offsets.dtype != torch.int32:
+            raise ValueError("offsets must be int32")
+        _refuse(("a", a, None, set(codes)),
+                ("b", b, (groups, n, k) if trans_b else (groups, k, n), dtype),
+                ("offsets", offsets, (groups + 1,), torch.int32),
+                ("out", out if given else None, (m, n), set(codes)))
+    d = _PRODUCT.pack(m, n, k, groups, offsets.data_ptr(), a.data_ptr(), b.data_ptr(),
+                      out.data_ptr(), 0, 0, lda, ldb, ldc, stride_b, 0, 0, 0, 0, 0, codes[dtype],
+                      codes[out.dtype], _abi.B_NK if trans_b else _abi.B_KN, 0)
     ws, wsb = _workspace_args(workspace)
-    _check(load().tiles_grouped_gemm(C.byref(d), ws, wsb, _stream_handle(stream)),
-           "tiles_grouped_gemm")
+    _check(load().tiles_grouped_gemm(d, ws, wsb, _raw_stream(stream)), "tiles_grouped_gemm")
     return out
 
 
@@ -816,23 +869,29 @@ def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stre
     """out[g] = a_g^T @ dc_g over the rows of group g: the weight gradients
     (groups x k x n) of out = grouped_gemm(a, w, offsets), given dc.  An
     empty group's gradient is zero."""
-    lda, lddc = _rows2(a, "a"), _rows2(dc, "dc")
-    m, k = a.shape
-    n = dc.shape[1]
-    if dc.shape[0] != m:
-        raise ValueError("a and dc must have the same rows")
-    if dc.dtype != a.dtype:
-        raise TypeError("a and dc must share a dtype")
+    torch = _TORCH or _torch()
+    codes = _DTYPE_CODES or _codes()
+    m, k, lda, ua = _matrix(a, "a")
+    md, n, lddc, ud = _matrix(dc, "dc")
+    dtype = a.dtype
     groups = offsets.shape[0] - 1
-    if out is None:
-        out, ldw, stride_dw = _alloc_out((groups, k, n), a, out_dtype), n, k * n
+    given, ok = out is not None, True
+    if given:
+        oshape, ldw, stride_dw, u = _weight(out, True, "out")
+        ok = u == 1 and oshape == (groups, k, n) and out.is_cuda and out.dtype in codes
     else:
-        if out.shape != (groups, k, n):
-            raise ValueError(f"out must have the shape {(groups, k, n)}")
-        ldw, stride_dw = _weight(out, True, "out")
-    d = _abi.WgradDesc(m, k, n, groups, _offsets(offsets, groups), a.data_ptr(), dc.data_ptr(),
-                       out.data_ptr(), lda, lddc, ldw, stride_dw, _dtype_code(a), _dtype_code(out))
+        dt = dtype if out_dtype is None else \
+            out_dtype if isinstance(out_dtype, torch.dtype) else _TYPES(torch)[out_dtype]
+        out = torch.empty((groups, k, n), dtype=dt, device=a.device)
+        ldw, stride_dw = n, k * n
+    if not (ok and ua == 1 and ud == 1 and md == m and dc.dtype == dtype and dtype in codes and
+            a.is_cuda and dc.is_cuda and offsets.is_cuda and offsets.dtype == torch.int32 and
+            offsets.dim() == 1 and offsets.stride(0) == 1):
+        _refuse(("a", a, None, set(codes)), ("dc", dc, (m, n), dtype),
+                ("offsets", offsets, (groups + 1,), torch.int32),
+                ("out", out if given else None, (groups, k, n), set(codes)))
+    d = _WGRAD.pack(m, k, n, groups, offsets.data_ptr(), a.data_ptr(), dc.data_ptr(),
+                    out.data_ptr(), lda, lddc, ldw, stride_dw, codes[dtype], codes[out.dtype])
     ws, wsb = _workspace_args(workspace)
-    _check(load().tiles_grouped_wgrad(C.byref(d), ws, wsb, _stream_handle(stream)),
-           "tiles_grouped_wgrad")
+    _check(load().tiles_grouped_wgrad(d, ws, wsb, _raw_stream(stream)), "tiles_grouped_wgrad")
     return out

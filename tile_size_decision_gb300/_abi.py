@@ -221,14 +221,15 @@ SIGNATURES = {
     "tiles_check": (C.c_int, [C.c_void_p, C.c_void_p]),
     "tiles_selftest_wait_timeout": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p]),
     "tiles_selftest_drop_stage": (C.c_int, [C.c_int, C.c_int64]),
-    "tiles_rmsnorm": (C.c_int, [C.POINTER(RmsnormDesc), C.c_void_p]),
+    # The descriptors of the calls below go by address: a structure (byref), or
+    # its bytes as the binding packs them.
+    "tiles_rmsnorm": (C.c_int, [C.c_void_p, C.c_void_p]),
     "tiles_rmsnorm_grad_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
-    "tiles_rmsnorm_grad": (C.c_int, [C.POINTER(RmsnormGradDesc), C.c_void_p, C.c_size_t,
-                                     C.c_void_p]),
-    "tiles_quantize_fp8": (C.c_int, [C.POINTER(QuantizeDesc), C.c_void_p]),
-    "tiles_gemm_fp8": (C.c_int, [C.POINTER(ProductDesc), C.c_void_p, C.c_size_t, C.c_void_p]),
-    "tiles_grouped_gemm": (C.c_int, [C.POINTER(ProductDesc), C.c_void_p, C.c_size_t, C.c_void_p]),
-    "tiles_grouped_wgrad": (C.c_int, [C.POINTER(WgradDesc), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_rmsnorm_grad": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_quantize_fp8": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "tiles_gemm_fp8": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_grouped_gemm": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_grouped_wgrad": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 _lib = None
