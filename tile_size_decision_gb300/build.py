@@ -51,6 +51,7 @@ def units():
         ("pair_sm103a.cu", "pair_sm103a.o", []),
         ("pair8_sm103a.cu", "pair8_sm103a.o", []),
         ("product_api.cu", "product_api.o", []),
+        ("launch_util.cu", "launch_util.o", []),
     ]
     for bn, cg in GEMM_VARIANTS:
         out.append(("gemm_sm103a.cu", f"gemm_bn{bn}_cg{cg}.o",

@@ -12,7 +12,7 @@
 #include <algorithm>
 
 #include "launch_util.h"
-#include "sm103_ptx.cuh"
+#include "op_ptx.cuh"
 #include "tiles_internal.h"
 
 namespace tiles {

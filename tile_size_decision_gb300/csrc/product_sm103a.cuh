@@ -8,6 +8,7 @@
 
 #include "gemm_sm103a.cuh"
 #include "launch_util.h"
+#include "op_ptx.cuh"
 
 namespace tiles {
 
