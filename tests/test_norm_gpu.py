@@ -128,6 +128,24 @@ def test_norm_of_zeros_infinities_and_nans():
     assert_fp8(q[3:], s[3:], y64)
 
 
+@pytest.mark.parametrize("rows,cols", [(4, 512), (700, 512), (700, 1024)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_of_quiet_rows_with_blocks_of_zeros(rows, cols, residual):
+    # 1 / sqrt(mean + eps) is 1000 here and a block of zeros has the smallest
+    # scale: their quotient is past fp32, the values are not.
+    x = draw((rows, cols), "bf16", 13, 1e-4)
+    x[:, 128:256] = 0
+    x[1] = 0
+    x[2, :128] = 2.0 ** -130
+    r = torch.zeros_like(x) if residual else None
+    w = draw((1, cols), "bf16", 14)[0]
+    q, s, _ = T.rmsnorm_fp8(x, w, residual=r)
+    y64, _ = OO.rmsnorm(f64(x), f64(w))
+    assert bool((q[:, 128:256].float() == 0).all()) and bool((s[:, 1] == OO.TINY_SCALE).all())
+    assert bool(q.float().isfinite().all())
+    assert_fp8(q, s, y64)
+
+
 def test_norm_of_no_rows_and_of_another_stream():
     w = torch.ones(64, dtype=torch.float16, device="cuda")
     y, h = T.rmsnorm(torch.empty((0, 64), dtype=torch.float16, device="cuda"), w)

@@ -367,20 +367,21 @@ __global__ void __launch_bounds__(kMaxThreads)
 }
 
 // The same with the rows' pieces 16-byte aligned: the block takes rows
-// blockIdx.x, + gridDim.x, ... (times blockDim.y), the next two of them on
-// their way in while one is worked on.
+// blockIdx.x, + gridDim.x, ..., the next two of them on their way in while one
+// is worked on.  DRAM bounds it: 16384 x 4096 bf16 rows with a residual, to
+// e4m3, 73.8 us, 94% of the measured copy bandwidth; without a residual the
+// work per byte does (11127 x 2728, 24.2 us, 56%).
 template <typename T, int VPT, bool FP8, bool RES>
 __global__ void __launch_bounds__(kRingThreads)
     rmsnorm_ring_kernel(const NormArgs a) {
     extern __shared__ uint4 ring_smem[];
     __shared__ float slots[64];
-    const int threads = blockDim.x * blockDim.y;
-    RowRing<T, RES ? 2 : 1, VPT> ring{ring_smem + threadIdx.y * blockDim.x + threadIdx.x};
+    const int threads = blockDim.x;
+    RowRing<T, RES ? 2 : 1, VPT> ring{ring_smem + threadIdx.x};
     const int step = blockDim.x * 8, tid = threadIdx.x, cols = static_cast<int>(a.cols);
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t stride = gridDim.x, row0 = blockIdx.x;
     auto fetch = [&](int64_t row, int slot) {
         if (row < a.rows) {
             ring.copy(slot, 0, static_cast<const T*>(a.x) + row * a.ldx, step, tid, threads, cols);
@@ -432,6 +433,11 @@ __global__ void __launch_bounds__(kRingThreads)
             if constexpr (FP8) {
                 s = block_scale(amax[j] * rstd);
                 factor = rstd * reciprocal(s);
+                if (isinf(factor)) {   // a quiet row over the smallest scale: in two steps
+                    factor = reciprocal(s);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] *= rstd;
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[j][i] *= factor;
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(512, 2)
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) 
+                for (int i = 0; i < 8; ++i)
                     dw[j][i] += side[y * (VPT * 256) + (j * 8 + i) * 32 + threadIdx.x];
     }
     float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
@@ -572,7 +578,9 @@ __global__ void __launch_bounds__(512, 2)
 }
 
 // The same with the rows' pieces 16-byte aligned and the whole row in one
-// block (gridDim.y == 1), the next two rows on their way in.
+// block (gridDim.y == 1), the next two rows on their way in.  DRAM bounds it:
+// 8192 x 4096 bf16 rows with dh 45.4 us, 87% of the measured copy bandwidth,
+// the reduction's launch included.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(512)
     rmsnorm_grad_ring_kernel(const GradArgs a) {
@@ -656,7 +664,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) 
+                for (int i = 0; i < 8; ++i)
                     side[(threadIdx.y - 1) * (VPT * 256) + (j * 8 + i) * 32 + tid] = dw[j][i];
         __syncthreads();
         if (threadIdx.y > 0) return;
@@ -664,7 +672,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) 
+                for (int i = 0; i < 8; ++i)
                     dw[j][i] += side[y * (VPT * 256) + (j * 8 + i) * 32 + tid];
     }
     float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
@@ -808,7 +816,7 @@ int launch_norm_ring(const NormArgs& a, int threads, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return static_cast<int>(e);
     // Blocks an SM: as many as it holds, but where residual rows stream through
     // DRAM only 512 threads, whose copies in flight saturate it with fewer
-    // rows open at once: 16384 x 4096 bf16 rows (470 MB) 71.5 us against 85.9,
+    // rows open at once: 16384 x 4096 bf16 rows (470 MB) 73.8 us against 85.9,
     // 8000 x 8192 69.9 against 82.0, while 16384 x 1024 (117 MB, an L2's worth)
     // takes 18.9 us against 17.7.
     const bool stream = RES && a.rows * a.cols * static_cast<int64_t>(3 * sizeof(T) + 1) > (160ll << 20);
@@ -822,8 +830,8 @@ int launch_norm_ring(const NormArgs& a, int threads, int sms, cudaStream_t st) {
 template <typename T, bool VEC, bool FP8>
 int launch_norm(const NormArgs& a, cudaStream_t st) {
     const int64_t vectors = (a.cols + 7) / 8;
-    // One 8-element vector a thread for as long as a block can hold the row: a row's
-    // loads are then all in flight at once.
+    // One vector a thread for as long as a block can hold the row: a row's loads
+    // are then all in flight at once.
     int vpt = 1;
     while (vpt <= 4 && (vectors + vpt - 1) / vpt > kMaxThreads) vpt *= 2;
     if (vpt > 4) {
@@ -893,15 +901,18 @@ size_t grad_bytes(int64_t rows, int64_t cols, int sms) {
 template <typename T>
 int launch_grad(const GradArgs& a, bool vec, int sms, int* parts, cudaStream_t st) {
     GradGeometry g = grad_geometry(a.rows, a.cols, sms, true);
-    size_t smem = RowRing<T, 3, kGradVpt>::bytes(g.threads * g.per_block);
+    const size_t smem = RowRing<T, 3, kGradVpt>::bytes(g.threads * g.per_block);
     if (vec && g.spans == 1 && smem <= kRingBytesMost) {
         static std::atomic<uint64_t> opted{0};
         const cudaError_t e =
             opt_in_smem(rmsnorm_grad_ring_kernel<T, kGradVpt>, kRingBytesMost, &opted);
         if (e != cudaSuccess) return static_cast<int>(e);
-        *parts = g.blocks;
-        return launch(rmsnorm_grad_ring_kernel<T, kGradVpt>, dim3(g.blocks),
-                      dim3(g.threads, g.per_block), std::max(smem, exact_smem(g.per_sm)), st, a);
+        // fp32 rows take twice the shared memory: fewer blocks then.
+        const int per_sm = std::max(
+            1, std::min(g.per_sm, static_cast<int>(220 * 1024 / (smem + 1024))));
+        *parts = std::min(g.blocks, sms * per_sm);
+        return launch(rmsnorm_grad_ring_kernel<T, kGradVpt>, dim3(*parts),
+                      dim3(g.threads, g.per_block), std::max(smem, exact_smem(per_sm)), st, a);
     }
     g = grad_geometry(a.rows, a.cols, sms, false);
     *parts = g.blocks;
