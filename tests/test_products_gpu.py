@@ -359,3 +359,206 @@ def test_python_refusals(ws):
         T.grouped_gemm(draw((4, 64), "bf16", 98, pitch=66), w, off, workspace=ws)
     with pytest.raises(ValueError):
         T.grouped_wgrad(a, a[:3], off, workspace=ws)
+
+
+# ---- sizes that take the large tiles -----------------------------------------------------
+# (Enough rows that the large-tile kernels are chosen; the float64 products are
+# made on the device.)
+
+
+def dev_fp8(a8, sa, b8, sb):
+    """(product, sum of magnitudes) of one weight in float64, on the device."""
+    ref = torch.zeros((a8.shape[0], b8.shape[0]), dtype=torch.float64, device="cuda")
+    bound = torch.zeros_like(ref)
+    for t in range(sa.shape[1]):
+        part = slice(128 * t, min(128 * (t + 1), a8.shape[1]))
+        s = sa[:, t].double()[:, None] * sb[:, t].double().repeat_interleave(128)[: b8.shape[0]]
+        x, w = a8[:, part].double(), b8[:, part].double()
+        ref += s * (x @ w.t())
+        bound += s.abs() * (x.abs() @ w.abs().t())
+    return ref, bound
+
+
+def dev_grouped(a, w, off, trans_b):
+    n = w.shape[1] if trans_b else w.shape[2]
+    ref = torch.zeros((a.shape[0], n), dtype=torch.float64, device="cuda")
+    bound = torch.zeros_like(ref)
+    for e, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        x, b = a[lo:hi].double(), (w[e].t() if trans_b else w[e]).double()
+        ref[lo:hi], bound[lo:hi] = x @ b, x.abs() @ b.abs()
+    return ref, bound
+
+
+def assert_close_dev(got, ref, bound, dtype, rel):
+    assert_close(got, f64(ref), f64(bound), dtype, rel)
+
+
+LARGE_DENSE = [(3000, 2050, 1040), (20000, 130, 528), (1100, 4100, 2064)]
+
+
+@pytest.mark.parametrize("out,shift", [("bf16", 0), ("f16", 0), ("f32", 0), ("f32", 3), ("bf16", 1)])
+@pytest.mark.parametrize("shape", LARGE_DENSE, ids=str)
+def test_dense_8bit_large_tiles(ws, shape, out, shift):
+    # `shift`: the result starts off a 16-byte boundary (it cannot leave in boxes).
+    m, n, k = shape
+    a8, sa, b8, sb = fp8_operands(m, n, k, 17)
+    sa = sa.clone()
+    sa[m - 2, 1] = float("nan")
+    full = torch.full((m + 2, (n + 23) // 8 * 8), 5.0, dtype=DT[out], device="cuda")
+    got = full[1:m + 1, shift:n + shift]
+    T.gemm_fp8(a8, sa, b8, sb, out=got, workspace=ws)
+    T.check(ws)
+    rows = torch.cat([torch.arange(0, 520), torch.arange(m - 300, m)]).cuda()
+    assert bool(got[m - 2].isnan().all()) and int(got.isnan().any(1).sum()) == 1
+    keep = rows[rows != m - 2]
+    ref, bound = dev_fp8(a8[keep], sa[keep], b8, sb)
+    assert_close_dev(got[keep], ref, bound, out, rel8(k))
+    again = torch.empty((m, n), dtype=DT[out], device="cuda")
+    T.gemm_fp8(a8, sa, b8, sb, out=again, workspace=ws)
+    T.check(ws)
+    assert torch.equal(again[: m - 2], got[: m - 2])
+    got.fill_(5.0)
+    assert bool((full == 5.0).all())
+
+
+LARGE_GROUPS = {
+    "ragged": ([700, 0, 257, 1, 300, 2000], 1003, 1000),
+    "wide": ([1, 5200, 256, 0, 255, 3], 600, 1040),
+    "many": ([300 * (i % 3) for i in range(70)], 264, 1032),
+    "uneven": ([0, 2500, 0], 1100, 264),
+}
+
+
+@pytest.mark.parametrize("dtype,out,shift", [("bf16", "bf16", 0), ("f16", "f32", 0),
+                                             ("bf16", "f32", 1), ("f16", "f16", 5)])
+@pytest.mark.parametrize("trans_b", [False, True], ids=["kn", "nk"])
+@pytest.mark.parametrize("name", list(LARGE_GROUPS))
+def test_grouped_16bit_large_tiles(ws, name, trans_b, dtype, out, shift):
+    sizes, n, k = LARGE_GROUPS[name]
+    off = offsets_of(sizes, first=2)
+    t = sum(sizes) + 5
+    a = draw((t, k), dtype, 101)
+    w = draw((len(sizes), n, k) if trans_b else (len(sizes), k, n), dtype, 102)
+    # The rows outside every group, and the group after the first, are not numbers.
+    a[:2] = a[t - 3:] = float("nan")
+    bad = slice(2 + sizes[0], 2 + sizes[0] + sizes[1])
+    a[bad] = float("inf")
+    full = torch.full((t, (n + 23) // 8 * 8), 5.0, dtype=DT[out], device="cuda")
+    got = full[:, shift:n + shift]
+    T.grouped_gemm(a, w, off, trans_b=trans_b, out=got, workspace=ws)
+    T.check(ws)
+    assert not bool(got[bad].isfinite().any())
+    a[bad] = 0
+    got[bad] = 0
+    ref, bound = dev_grouped(a, w, off.tolist(), trans_b)
+    inside = slice(2, t - 3)
+    assert_close_dev(got[inside], ref[inside], bound[inside], out, rel16(k))
+    got[inside] = 5.0
+    assert bool((full == 5.0).all())
+
+
+@pytest.mark.parametrize("out,shift", [("bf16", 0), ("f32", 0), ("f32", 2)])
+@pytest.mark.parametrize("name", list(LARGE_GROUPS))
+def test_grouped_8bit_large_tiles(ws, name, out, shift):
+    sizes, n, k = LARGE_GROUPS[name]
+    off = offsets_of(sizes, first=1)
+    t = sum(sizes) + 3
+    a8, sa = T.quantize_fp8(draw((t, k), "f32", 103))
+    b8, sb = T.quantize_fp8(draw((len(sizes), n, k), "f32", 104), block_rows=128)
+    sa = sa.clone()
+    sa[0] = sa[t - 2:] = float("nan")
+    full = torch.full((t, (n + 23) // 8 * 8), 5.0, dtype=DT[out], device="cuda")
+    got = full[:, shift:n + shift]
+    T.grouped_gemm_fp8(a8, sa, b8, sb, off, out=got, workspace=ws)
+    T.check(ws)
+    for e, (lo, hi) in enumerate(zip(off.tolist()[:-1], off.tolist()[1:])):
+        if hi > lo:
+            ref, bound = dev_fp8(a8[lo:hi], sa[lo:hi], b8[e], sb[e])
+            assert_close_dev(got[lo:hi], ref, bound, out, rel8(k))
+    got[1:t - 2] = 5.0
+    assert bool((full == 5.0).all())
+
+
+@pytest.mark.parametrize("kind", ["fp8", "grouped", "dgrad", "grouped_fp8"])
+def test_large_tile_wait_expires_and_the_context_recovers(ws, kind):
+    rows, k, n = 2500, 1024, 1104
+    off = offsets_of([rows - 300, 300])
+    a, w = draw((rows, k), "bf16", 105), draw((2, k, n), "bf16", 106)
+    wt = w.transpose(1, 2).contiguous()
+    a8, sa = T.quantize_fp8(a)
+    b8, sb = T.quantize_fp8(wt, block_rows=128)
+
+    def call():
+        if kind == "fp8":
+            return T.gemm_fp8(a8, sa, b8[0], sb[0], workspace=ws)
+        if kind == "grouped_fp8":
+            return T.grouped_gemm_fp8(a8, sa, b8, sb, off, workspace=ws)
+        return T.grouped_gemm(a, wt if kind == "dgrad" else w, off, trans_b=kind == "dgrad",
+                              workspace=ws)
+
+    want = call()
+    T.check(ws)
+    for stage in (0, 2):
+        T.selftest_drop_stage(stage, 50_000_000)
+        call()
+        expect_timeout(ws)
+        got = call()
+        T.check(ws)
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kn", [(264, 257), (200, 518), (40, 4)], ids=str)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+def test_wgrad_writes_only_its_columns(ws, kn, dtype, out):
+    k, n = kn
+    sizes = [130, 0, 77]
+    off = offsets_of(sizes)
+    a, dc = draw((sum(sizes), k), dtype, 108), draw((sum(sizes), n), dtype, 109)
+    full = torch.full((3, k + 2, (n + 15) // 8 * 8), 9.0, dtype=DT[out], device="cuda")
+    T.grouped_wgrad(a, dc, off, out=full[:, 1:k + 1, :n], workspace=ws)
+    T.check(ws)
+    ref, bound = OO.wgrad(f64(a), f64(dc), off.tolist())
+    assert_close(full[:, 1:k + 1, :n], ref, bound, out, rel16(max(sizes)))
+    full[:, 1:k + 1, :n] = 9.0
+    assert bool((full == 9.0).all())
+
+
+@pytest.mark.parametrize("k", [16, 128, 200, 384, 512, 640])
+def test_many_large_tiles_of_few_k_blocks(ws, k):
+    # Every pair of CTAs walks many units, each only a few K blocks long.
+    m, n = 9000, 5000
+    a8, sa, b8, sb = fp8_operands(m, n, k, 110)
+    off = offsets_of([4000, 0, 5000])
+    w8, sw = T.quantize_fp8(draw((3, n, k), "f32", 111), block_rows=128)
+    a, w = draw((m, k), "bf16", 112), draw((3, k, n), "bf16", 113)
+    dense = T.gemm_fp8(a8, sa, b8, sb, workspace=ws)
+    T.check(ws)
+    grouped8 = T.grouped_gemm_fp8(a8, sa, w8, sw, off, workspace=ws)
+    T.check(ws)
+    grouped = T.grouped_gemm(a, w, off, workspace=ws)
+    T.check(ws)
+    for rows, e in ((slice(0, 300), 0), (slice(3900, 4000), 0), (slice(8700, 9000), 2)):
+        ref, bound = dev_fp8(a8[rows], sa[rows], b8, sb)
+        assert_close_dev(dense[rows], ref, bound, "bf16", rel8(k))
+        ref, bound = dev_fp8(a8[rows], sa[rows], w8[e], sw[e])
+        assert_close_dev(grouped8[rows], ref, bound, "bf16", rel8(k))
+        x, y = a[rows].double(), w[e].double()
+        assert_close_dev(grouped[rows], x @ y, x.abs() @ y.abs(), "bf16", rel16(k))
+
+
+def test_results_past_32_bit_offsets(ws):
+    # More than 2^31 elements of the result; its last rows are compared.
+    m, n, k = 530000, 4104, 64
+    a8, sa, b8, sb = fp8_operands(m, n, k, 107)
+    c = T.gemm_fp8(a8, sa, b8, sb, out_dtype="bf16", workspace=ws)
+    T.check(ws)
+    for rows in (slice(0, 130), slice(523000, 523600), slice(m - 300, m)):
+        ref, bound = dev_fp8(a8[rows], sa[rows], b8, sb)
+        assert_close_dev(c[rows], ref, bound, "bf16", rel8(k))
+    q, s, _ = T.rmsnorm_fp8(c[:, :4096], torch.ones(4096, dtype=torch.bfloat16, device="cuda"))
+    tail = c[m - 5:, :4096].double()
+    want = tail / (tail.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    got = q[m - 5:].double() * s[m - 5:].double().repeat_interleave(128, 1)
+    peak = want.abs().reshape(5, 32, 128).amax(2).repeat_interleave(128, 1)
+    # e4m3 rounds by at most 2^-4 of a value and, below 2^-6, by 2^-10.
+    assert bool(((got - want).abs() <= want.abs() * 0.0626 + peak / 448 * 2.0 ** -9).all())

@@ -17,15 +17,20 @@
 // the width that fills whole rounds of the pairs.
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA (leader), warp 2 scales (a small
-// ring in shared memory, fetched four K blocks at a time), warps 4-11
-// epilogue: rows 32*(warp%4), 64-column chunks in turn between the two sets.
+// ring in shared memory, filled by asynchronous copies ten K blocks ahead),
+// warps 4-11 epilogue: rows 32*(warp%4), 64-column chunks in turn between the
+// two sets.
 #include "pair_sm103a.cuh"
 
 namespace tiles {
 namespace {
 
 constexpr int kScaleSlots = kSideSlots;
-constexpr int kScaleLag = 10;                         // K blocks whose scales are on their way in
+// K blocks whose scales are on their way in.  The scale warp walks the units
+// that much ahead of the epilogue, and no role is more than two units ahead of
+// another (the answers' ring): with few K blocks a unit it must not wait for
+// more, 2 x K blocks at most.
+constexpr int kScaleLag = 10, kScaleLagShort = 2;
 constexpr int kSlotFloats = 128 + 8;                  // 128 rows, 8 chunks of 32 columns
 constexpr int kScaleBytes = kScaleSlots * kSlotFloats * 4;
 constexpr int kSmemBytes = kStages * kStageBytes + kStagingBytes + kScaleBytes + kBarrierBytes +
@@ -87,12 +92,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The grid is the host's upper bound: clusters past the last unit leave.
     ptx::grid_dependency_wait();
     if (!units.get(pair, args, &un)) return;
+    const uint64_t limit = wait_limit(args);
     // Walkers: both TMA and scale warps, every epilogue warp, the MMA warp.
     pair_setup(bar, 1, 2 + 2 + 16 + 1, 8, &tmW, &tmA);
 
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
-    const uint64_t limit = args.wait_limit_ns;
     const int blocks = args.k_blocks;
     bool failed = false;
 
@@ -182,11 +187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ---------------- scales ----------------
-            // Asynchronous copies into the ring, kScaleLag K blocks ahead of
+            // Asynchronous copies into the ring, `lag` K blocks ahead of
             // the slot that is handed on (across units).  Scales of rows past
             // the end are not copied: their sums are never written.
             uint32_t slot = 0, phase = 0, done = 0;
             int pending = 0;
+            const int lag = 2 * blocks >= kScaleLag ? kScaleLag : kScaleLagShort;
             do {
                 const int row0 = un.row0 + static_cast<int>(rank) * 128 + lane;
                 const float* sa = args.sa + row0 * args.sa_row;
@@ -208,8 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sa += args.sa_block;
                     sb += args.sb_block;
                     if (++slot == kScaleSlots) { slot = 0; phase ^= 1u; }
-                    if (++pending > kScaleLag) {
-                        ptx::cp_async_wait_groups<kScaleLag>();
+                    if (++pending > lag) {
+                        if (lag == kScaleLag) ptx::cp_async_wait_groups<kScaleLag>();
+                        else ptx::cp_async_wait_groups<kScaleLagShort>();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(&bar->side_full[done]);
                         done = (done + 1) % kScaleSlots;

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The grid is the host's upper bound: clusters past the last unit leave.
     ptx::grid_dependency_wait();
     if (!units.get(pair, args, &un)) return;
+    const uint64_t limit = wait_limit(args);
     // The weight gradient's stages are completed by both CTAs (the producers,
     // or the warps that clear a ragged end).  Walkers: both TMA warps, every
     // epilogue warp, the MMA warp, and the clearing warps.
@@ -103,7 +104,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
-    const uint64_t limit = args.wait_limit_ns;
     bool failed = false;
 
     if (warp == 0) {

@@ -153,7 +153,8 @@ __device__ __forceinline__ void box_begin() {
 
 // The warp's box leaves for columns x .. and rows y .. of item z of c: whole
 // boxes through one TMA store (clipped at the tensor's edges), a ragged
-// group's last rows, or a c that TMA cannot address, through the registers.
+// group's last rows, columns that end inside 16 bytes (a store clips to those,
+// not to the element), or a c that TMA cannot address, through the registers.
 // `out` is the box's first element, and rows x cols what may be written.
 template <typename E>
 __device__ __forceinline__ void box_end(const CUtensorMap* map, bool tma, const uint8_t* box, int x,
@@ -161,7 +162,7 @@ __device__ __forceinline__ void box_end(const CUtensorMap* map, bool tma, const 
                                         bool whole_rows) {
     constexpr int PER = 16 / static_cast<int>(sizeof(E));
     const int lane = threadIdx.x & 31;
-    if (tma && (whole_rows || rows >= 32)) {
+    if (tma && (whole_rows || rows >= 32) && (cols >= 4 * PER || cols % PER == 0)) {
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {

@@ -42,6 +42,15 @@ struct ProductArgs {
     int32_t drop_stage;               // test hook (-1: none)
 };
 
+// How long a wait of the large-tile kernels may take.  Once one has expired in
+// this call, the CTAs that start later, which may miss the same thing, give up
+// soon: a call of many units then ends too, in seconds.
+__device__ __forceinline__ uint64_t wait_limit(const ProductArgs& a) {
+    const uint64_t after = 10000000ull;
+    return *static_cast<const volatile int32_t*>(a.err) != 0 && a.wait_limit_ns > after
+               ? after : a.wait_limit_ns;
+}
+
 // Rows [row0, end) of one tile of `group`.
 struct RowTile { int group, row0, end; };
 
