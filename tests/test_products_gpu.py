@@ -562,3 +562,48 @@ def test_results_past_32_bit_offsets(ws):
     peak = want.abs().reshape(5, 32, 128).amax(2).repeat_interleave(128, 1)
     # e4m3 rounds by at most 2^-4 of a value and, below 2^-6, by 2^-10.
     assert bool(((got - want).abs() <= want.abs() * 0.0626 + peak / 448 * 2.0 ** -9).all())
+
+
+@pytest.mark.parametrize("k", [1, 7, 130, 203, 1003])
+@pytest.mark.parametrize("sizes", [[5, 0, 9], [700, 0, 2100]], ids=["few", "large"])
+def test_what_lies_between_the_rows_is_not_read(ws, sizes, k):
+    # Row lengths that end inside 16 bytes, with not-a-numbers up to the pitch.
+    n, t = 1104 if sizes[0] > 100 else 136, sum(sizes)
+    off = offsets_of(sizes)
+    pad = (k + 23) // 8 * 8
+
+    def apart(x, pitch):
+        wide = torch.full((*x.shape[:-1], pitch), float("nan"), dtype=x.dtype, device="cuda")
+        wide[..., : x.shape[-1]] = x
+        return wide[..., : x.shape[-1]]
+
+    a = apart(draw((t, k), "bf16", 114), pad)
+    w = draw((3, n, k), "bf16", 115)
+    kn = w.transpose(1, 2).contiguous()
+    ref, bound = dev_grouped(a, w, off.tolist(), True)
+    c = T.grouped_gemm(a, apart(w, pad), off, trans_b=True, out_dtype="f32", workspace=ws)
+    T.check(ws)
+    assert_close_dev(c, ref, bound, "f32", rel16(k))
+    c = T.grouped_gemm(a, kn, off, out_dtype="f32", workspace=ws)
+    T.check(ws)
+    assert_close_dev(c, ref, bound, "f32", rel16(k))
+    da = T.grouped_wgrad(a, apart(draw((t, n - 3), "bf16", 116), n + 8), off, out_dtype="f32",
+                         workspace=ws)
+    T.check(ws)
+    assert bool(da.isfinite().all())
+
+    pad8 = (k + 31) // 16 * 16
+    a8, sa = T.quantize_fp8(draw((t, k), "f32", 117))
+    b8, sb = T.quantize_fp8(draw((3, n, k), "f32", 118), block_rows=128)
+    as_bytes = torch.full((t, pad8), 0x7f, dtype=torch.uint8, device="cuda")
+    as_bytes[:, :k] = a8.view(torch.uint8)
+    a8 = as_bytes.view(torch.float8_e4m3fn)[:, :k]
+    as_bytes = torch.full((3, n, pad8), 0x7f, dtype=torch.uint8, device="cuda")
+    as_bytes[:, :, :k] = b8.view(torch.uint8)
+    b8 = as_bytes.view(torch.float8_e4m3fn)[:, :, :k]
+    c = T.grouped_gemm_fp8(a8, sa, b8, sb, off, out_dtype="f32", workspace=ws)
+    T.check(ws)
+    for e, (lo, hi) in enumerate(zip(off.tolist()[:-1], off.tolist()[1:])):
+        if hi > lo:
+            ref, bound = dev_fp8(a8[lo:hi], sa[lo:hi], b8[e], sb[e])
+            assert_close_dev(c[lo:hi], ref, bound, "f32", rel8(k))
