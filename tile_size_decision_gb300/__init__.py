@@ -519,8 +519,34 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
 #
 # These calls are short: a decoding step's norm or product takes a few
 # microseconds on the GPU, less than a dozen Python calls take.  So each one
-# checks its arguments in one expression and packs its descriptor directly;
-# only where that fails does _refuse look for what is wrong.
+# goes through the compiled module first (_calls: checks, allocation and launch
+# without Python objects in between), which returns None for what it does not
+# take.  The Python function then makes the same call the long way, where
+# _refuse finds what is wrong with the arguments.
+
+
+class _NoCalls:
+    """Stands in for the compiled calls where they were not built."""
+
+    rmsnorm = rmsnorm_grad = product_fp8 = grouped_gemm = grouped_wgrad = \
+        staticmethod(lambda *args: None)
+
+
+_CALLS = None
+
+
+def _compiled():
+    global _CALLS
+    _torch()
+    lib = load()
+    if os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_calls.so")):
+        from . import _calls
+        _calls.bind(*(C.cast(getattr(lib, "tiles_" + name), C.c_void_p).value for name in
+                      ("rmsnorm", "rmsnorm_grad", "gemm_fp8", "grouped_gemm", "grouped_wgrad")))
+        _CALLS = _calls
+    else:
+        _CALLS = _NoCalls
+    return _CALLS
 
 
 SCALE_BLOCK = 128     # columns (and weight rows) that share one scale
@@ -645,8 +671,10 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=Non
     """h = x + residual and y = h * (mean(h^2) + eps)^(-1/2) * weight, row by
     row of a matrix; returns (y, h) in x's type.  Without a residual h is x
     itself.  h_out may be the residual (updated in place)."""
-    y, _, h = _rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
-    return y, h
+    r = (_CALLS or _compiled()).rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
+    if r is None:
+        r = _rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
+    return r[0], r[2]
 
 
 def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out=None,
@@ -655,7 +683,9 @@ def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out
     values and one fp32 scale per row and 128 columns, y ~ q * scale.  New
     scales are stored block by block (a transposed view, rows x blocks),
     which the products read fastest."""
-    return _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, True)
+    r = (_CALLS or _compiled()).rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, True)
+    return r if r is not None else _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream,
+                                            True)
 
 
 def rmsnorm_grad_workspace(x):
@@ -673,6 +703,10 @@ def rmsnorm_grad(dy, h, weight, eps=1e-6, dh=None, dx_out=None, dweight_out=None
     """Gradients of rmsnorm at h, given those of y (dy) and, where h is used
     past the norm, of h (dh): returns (dx, dweight).  dx, in h's type, is the
     gradient of x and of the residual alike; dweight is fp32."""
+    r = (_CALLS or _compiled()).rmsnorm_grad(dy, h, weight, eps, dh, dx_out, dweight_out,
+                                             workspace, stream)
+    if r is not None:
+        return r
     torch = _TORCH or _torch()
     codes = _DTYPE_CODES or _codes()
     rows, cols, ldh, unit = _matrix(h, "h")
@@ -813,8 +847,10 @@ def gemm_fp8(a, a_scales, b, b_scales, out=None, out_dtype=None, workspace=None,
     * (a[i] . b[j] within t): e4m3 rows (m x k, as rmsnorm_fp8 and
     quantize_fp8 give them) times an e4m3 weight stored n x k.  out is bf16
     unless out_dtype ("f32", "f16", "bf16") says otherwise."""
-    return _product_fp8(a, a_scales, b, b_scales, None, out, out_dtype, workspace, stream,
-                        "tiles_gemm_fp8")
+    r = (_CALLS or _compiled()).product_fp8(a, a_scales, b, b_scales, None, out, out_dtype,
+                                            workspace, stream)
+    return r if r is not None else _product_fp8(a, a_scales, b, b_scales, None, out, out_dtype,
+                                                workspace, stream, "tiles_gemm_fp8")
 
 
 def grouped_gemm_fp8(a, a_scales, b, b_scales, offsets, out=None, out_dtype=None, workspace=None,
@@ -822,8 +858,10 @@ def grouped_gemm_fp8(a, a_scales, b, b_scales, offsets, out=None, out_dtype=None
     """gemm_fp8 with a weight per group (b: groups x n x k): rows offsets[g] ..
     offsets[g+1] - 1 of a meet b[g].  offsets is an int32 CUDA vector that
     only the kernel reads.  Rows outside every group are not written."""
-    return _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype, workspace, stream,
-                        "tiles_grouped_gemm")
+    r = (_CALLS or _compiled()).product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype,
+                                            workspace, stream)
+    return r if r is not None else _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype,
+                                                workspace, stream, "tiles_grouped_gemm")
 
 
 def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspace=None,
@@ -834,6 +872,10 @@ def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspa
     is the gradient of the rows when a is that of the products.  offsets is
     an int32 CUDA vector that only the kernel reads.  Rows outside every
     group are not written."""
+    r = (_CALLS or _compiled()).grouped_gemm(a, b, offsets, trans_b, out, out_dtype, workspace,
+                                             stream)
+    if r is not None:
+        return r
     torch = _TORCH or _torch()
     codes = _DTYPE_CODES or _codes()
     m, k, lda, ua = _matrix(a, "a")
@@ -869,6 +911,9 @@ def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stre
     """out[g] = a_g^T @ dc_g over the rows of group g: the weight gradients
     (groups x k x n) of out = grouped_gemm(a, w, offsets), given dc.  An
     empty group's gradient is zero."""
+    r = (_CALLS or _compiled()).grouped_wgrad(a, dc, offsets, out, out_dtype, workspace, stream)
+    if r is not None:
+        return r
     torch = _TORCH or _torch()
     codes = _DTYPE_CODES or _codes()
     m, k, lda, ua = _matrix(a, "a")

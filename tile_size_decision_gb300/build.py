@@ -1,4 +1,5 @@
-"""Build libtiles.so in-tree with nvcc for sm_103a (no cmake).
+"""Build libtiles.so in-tree with nvcc for sm_103a (no cmake), and the compiled
+half of the Python binding (_calls.so, against the installed PyTorch).
 
     python -m tile_size_decision_gb300.build [-v] [--force]
 
@@ -13,10 +14,12 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +27,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtiles.so")
+CALLS = os.path.join(HERE, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -84,13 +88,45 @@ def _compile(src: str, obj: str, extra: list, force: bool, verbose: bool) -> str
     return obj_path
 
 
+def build_calls(force: bool = False, verbose: bool = False) -> str | None:
+    """Compile the compiled calls (csrc/torch_calls.cpp); None without PyTorch,
+    whose headers and libraries they need."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = os.path.dirname(spec.origin)
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "tiles.h"),
+                                               os.path.join(torch, "version.py")))
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return CALLS
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = CALLS + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, src,
+           "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-L", os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_calls.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every unit and link libtiles.so; return its path."""
+    """Compile every unit, link libtiles.so and the compiled calls; return
+    libtiles.so's path."""
     os.makedirs(BUILD, exist_ok=True)
-    jobs = min(len(units()), max(1, os.cpu_count() or 1))
+    jobs = min(len(units()) + 1, max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        calls = ex.submit(build_calls, force, verbose)
         futs = [ex.submit(_compile, s, o, e, force, verbose) for s, o, e in units()]
         objs = [f.result() for f in futs]
+        calls.result()
     if force or not os.path.exists(LIB) or \
             os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + ".tmp"
