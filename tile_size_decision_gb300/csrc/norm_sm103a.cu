@@ -475,106 +475,83 @@ struct GradArgs {
 template <typename T, bool VEC, bool SPANS>
 __global__ void __launch_bounds__(512, 2)
     rmsnorm_grad_kernel(const GradArgs a) {
-    constexpr int VPT = 1;
     __shared__ float slots[128];
     extern __shared__ float side[];                // blockDim.y > 1: the other warps' parts
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int step = blockDim.x * 8;
     const int cols = static_cast<int>(a.cols);
-    const int first = static_cast<int>(blockIdx.y) * VPT * step;
-    float dw[VPT][8];
+    const int first = static_cast<int>(blockIdx.y) * step;
+    const int c = first + threadIdx.x * 8;
+    const float inv_n = 1.0f / static_cast<float>(a.cols);
+    float dw[8];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
+    for (int i = 0; i < 8; ++i) dw[i] = 0.0f;
     int turn = 0;
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; row < a.rows;
          row += static_cast<int64_t>(gridDim.x) * blockDim.y, turn ^= 1) {
         const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
         const T* h = static_cast<const T*>(a.h) + row * a.ldh;
-        float g[VPT][8], v[VPT][8];
+        const T* dh = a.dh ? static_cast<const T*>(a.dh) + row * a.lddh : nullptr;
+        float g[8], v[8], w[8], past[8];
+        load8<T, VEC>(dy, c, cols, g);
+        load8<T, VEC>(h, c, cols, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) past[i] = 0.0f;
+        // dh with the others where it is one load (8192 x 4096 fp32: 88 us
+        // against 95), after the sums where it is eight (3000 x 3001: 40
+        // against 45; the registers spill otherwise).
+        if (VEC && dh) load8<T, VEC>(dh, c, cols, past);
+        load8_any<VEC>(a.weight, a.weight_dtype, c, cols, w);
         float s[2] = {0.0f, 0.0f};                 // sum h^2, sum dy w h
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = first + j * step + threadIdx.x * 8;
-            load8<T, VEC>(dy, c, cols, g[j]);
-            load8<T, VEC>(h, c, cols, v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            float w[8];
-            load8_any<VEC>(a.weight, a.weight_dtype, first + j * step + threadIdx.x * 8, cols, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s[0] += v[j][i] * v[j][i];
-                s[1] += g[j][i] * w[i] * v[j][i];
-            }
+        for (int i = 0; i < 8; ++i) {
+            s[0] += v[i] * v[i];
+            s[1] += g[i] * w[i] * v[i];
         }
         if constexpr (SPANS) {
             for (int c0 = 0; c0 < cols; c0 += step) {
-                if (c0 >= first && c0 < first + VPT * step) continue;
-                const int c = c0 + threadIdx.x * 8;
-                float p[8], q[8], w[8];
-                load8<T, VEC>(dy, c, cols, p);
-                load8<T, VEC>(h, c, cols, q);
-                load8_any<VEC>(a.weight, a.weight_dtype, c, cols, w);
+                if (c0 == first) continue;
+                const int at = c0 + threadIdx.x * 8;
+                float p[8], q[8], u[8];
+                load8<T, VEC>(dy, at, cols, p);
+                load8<T, VEC>(h, at, cols, q);
+                load8_any<VEC>(a.weight, a.weight_dtype, at, cols, u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     s[0] += q[i] * q[i];
-                    s[1] += p[i] * w[i] * q[i];
+                    s[1] += p[i] * u[i] * q[i];
                 }
             }
         }
         row_sum(s, slots, turn);
-        const float inv_n = 1.0f / static_cast<float>(a.cols);
         const float rstd = rsqrtf(s[0] * inv_n + a.eps);
         const float back = s[1] * inv_n * rstd * rstd * rstd;
-        const T* dh = a.dh ? static_cast<const T*>(a.dh) + row * a.lddh : nullptr;
-        T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+        if (!VEC && dh) load8<T, VEC>(dh, c, cols, past);
+        load8_any<VEC>(a.weight, a.weight_dtype, c, cols, w);
+        float o[8];
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = first + j * step + threadIdx.x * 8;
-            float w[8], o[8];
-            load8_any<VEC>(a.weight, a.weight_dtype, c, cols, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                o[i] = g[j][i] * w[i] * rstd - v[j][i] * back;
-                dw[j][i] += g[j][i] * v[j][i] * rstd;
-            }
-            if (dh) {
-                float q[8];
-                load8<T, VEC>(dh, c, cols, q);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] += q[i];
-            }
-            store8<T, VEC>(dx, c, cols, o);
+        for (int i = 0; i < 8; ++i) {
+            o[i] = g[i] * w[i] * rstd - v[i] * back + past[i];
+            dw[i] += g[i] * v[i] * rstd;
         }
+        store8<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx, c, cols, o);
     }
     if (blockDim.y > 1) {                          // then blockDim.x == 32: one warp a row
         if (threadIdx.y > 0)
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    side[(threadIdx.y - 1) * (VPT * 256) + (j * 8 + i) * 32 + threadIdx.x] = dw[j][i];
+            for (int i = 0; i < 8; ++i)
+                side[(threadIdx.y - 1) * 256 + i * 32 + threadIdx.x] = dw[i];
         __syncthreads();
         if (threadIdx.y > 0) return;
         for (int y = 0; y < static_cast<int>(blockDim.y) - 1; ++y)
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dw[j][i] += side[y * (VPT * 256) + (j * 8 + i) * 32 + threadIdx.x];
+            for (int i = 0; i < 8; ++i) dw[i] += side[y * 256 + i * 32 + threadIdx.x];
     }
     float* out = a.partials + static_cast<int64_t>(blockIdx.x) * a.cols;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int c = first + j * step + threadIdx.x * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (column<VEC>(c, i) < cols) out[column<VEC>(c, i)] = dw[j][i];
-    }
+    for (int i = 0; i < 8; ++i)
+        if (column<VEC>(c, i) < cols) out[column<VEC>(c, i)] = dw[i];
 }
 
 // The same with the rows' pieces 16-byte aligned and the whole row in one
@@ -902,7 +879,11 @@ template <typename T>
 int launch_grad(const GradArgs& a, bool vec, int sms, int* parts, cudaStream_t st) {
     GradGeometry g = grad_geometry(a.rows, a.cols, sms, true);
     const size_t smem = RowRing<T, 3, kGradVpt>::bytes(g.threads * g.per_block);
-    if (vec && g.spans == 1 && smem <= kRingBytesMost) {
+    // fp32 pieces are half a vector, and fewer blocks fit beside their ring: only
+    // while a block has few rows (fp32, 64 x 4096: 6.6 us against 9.5 without
+    // the ring, 300 x 4096 9.7 against 11.3, 3187 x 1600 25.3 against 19.4).
+    if (vec && g.spans == 1 && smem <= kRingBytesMost &&
+        (sizeof(T) == 2 || a.rows <= 4 * sms)) {
         static std::atomic<uint64_t> opted{0};
         const cudaError_t e =
             opt_in_smem(rmsnorm_grad_ring_kernel<T, kGradVpt>, kRingBytesMost, &opted);
