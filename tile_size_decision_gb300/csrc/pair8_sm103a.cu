@@ -20,6 +20,14 @@
 // ring in shared memory, filled by asynchronous copies ten K blocks ahead),
 // warps 4-11 epilogue: rows 32*(warp%4), 64-column chunks in turn between the
 // two sets.
+//
+// The reading back bounds it: per K block the MMA's 448 to 512 clocks, the
+// hand-over and the epilogue's 440 follow one another through two buffers that
+// fill tensor memory, about 860 in all.  4096^3 67 us (54% of twice the 16-bit
+// rate), 8192 rows in 32 uneven groups by 4096 x 2048 88 us (55% of the DRAM
+// floor).  Slower when measured: halves of a tile handed over apart (102 us on
+// the groups), 16 epilogue warps (75 on 4096^3), wider TMEM loads (74 to 96),
+// scales through registers (79), tiles of one CTA (67 and 89).
 #include "pair_sm103a.cuh"
 
 namespace tiles {

@@ -21,6 +21,14 @@
 // memory in the matrix fragment layout (a quarter of the plain layout's rate,
 // one K block's MMA time per tile), because stmatrix then transposes it: a row
 // of c is a TMEM column.
+//
+// The tensor cores bound long contractions, the results' way out short ones.
+// 32768 rows in 16 uneven groups, 1024 x 2048 bf16: products 95 us (77% of the
+// measured rate), the rows' gradient 88 (83%), the weight gradient 91 (81%).
+// Measured on 30000 x 1024 x 2048 (83.5 us): without the stores 74.9, without
+// the transposition 83.9, through registers instead of TMA 84.9, with two boxes
+// a warp and the TMEM loads a chunk ahead 84.3: the write traffic itself costs
+// the tenth.
 #include "pair_sm103a.cuh"
 
 namespace tiles {
