@@ -103,19 +103,20 @@ int resident_pairs(int sms, int* pairs) {
 // columns of a tile, and the CTAs along K.
 struct Choice { bool pair; int rows, cols, split; };
 
-// The cheaper by a model in nanoseconds, whose constants were measured on a
-// GB300 (times of single products, 8 to 1024 rows, weights of 512^2 to
-// 4096^2).  A kernel takes a fixed time, then the larger of
-//   - its rounds over the resident blocks x K blocks x the time of one, and
-//   - its bytes at the measured copy rate, times how far it stays from it.
-// Few rows (two blocks an SM): 330 / 360 / 530 ns a K block of 128 for tiles of
-// 16 / 32 / 64 rows in 8 bits, 250 / 280 / 360 ns a K block of 64 in 16 bits.
-// Pairs: 460 ns in 8 bits (whatever the tile's width: the hand-over of the
-// sums bounds it), 330 ns in 16 bits.  Both sides of the choice, 4096 x 4096
-// in 8 bits: 64 rows 8.1 us against 18.4 on pairs, 256 rows 13.3 against 18.4,
-// 1024 rows 37.8 against 20.2; 8 groups of 2048 x 2048 in 16 bits: 8 rows a
-// group 12.3 against 13.3, 128 rows 21.3 against 16.0.  Tiles of 128 rows never
-// won: 8-bit sums of 128 rows leave room for one block an SM.
+// The cheapest by a model in nanoseconds: a start, then the larger of
+//   - the rounds over the resident blocks x (a round's own start and end + its
+//     K blocks x the time of one), and
+//   - the bytes at the measured copy rate, times how far a kernel stays from it.
+// Few rows (two blocks an SM): a second resident block and the addition over a
+// cluster cost extra.  8-bit pairs: a K block's time does not depend on the
+// tile's width (the hand-over of the sums bounds it).  The constants are fitted
+// to the times of 150 products on a GB300 with every kernel (m 1 to 25,000, n
+// and k 128 to 4096, up to 32 groups): within 5 to 9% of them on average, and
+// the choice within 1% of the best.  Both sides, in 8 bits: 16 rows of 4096 x
+// 4096 5.4 us against 20.3 on pairs, 1000 x 4096 x 128 10.0 against 6.4; 32
+// groups of 53 rows, 128 x 2816 in 16 bits, 16.6 against 11.8, 8 of 62 rows,
+// 128 x 1024, 3.9 against 5.5.  Tiles of 128 rows never won: 8-bit sums of 128
+// rows leave room for one block an SM.
 Choice choose(int kind, int64_t m, int64_t n, int64_t k, int64_t groups, int sms, int pairs) {
     const bool fp8 = kind == kWeight8NK;
     const int64_t kb = (k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
@@ -133,19 +134,24 @@ Choice choose(int kind, int64_t m, int64_t n, int64_t k, int64_t groups, int sms
     auto offer = [&](const Choice& c, double ns) {
         if (best_ns == 0 || ns < best_ns) { best = c; best_ns = ns; }
     };
-    const struct { int rows; double ns8, ns16, far; } few[] = {
-        {16, 330, 250, 1.0}, {32, 360, 280, 1.15}, {64, 530, 360, 1.35}};
-    for (const auto& f : few) {
+    struct Few { int rows; double start, round, block, second, cluster, far; };
+    static constexpr Few few16[] = {{16, 1150, 2260, 250, 640, 35, 1.08},
+                                    {32, 1000, 2720, 265, 900, 16, 1.10},
+                                    {64, 570, 3710, 340, 1490, 5, 1.15}};
+    static constexpr Few few8[] = {{16, 820, 2230, 310, 610, 35, 1.00},
+                                   {32, 720, 2780, 360, 870, 8, 1.10},
+                                   {64, 120, 4010, 465, 1760, 4, 1.20}};
+    for (const Few& f : fp8 ? few8 : few16) {
         const int64_t units = row_tiles(f.rows) * ((n + 127) / 128);
         // CTAs along K: while the units leave SMs without a block, at least
         // two K blocks a CTA.
         int split = 1;
         while (split < 8 && units * split < sms && kb >= split * 4) split *= 2;
-        const int64_t rounds = (units * split + 2 * sms - 1) / (2 * sms);
-        const double ns = std::max(static_cast<double>(rounds * ((kb + split - 1) / split)) *
-                                       (fp8 ? f.ns8 : f.ns16) + (split > 1 ? 20.0 * f.rows : 0),
-                                   dram_ns * f.far);
-        offer(Choice{false, f.rows, 128, split}, 3000 + ns);
+        const double rounds = static_cast<double>((units * split + 2 * sms - 1) / (2 * sms));
+        const double work = rounds * (f.round + static_cast<double>((kb + split - 1) / split) * f.block) +
+                            (units * split > sms ? f.second : 0);
+        offer(Choice{false, f.rows, 128, split},
+              f.start + std::max(work, dram_ns * f.far) + (split > 1 ? f.cluster * f.rows : 0));
     }
     // 8-bit pairs: the narrowest tile that takes the fewest rounds.
     int64_t fewest = INT64_MAX;
@@ -154,8 +160,10 @@ Choice choose(int kind, int64_t m, int64_t n, int64_t k, int64_t groups, int sms
         const int64_t rounds = (row_tiles(256) * ((n + c - 1) / c) + pairs - 1) / pairs;
         if (rounds <= fewest) { fewest = rounds; cols = c; }
     }
+    const double round = fp8 ? 1620 : 1840, block = fp8 ? 460 : 250;
     offer(Choice{true, 256, cols, 1},
-          4000 + std::max(static_cast<double>(fewest * kb) * (fp8 ? 460 : 330), dram_ns * 1.05));
+          (fp8 ? 3970 : 2940) + std::max(static_cast<double>(fewest) * (round + kb * block),
+                                         dram_ns * 1.05));
     return best;
 }
 
