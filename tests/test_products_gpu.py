@@ -393,7 +393,8 @@ def assert_close_dev(got, ref, bound, dtype, rel):
     assert_close(got, f64(ref), f64(bound), dtype, rel)
 
 
-LARGE_DENSE = [(3000, 2050, 1040), (20000, 130, 528), (1100, 4100, 2064)]
+LARGE_DENSE = [(3000, 2050, 1040), (20000, 130, 528), (1100, 4100, 2064), (2100, 4100, 1040),
+               (1100, 1030, 2064)]
 
 
 @pytest.mark.parametrize("out,shift", [("bf16", 0), ("f16", 0), ("f32", 0), ("f32", 3), ("bf16", 1)])
@@ -422,6 +423,7 @@ def test_dense_8bit_large_tiles(ws, shape, out, shift):
 
 
 LARGE_GROUPS = {
+    "heavy": ([900, 1300, 0, 2100, 800], 1500, 1040),
     "ragged": ([700, 0, 257, 1, 300, 2000], 1003, 1000),
     "wide": ([1, 5200, 256, 0, 255, 3], 600, 1040),
     "many": ([300 * (i % 3) for i in range(70)], 264, 1032),

@@ -1,7 +1,7 @@
 // 8-bit products with many rows, on CTA pairs, dense or grouped:
 //   c[i][j] = sum over blocks t of 128 of sa[i][t] * sb[j/128][t] * (a[i] . b[j] within t)
 //
-// The tensor core sums one K block of 128 from zero into one of two TMEM
+// The tensor core sums one K block of 128 from zero into one of its TMEM
 // buffers (4 MMA steps of 32), and the epilogue warps add it into fp32
 // registers, times the two scales.  So every K block is read back from tensor
 // memory.  Its read port also feeds the MMA's accumulation: per K block of a
@@ -13,21 +13,25 @@
 // need a scale per column from shared memory, which the operands already use.
 //
 // A pair's tile is 256 rows (128 a CTA) by args.tile_cols weight rows (a
-// multiple of 32, at most 256, half of them loaded by each CTA); the host picks
-// the width that fills whole rounds of the pairs.
+// multiple of 32, half of them loaded by each CTA).  Wide tiles (up to 256) have
+// two buffers in tensor memory, narrow ones (up to 128) four; the host picks
+// the width and with it the kernel (for few tiles the narrow one: 1024 x 1024 x
+// 4096 14.1 us against 19.8, while 4096^3 takes 75.5 against 67.7).
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA (leader), warp 2 scales (a small
 // ring in shared memory, filled by asynchronous copies ten K blocks ahead),
 // warps 4-11 epilogue: rows 32*(warp%4), 64-column chunks in turn between the
 // two sets.
 //
-// The reading back bounds it: per K block the MMA's 448 to 512 clocks, the
-// hand-over and the epilogue's 440 follow one another through two buffers that
-// fill tensor memory, about 860 in all.  4096^3 67 us (54% of twice the 16-bit
-// rate), 8192 rows in 32 uneven groups by 4096 x 2048 88 us (55% of the DRAM
-// floor).  Slower when measured: halves of a tile handed over apart (102 us on
-// the groups), 16 epilogue warps (75 on 4096^3), wider TMEM loads (74 to 96),
-// scales through registers (79), tiles of one CTA (67 and 89).
+// The reading back bounds it: a K block of a wide tile takes about 860 clocks
+// (512 of them MMA), of a narrow one 570 (256).  The epilogue warps never wait
+// for a sum; of their time some 250 clocks a K block go to the two waits, the
+// scales and the first load, the rest to loads and additions.  4096^3 67.7 us
+// (54% of twice the 16-bit rate), 8192 rows in 32 uneven groups by 4096 x 2048
+// 88 us (55% of the DRAM floor).  Slower when measured: halves of a tile handed
+// over apart (102 us on the groups), 16 epilogue warps (75 on 4096^3), wider
+// TMEM loads (72 to 96), scales through registers (79), tiles of one CTA (67
+// and 89).
 #include "pair_sm103a.cuh"
 
 namespace tiles {
@@ -46,10 +50,14 @@ constexpr int kSmemBytes = kStages * kStageBytes + kStagingBytes + kScaleBytes +
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per block");
 static_assert(kScaleBytes % 16 == 0, "the barriers follow the scales");
 constexpr int BK = 128;
-// Registers a thread: the epilogue holds 128 sums.  The block is launched
-// with 168 (384 x 168 = 64512), and 128 x 72 + 256 x 216 is the same total.
-constexpr int kServiceRegisters = 72, kEpilogueRegisters = 216;
-static_assert(128 * kServiceRegisters + 256 * kEpilogueRegisters <= kThreads * 168, "registers");
+// Registers a thread.  The block is launched with 168 (384 x 168 = 64512); the
+// epilogue holds 128 sums (64 of the narrow tile's) and gets what the service
+// warps do not need.
+template <int WIDTH> constexpr int kServiceRegisters = WIDTH == 256 ? 96 : 80;
+template <int WIDTH> constexpr int kEpilogueRegisters = WIDTH == 256 ? 200 : 208;
+static_assert(128 * kServiceRegisters<256> + 256 * kEpilogueRegisters<256> <= kThreads * 168 &&
+              128 * kServiceRegisters<128> + 256 * kEpilogueRegisters<128> <= kThreads * 168,
+              "registers");
 
 struct Unit {
     int group;
@@ -78,9 +86,11 @@ struct Units {
     }
 };
 
+template <int WIDTH>
 __global__ void __launch_bounds__(kThreads, 1)
     pair8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                  const __grid_constant__ CUtensorMap tmC, const ProductArgs args) {
+    constexpr int BUFFERS = 512 / WIDTH, HALVES = WIDTH / 128;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     uint8_t* base = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -110,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool failed = false;
 
     if (warp < 4) {
-        ptx::registers_dec<kServiceRegisters>();
+        ptx::registers_dec<kServiceRegisters<WIDTH>>();
         if (warp == 0) {
             // ---------------- TMA producer ----------------
             uint32_t stage = 0, phase = 0;
@@ -175,15 +185,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t at = (stage * kStageBytes) >> 4;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            ptx::mma_f8<2>(tmem + acc * kMaxWidth, a0 + at + kk * 2, w0 + at + kk * 2,
+                            ptx::mma_f8<2>(tmem + acc * WIDTH, a0 + at + kk * 2, w0 + at + kk * 2,
                                            idesc, kk != 0);
                         ptx::mma_commit<2>(&bar->empty[stage]);
                         ptx::mma_commit<2>(&bar->acc_full[acc]);
                     }
                     __syncwarp();
                     if (++stage == kStages) { stage = 0; phase ^= 1u; }
-                    acc ^= 1u;
-                    if (acc == 0) acc_phase ^= 1u;
+                    acc = (acc + 1) % BUFFERS;
+                acc_phase ^= acc == 0;
                 }
             } while (!failed && walk.next(bar, abort, limit, &failed) &&
                      units.get(walk.unit, args, &un));
@@ -243,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------- epilogue ----------------
-        ptx::registers_inc<kEpilogueRegisters>();
+        ptx::registers_inc<kEpilogueRegisters<WIDTH>>();
         const int quarter = warp & 3, set = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         uint8_t* box = staging + (warp - 4) * kBoxBytes;
@@ -263,65 +273,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         do {
             // This thread's row: columns 64 * (2h + set) + 32q + .. in
             // sum[2h + q], as pairs.
-            uint64_t sum[4][16];
+            uint64_t sum[2 * HALVES][16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2 * HALVES; ++j)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) sum[j][i] = 0;
-            for (int b = 0; b < blocks; ++b) {
+            // 16 columns at a time, the next ones' load in flight while these are
+            // added; the first of the next K block's too, so that its waits
+            // and the first load's latency are behind the last additions.
+            // (Columns past the width hold old sums that nothing reads.)
+            constexpr int PARTS = 4 * HALVES;
+            auto column = [](int i) { return (i >> 2) * 128 + (i & 3) * 16; };
+            uint32_t v[2][16];
+            float scale[2 * HALVES], next[2 * HALVES];     // row's times chunk's
+            uint32_t t = 0;
+            // Waits for the next K block, reads its scales into `to` and starts
+            // the load of its first columns.
+            auto open = [&](float (&to)[2 * HALVES]) {
                 bool ok = ptx::mbar_wait(&bar->side_full[slot], slot_phase, abort, limit);
                 const float* sc = scales + slot * kSlotFloats;
                 const float row_scale = sc[quarter * 32 + lane];
-                const float2 w01 = *reinterpret_cast<const float2*>(sc + 128 + set * 2);
-                const float2 w23 = *reinterpret_cast<const float2*>(sc + 132 + set * 2);
-                const float w[4] = {w01.x, w01.y, w23.x, w23.y};
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    const float2 w = *reinterpret_cast<const float2*>(sc + 128 + 4 * h + set * 2);
+                    to[2 * h] = row_scale * w.x;
+                    to[2 * h + 1] = row_scale * w.y;
+                }
                 ok = ok && ptx::mbar_wait(&bar->acc_full[acc], acc_phase, abort, limit);
-                if (!__all_sync(0xffffffffu, ok)) {
+                if (!__all_sync(0xffffffffu, ok)) return false;
+                if (lane == 0) ptx::mbar_arrive(&bar->side_empty[slot]);
+                if (++slot == kScaleSlots) { slot = 0; slot_phase ^= 1u; }
+                ptx::tc_fence_after();
+                t = tmem + lanes + acc * WIDTH + set * 64;
+                ptx::tmem_ld_16cols(t, v[0], 0);
+                return true;
+            };
+            if (!open(scale)) {
+                failed = true;
+                break;
+            }
+            auto add = [&](int i) {
+                const uint32_t s = __float_as_uint(scale[i >> 1]);
+                const uint64_t ss = ptx::pack_pair(s, s);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    ptx::fma_pair(sum[i >> 1][(i & 1) * 8 + q],
+                                  ptx::pack_pair(v[i & 1][2 * q], v[i & 1][2 * q + 1]), ss);
+            };
+#pragma unroll 1
+            for (int b = 0; b < blocks; ++b) {
+                ptx::tmem_ld_wait_for(v[0]);
+#pragma unroll
+                for (int i = 0; i + 1 < PARTS; ++i) {
+                    ptx::tmem_ld_16cols(t + column(i + 1), v[(i + 1) & 1], 0);
+                    add(i);
+                    ptx::tmem_ld_wait_for(v[(i + 1) & 1]);
+                }
+                // All read: back to the MMA before the last sums.
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_remote(acc_empty + acc * 8);
+                acc = (acc + 1) % BUFFERS;
+                acc_phase ^= acc == 0;
+                if (b + 1 < blocks && !open(next)) {
                     failed = true;
                     break;
                 }
-                if (lane == 0) ptx::mbar_arrive(&bar->side_empty[slot]);
-                ptx::tc_fence_after();
-                // 16 columns at a time, the next ones' load in flight while
-                // these are added.  (Columns past the width hold old sums
-                // that nothing reads.)
-                const uint32_t t = tmem + lanes + acc * kMaxWidth + set * 64;
-                auto column = [](int i) { return (i >> 2) * 128 + (i & 3) * 16; };
-                constexpr int parts = 8;
-                uint32_t v[2][16];
-                if (parts > 0) {
-                    ptx::tmem_ld_16cols(t, v[0], 0);
-                    ptx::tmem_ld_wait();
-                }
+                add(PARTS - 1);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (i < parts) {
-                        if (i + 1 < parts) {
-                            ptx::tmem_ld_16cols(t + column(i + 1), v[(i + 1) & 1], 0);
-                        } else {
-                            // All read: back to the MMA before the last sums.
-                            ptx::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive_remote(acc_empty + acc * 8);
-                        }
-                        const float s = row_scale * w[i >> 1];
-                        const uint64_t ss = ptx::pack_pair(__float_as_uint(s), __float_as_uint(s));
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            ptx::fma_pair(sum[i >> 1][(i & 1) * 8 + q],
-                                          ptx::pack_pair(v[i & 1][2 * q], v[i & 1][2 * q + 1]), ss);
-                        if (i + 1 < parts) ptx::tmem_ld_wait_for(v[(i + 1) & 1]);
-                    }
-                }
-                if (++slot == kScaleSlots) { slot = 0; slot_phase ^= 1u; }
-                acc ^= 1u;
-                if (acc == 0) acc_phase ^= 1u;
+                for (int i = 0; i < 2 * HALVES; ++i) scale[i] = next[i];
             }
             if (failed) break;
             const int row0 = un.row0 + static_cast<int>(rank) * 128 + quarter * 32;
             const int rows = un.end - row0;                // what is left to write
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2 * HALVES; ++j) {
                 const int col0 = un.n0 + (j >> 1) * 128 + set * 64 + (j & 1) * 32;
                 const int cols = min(args.n, un.n0 + un.width) - col0;
                 if (rows <= 0 || cols <= 0) break;
@@ -359,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 int pair_max_groups(int sms) {
-    if (cudaFuncSetAttribute(pair8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(pair8_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes) != cudaSuccess) {
         cudaGetLastError();
         return sms / 2;
@@ -376,7 +402,7 @@ int pair_max_groups(int sms) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, pair8_kernel, &cfg) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveClusters(&clusters, pair8_kernel<256>, &cfg) != cudaSuccess ||
         clusters <= 0) {
         cudaGetLastError();
         return sms / 2;
@@ -384,13 +410,24 @@ int pair_max_groups(int sms) {
     return clusters;
 }
 
-int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const CUtensorMap& out,
+namespace {
+
+template <int WIDTH>
+int launch_width(const CUtensorMap& w, const CUtensorMap& a, const CUtensorMap& c,
                  const ProductArgs& args, int units, cudaStream_t st) {
     static std::atomic<uint64_t> opted{0};
-    const cudaError_t e = opt_in_smem(pair8_kernel, kSmemBytes, &opted);
+    const cudaError_t e = opt_in_smem(pair8_kernel<WIDTH>, kSmemBytes, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
-    return launch_cluster(pair8_kernel, 2, dim3(static_cast<unsigned>(2 * units)), dim3(kThreads),
-                          kSmemBytes, st, weight, rows, out, args);
+    return launch_cluster(pair8_kernel<WIDTH>, 2, dim3(static_cast<unsigned>(2 * units)),
+                          dim3(kThreads), kSmemBytes, st, w, a, c, args);
+}
+
+}  // namespace
+
+int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const CUtensorMap& out,
+                 const ProductArgs& args, int units, cudaStream_t st) {
+    return args.tile_cols > 128 ? launch_width<256>(weight, rows, out, args, units, st)
+                                : launch_width<128>(weight, rows, out, args, units, st);
 }
 
 }  // namespace tiles

@@ -24,7 +24,7 @@ constexpr int kBarrierBytes = 768;
 constexpr int kSideSlots = 16;
 
 struct PairBarriers {
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    uint64_t full[kStages], empty[kStages], acc_full[4], acc_empty[4];
     uint64_t side_full[kSideSlots], side_empty[kSideSlots];   // scales (8-bit), ragged ends (gradient)
     uint64_t drain;
     uint64_t next_full[2], next_empty[2];
@@ -101,9 +101,11 @@ __device__ __forceinline__ void pair_setup(PairBarriers* bar, int stage_arrivals
             ptx::mbar_init(&bar->full[s], stage_arrivals);
             ptx::mbar_init(&bar->empty[s], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             ptx::mbar_init(&bar->acc_full[i], 1);
             ptx::mbar_init(&bar->acc_empty[i], 2 * readers);
+        }
+        for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bar->next_full[i], 1);
             ptx::mbar_init(&bar->next_empty[i], walkers);
         }

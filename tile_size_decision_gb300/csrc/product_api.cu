@@ -108,8 +108,8 @@ struct Choice { bool pair; int rows, cols, split; };
 //     K blocks x the time of one), and
 //   - the bytes at the measured copy rate, times how far a kernel stays from it.
 // Few rows (two blocks an SM): a second resident block and the addition over a
-// cluster cost extra.  8-bit pairs: a K block's time does not depend on the
-// tile's width (the hand-over of the sums bounds it).  The constants are fitted
+// cluster cost extra.  8-bit pairs: a K block's time depends on the kernel
+// (tiles up to 128 or 256 wide), not on the tile's width.  The constants are fitted
 // to the times of 150 products on a GB300 with every kernel (m 1 to 25,000, n
 // and k 128 to 4096, up to 32 groups): within 5 to 9% of them on average, and
 // the choice within 1% of the best.  Both sides, in 8 bits: 16 rows of 4096 x
@@ -153,17 +153,22 @@ Choice choose(int kind, int64_t m, int64_t n, int64_t k, int64_t groups, int sms
         offer(Choice{false, f.rows, 128, split},
               f.start + std::max(work, dram_ns * f.far) + (split > 1 ? f.cluster * f.rows : 0));
     }
-    // 8-bit pairs: the narrowest tile that takes the fewest rounds.
-    int64_t fewest = INT64_MAX;
-    int cols = 256;
-    for (int c = 256; c >= (fp8 ? 64 : 256); c -= 32) {
-        const int64_t rounds = (row_tiles(256) * ((n + c - 1) / c) + pairs - 1) / pairs;
-        if (rounds <= fewest) { fewest = rounds; cols = c; }
+    // Pairs: 8-bit tiles as narrow as the rounds allow, in either kernel.
+    struct Pair { int most, least; double start, round, block; };
+    static constexpr Pair pair16[] = {{256, 256, 2940, 1840, 250}};
+    static constexpr Pair pair8[] = {{256, 160, 3970, 1620, 460}, {128, 64, 3500, 1100, 300}};
+    for (int i = 0; i < (fp8 ? 2 : 1); ++i) {
+        const Pair& p = fp8 ? pair8[i] : pair16[i];
+        int64_t fewest = INT64_MAX;
+        int cols = p.most;
+        for (int c = p.most; c >= p.least; c -= 32) {
+            const int64_t rounds = (row_tiles(256) * ((n + c - 1) / c) + pairs - 1) / pairs;
+            if (rounds <= fewest) { fewest = rounds; cols = c; }
+        }
+        offer(Choice{true, 256, cols, 1},
+              p.start + std::max(static_cast<double>(fewest) * (p.round + kb * p.block),
+                                 dram_ns * 1.05));
     }
-    const double round = fp8 ? 1620 : 1840, block = fp8 ? 460 : 250;
-    offer(Choice{true, 256, cols, 1},
-          (fp8 ? 3970 : 2940) + std::max(static_cast<double>(fewest) * (round + kb * block),
-                                         dram_ns * 1.05));
     return best;
 }
 
