@@ -173,6 +173,12 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Between the generic proxy's accesses so far, seen from any CTA of the cluster,
+// and the async proxy's that follow.
+__device__ __forceinline__ void fence_proxy_async() {
+    asm volatile("fence.proxy.async;" ::: "memory");
+}
+
 // An asynchronous global -> shared copy of 4 bytes.
 __device__ __forceinline__ void cp_async_4(void* smem_dst, const void* gmem_src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(smem_dst)),

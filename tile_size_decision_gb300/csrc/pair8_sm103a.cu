@@ -19,8 +19,8 @@
 // 4096 14.1 us against 19.8, while 4096^3 takes 75.5 against 67.7).
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA (leader), warp 2 scales (a small
-// ring in shared memory, filled by asynchronous copies ten K blocks ahead),
-// warps 4-11 epilogue: rows 32*(warp%4), 64-column chunks in turn between the
+// ring in shared memory, filled by asynchronous copies ten K blocks ahead), warp
+// 3 the units, warps 4-11 epilogue: rows 32*(warp%4), 64-column chunks in turn between the
 // two sets.
 //
 // The reading back bounds it: a K block of a wide tile takes about 860 clocks
@@ -111,8 +111,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::grid_dependency_wait();
     if (!units.get(pair, args, &un)) return;
     const uint64_t limit = wait_limit(args);
-    // Walkers: both TMA and scale warps, every epilogue warp, the MMA warp.
-    pair_setup(bar, 1, 2 + 2 + 16 + 1, 8, &tmW, &tmA);
+    // Walkers: both TMA and scale warps, every epilogue warp, the MMA warp and
+    // the asking warp.
+    pair_setup(bar, 1, 2 + 2 + 16 + 1 + 1, 8, &tmW, &tmA);
 
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
@@ -125,17 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- TMA producer ----------------
             uint32_t stage = 0, phase = 0;
             int issued = 0;
-            Asker asker;
+            const bool issuer = ptx::elect_one_sync();
+            const uint32_t full0 = ptx::map_to_cta(ptx::smem_addr(&bar->full[0]), 0);
+            // (A box of half a tile's weight rows, also where the last tile has fewer.)
+            const uint32_t both = 2u * static_cast<uint32_t>(kHalfBytes + args.tile_cols / 2 * 128);
             do {
-                if (leader && !asker.ask(bar, abort, limit)) {
-                    failed = true;
-                    break;
-                }
-                const int half = un.width / 2;             // weight rows this CTA loads
-                const int first = un.n0 + static_cast<int>(rank) * half;
+                const int first = un.n0 + static_cast<int>(rank) * (un.width / 2);
                 const int row0 = un.row0 + static_cast<int>(rank) * 128;
-                const int boxes = (half + kBoxRows - 1) / kBoxRows;
-                const uint32_t both = 2u * (kHalfBytes + boxes * kBoxRows * 128);
                 for (int b = 0; b < blocks; ++b) {
                     if (!__all_sync(0xffffffffu,
                                     ptx::mbar_wait(&bar->empty[stage], phase ^ 1u, abort, limit))) {
@@ -143,14 +140,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const bool planted = pair == 0 && issued == args.drop_stage;
-                    if (!planted && ptx::elect_one_sync()) {
+                    if (!planted && issuer) {
                         uint8_t* a = base + stage * kStageBytes;
-                        const uint32_t fb = ptx::map_to_cta(ptx::smem_addr(&bar->full[stage]), 0);
+                        const uint32_t fb = full0 + stage * 8;
                         if (leader) ptx::mbar_arrive_expect_tx(&bar->full[stage], both);
                         ptx::tma_load_3d_pair(a, &tmA, fb, b * BK, row0, 0);
-                        for (int j = 0; j < boxes; ++j)
-                            ptx::tma_load_3d_pair(a + kHalfBytes + j * kBoxRows * 128, &tmW, fb, b * BK,
-                                                  first + j * kBoxRows, un.group);
+                        ptx::tma_load_3d_pair(a + kHalfBytes, &tmW, fb, b * BK, first, un.group);
                     }
                     __syncwarp();
                     ++issued;
@@ -203,6 +198,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::mbar_wait(&bar->drain, 0, nullptr, limit);
             }
             __syncwarp();
+        } else if (warp == 3 && leader) {
+            // ---------------- the next units ----------------
+            Asker asker;
+            do {
+                if (!asker.ask(bar, abort, limit)) {
+                    failed = true;
+                    break;
+                }
+            } while (walk.next(bar, abort, limit, &failed) && units.get(walk.unit, args, &un));
+            if (failed) {
+                if (lane == 0) raise_error(args.err, abort, kErrProducer);
+                settle_after_abort();
+            }
         } else if (warp == 2) {
             // ---------------- scales ----------------
             // Asynchronous copies into the ring, `lag` K blocks ahead of

@@ -16,19 +16,21 @@
 // infinity times zero would not be zero) before the MMA reads them.
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA (leader), warp 2 the clearing of
-// ragged ends (weight gradient), warps 4-11 epilogue: lanes 32*(warp%4), column
-// chunks of 32 in turn between the two sets of four.  The epilogue reads tensor
-// memory in the matrix fragment layout (a quarter of the plain layout's rate,
-// one K block's MMA time per tile), because stmatrix then transposes it: a row
-// of c is a TMEM column.
+// ragged ends (weight gradient), warp 3 the units (leader), warps 4-11 epilogue:
+// lanes 32*(warp%4), column chunks of 32 in turn between the two sets of four.
+// The epilogue reads tensor memory in the matrix fragment layout (a quarter of
+// the plain layout's rate, one K block's MMA time per tile), because stmatrix
+// then transposes it: a row of c is a TMEM column.
 //
 // The tensor cores bound long contractions, the results' way out short ones.
-// 32768 rows in 16 uneven groups, 1024 x 2048 bf16: products 95 us (77% of the
-// measured rate), the rows' gradient 88 (83%), the weight gradient 91 (81%).
-// Measured on 30000 x 1024 x 2048 (83.5 us): without the stores 74.9, without
-// the transposition 83.9, through registers instead of TMA 84.9, with two boxes
-// a warp and the TMEM loads a chunk ahead 84.3: the write traffic itself costs
-// the tenth.
+// 32768 rows in 16 uneven groups, 1024 x 2048 bf16: products 85 us (86% of the
+// measured rate), the rows' gradient 84 (87%), the weight gradient 91 (80%).
+// What made the products faster than 95: the next units asked for by a warp of
+// its own, and a stage's rows in one load (the TMA warp, with six loads a stage,
+// had been the slowest role: 650 clocks a K block).  Measured before that on
+// 30000 x 1024 x 2048 (83.5 us): without the stores 74.9, without the
+// transposition 83.9, through registers instead of TMA 84.9, with two boxes a
+// warp and the TMEM loads a chunk ahead 84.3.
 #include "pair_sm103a.cuh"
 
 namespace tiles {
@@ -84,7 +86,8 @@ struct Units {
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
-                const __grid_constant__ CUtensorMap tmC, const ProductArgs args) {
+                const __grid_constant__ CUtensorMap tmA128, const __grid_constant__ CUtensorMap tmC,
+                const ProductArgs args) {
     constexpr bool GRAD = KIND == kWeightGrad;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -107,8 +110,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t limit = wait_limit(args);
     // The weight gradient's stages are completed by both CTAs (the producers,
     // or the warps that clear a ragged end).  Walkers: both TMA warps, every
-    // epilogue warp, the MMA warp, and the clearing warps.
-    pair_setup(bar, GRAD ? 2 : 1, 2 + 16 + 1 + (GRAD ? 2 : 0), 8, &tmW, &tmA);
+    // epilogue warp, the MMA warp, and the clearing warps or the asking warp.
+    pair_setup(bar, GRAD ? 2 : 1, 2 + 16 + 1 + (GRAD ? 2 : 1), 8, &tmW, &tmA);
 
     const uint32_t tmem = bar->tmem_base;
     volatile int* abort = &bar->abort;
@@ -118,20 +121,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- TMA producer ----------------
         uint32_t stage = 0, phase = 0;
         int issued = 0;
+        const bool issuer = ptx::elect_one_sync();
+        const uint32_t full0 = ptx::map_to_cta(ptx::smem_addr(&bar->full[0]), 0);
         Asker asker;
         do {
-            // Ask for the unit after this one; its answer arrives while this
-            // unit's loads are issued.
-            if (leader && !asker.ask(bar, abort, limit)) {
+            if (GRAD && leader && !asker.ask(bar, abort, limit)) {
                 failed = true;
                 break;
             }
             const int half = un.width / 2;                 // rows this CTA loads
             const int col0 = un.n0 + static_cast<int>(rank) * 128;
             const int first = un.row0 + static_cast<int>(rank) * half;
+            // More than 64 rows come as one box (each load takes the warp time
+            // that it does not have: six of them 650 clocks a K block).
+            const bool whole = !GRAD && half > 64;
             const int boxes = GRAD ? half / 64 : (half + kBoxRows - 1) / kBoxRows;
             const uint32_t mine = static_cast<uint32_t>(
-                kHalfBytes + boxes * (GRAD ? kAtomBytes : kBoxRows * 128));
+                kHalfBytes + (whole ? kHalfBytes : boxes * (GRAD ? kAtomBytes : kBoxRows * 128)));
             for (int b = 0; b < un.blocks; ++b) {
                 if (!__all_sync(0xffffffffu,
                                 ptx::mbar_wait(&bar->empty[stage], phase ^ 1u, abort, limit))) {
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const bool planted = pair == 0 && issued == args.drop_stage;
-                if (!planted && ptx::elect_one_sync()) {
+                if (!planted && issuer) {
                     uint8_t* w = base + stage * kStageBytes;
                     uint8_t* r = w + kHalfBytes;
                     const int kk = un.k0 + b * BK;
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::mbar_arrive_expect_tx(&bar->side_full[stage], mine);
                         fb = ptx::map_to_cta(ptx::smem_addr(&bar->side_full[stage]), rank);
                     } else {
-                        fb = ptx::map_to_cta(ptx::smem_addr(&bar->full[stage]), 0);
+                        fb = full0 + stage * 8;
                         if (leader) ptx::mbar_arrive_expect_tx(&bar->full[stage], 2 * mine);
                         else if (GRAD) ptx::mbar_arrive_remote(fb);
                     }
@@ -165,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         ptx::tma_load_3d_pair(w, &tmW, fb, kk, col0, un.group);
                     }
-                    for (int j = 0; j < boxes; ++j) {
+                    if (whole) ptx::tma_load_3d_pair(r, &tmA128, fb, kk, first, 0);
+                    for (int j = 0; j < (whole ? 0 : boxes); ++j) {
                         if constexpr (GRAD)
                             ptx::tma_load_3d_pair(r + j * kAtomBytes, &tmA, fb, first + j * 64, kk, 0);
                         else
@@ -238,6 +245,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_wait(&bar->drain, 0, nullptr, limit);
         }
         __syncwarp();
+    } else if (!GRAD && warp == 3 && leader) {
+        // ---------------- the next units ----------------
+        // (Asking takes the TMA warp 1200 clocks a unit, which the products' loads
+        // do not have: 32768 rows in 16 uneven groups, 1024 x 2048, 84 us against
+        // 95.  The weight gradient asks there, which measured better: 91 against
+        // 94.)
+        Asker asker;
+        do {
+            if (!asker.ask(bar, abort, limit)) {
+                failed = true;
+                break;
+            }
+        } while (walk.next(bar, abort, limit, &failed) && units.get(walk.unit, args, &un));
+        if (failed) {
+            if (lane == 0) raise_error(args.err, abort, kErrProducer);
+            settle_after_abort();
+        }
     } else if (GRAD && warp == 2) {
         // ---------------- ragged ends: clear the rows past the group's ----------------
         int issued = 0;
@@ -351,23 +375,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int KIND>
-int launch_kind(const CUtensorMap& w, const CUtensorMap& a, const CUtensorMap& c,
-                const ProductArgs& args, int units, cudaStream_t st) {
+int launch_kind(const CUtensorMap& w, const CUtensorMap& a, const CUtensorMap& a128,
+                const CUtensorMap& c, const ProductArgs& args, int units, cudaStream_t st) {
     static std::atomic<uint64_t> opted{0};
     const cudaError_t e = opt_in_smem(pair_kernel<KIND>, kSmemBytes, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
     return launch_cluster(pair_kernel<KIND>, 2, dim3(static_cast<unsigned>(2 * units)),
-                          dim3(kThreads), kSmemBytes, st, w, a, c, args);
+                          dim3(kThreads), kSmemBytes, st, w, a, a128, c, args);
 }
 
 }  // namespace
 
 int launch_pair(int kind, const CUtensorMap& weight, const CUtensorMap& rows,
-                const CUtensorMap& out, const ProductArgs& args, int units, cudaStream_t st) {
+                const CUtensorMap& rows128, const CUtensorMap& out, const ProductArgs& args,
+                int units, cudaStream_t st) {
     switch (kind) {
-        case kWeight16KN: return launch_kind<kWeight16KN>(weight, rows, out, args, units, st);
-        case kWeight16NK: return launch_kind<kWeight16NK>(weight, rows, out, args, units, st);
-        default: return launch_kind<kWeightGrad>(weight, rows, out, args, units, st);
+        case kWeight16KN:
+            return launch_kind<kWeight16KN>(weight, rows, rows128, out, args, units, st);
+        case kWeight16NK:
+            return launch_kind<kWeight16NK>(weight, rows, rows128, out, args, units, st);
+        default: return launch_kind<kWeightGrad>(weight, rows, rows128, out, args, units, st);
     }
 }
 

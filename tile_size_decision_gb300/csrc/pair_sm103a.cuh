@@ -22,21 +22,24 @@ constexpr int kBoxBytes = 32 * 64;
 constexpr int kStagingBytes = 8 * kBoxBytes;
 constexpr int kBarrierBytes = 768;
 constexpr int kSideSlots = 16;
+// Answers about the next unit that are kept: the loads can be two units ahead of
+// the epilogue, whose warps free an answer last, as short units need.
+constexpr int kAnswers = 3;
 
 struct PairBarriers {
     uint64_t full[kStages], empty[kStages], acc_full[4], acc_empty[4];
     uint64_t side_full[kSideSlots], side_empty[kSideSlots];   // scales (8-bit), ragged ends (gradient)
     uint64_t drain;
-    uint64_t next_full[2], next_empty[2];
-    ulonglong2 next[2];                               // answers about the next unit
+    uint64_t next_full[kAnswers], next_empty[kAnswers];
+    ulonglong2 next[kAnswers];                        // answers about the next unit
     uint32_t tmem_base;
     int abort;
 };
 static_assert(sizeof(PairBarriers) <= kBarrierBytes, "barrier block too large");
 
 // The pair's units in turn: its own, then those of clusters that have not
-// started yet, which the leader's TMA warp claims a unit ahead.  Every role's
-// warp walks through the same answers.  (The units are uneven where groups
+// started yet, which a warp of the leader claims a unit or two ahead.  Every role's warp walks through the
+// same answers.  (The units are uneven where groups
 // are: a fixed assignment left pairs idle for a fifth of the time on the
 // weight gradient of 16 uneven groups.)
 struct Walk {
@@ -52,12 +55,10 @@ struct Walk {
             return false;
         }
         const int x = ptx::cancelled_cta_x(&bar->next[slot]);
-        // Read before the next answer is written here (by the async proxy).
-        ptx::fence_proxy_async_smem();
         __syncwarp();
         if ((threadIdx.x & 31) == 0)
             ptx::mbar_arrive_remote(ptx::map_to_cta(ptx::smem_addr(&bar->next_empty[slot]), 0));
-        if (++slot == 2) { slot = 0; phase ^= 1u; }
+        if (++slot == kAnswers) { slot = 0; phase ^= 1u; }
         unit = x >> 1;
         return x >= 0;
     }
@@ -73,13 +74,16 @@ struct Asker {
                         ptx::mbar_wait(&bar->next_empty[slot], phase ^ 1u, abort, limit)))
             return false;
         if ((threadIdx.x & 31) == 0) {
+            // The walkers' reads of the last answer here come before the
+            // async proxy's write of the next.
+            ptx::fence_proxy_async();
             ptx::mbar_arrive_expect_tx(&bar->next_full[slot], 16);
             ptx::mbar_arrive_expect_tx_cluster(
                 ptx::map_to_cta(ptx::smem_addr(&bar->next_full[slot]), 1), 16);
             ptx::try_cancel_cluster(&bar->next[slot], &bar->next_full[slot]);
         }
         __syncwarp();
-        if (++slot == 2) { slot = 0; phase ^= 1u; }
+        if (++slot == kAnswers) { slot = 0; phase ^= 1u; }
         return true;
     }
 };
@@ -105,7 +109,7 @@ __device__ __forceinline__ void pair_setup(PairBarriers* bar, int stage_arrivals
             ptx::mbar_init(&bar->acc_full[i], 1);
             ptx::mbar_init(&bar->acc_empty[i], 2 * readers);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kAnswers; ++i) {
             ptx::mbar_init(&bar->next_full[i], 1);
             ptx::mbar_init(&bar->next_empty[i], walkers);
         }

@@ -155,7 +155,7 @@ Choice choose(int kind, int64_t m, int64_t n, int64_t k, int64_t groups, int sms
     }
     // Pairs: 8-bit tiles as narrow as the rounds allow, in either kernel.
     struct Pair { int most, least; double start, round, block; };
-    static constexpr Pair pair16[] = {{256, 256, 2940, 1840, 250}};
+    static constexpr Pair pair16[] = {{256, 256, 2940, 1400, 250}};
     static constexpr Pair pair8[] = {{256, 160, 3970, 1620, 460}, {128, 64, 3500, 1100, 300}};
     for (int i = 0; i < (fp8 ? 2 : 1); ++i) {
         const Pair& p = fp8 ? pair8[i] : pair16[i];
@@ -220,12 +220,12 @@ int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_b
                                       : (d->m + choice.rows - 1) / choice.rows;
     const int64_t units = row_tiles * args.n_blocks;
     if (units > INT32_MAX / 16) return fail(TILES_ERR_TOO_LARGE, "too many output tiles");
-    // Boxes: one operand of a stage (MN-major: 64-column atoms), except the
-    // MMA's N operand of a pair, whose tile ends anywhere (32 rows).
+    // Boxes: one operand of a stage (MN-major: 64-column atoms).  In pairs half a
+    // tile's columns (8 bits), and rows by 128 or, as a tile ends anywhere, by 32.
     const bool pair = choice.pair;
     CUtensorMap tw, ta;
     s = encode_box(&tw, map_type(d->in_dtype), d->b, kn ? d->n : d->k, kn ? d->k : d->n, groups,
-                   d->ldb * eb, stride_b * eb, kn ? 64 : bk, kn ? 64 : pair && fp8 ? 32 : 128);
+                   d->ldb * eb, stride_b * eb, kn ? 64 : bk, kn ? 64 : pair && fp8 ? choice.cols / 2 : 128);
     if (s != TILES_OK) return s;
     s = encode_box(&ta, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
                    !pair ? choice.rows : fp8 ? 128 : 32);
@@ -241,9 +241,13 @@ int run_product(const tiles_product_desc* d, bool grouped, void* ws, size_t ws_b
     args.tile_cols = choice.cols;
     CUtensorMap tc{};
     args.tma_store = encode_out_boxes(&tc, d->out_dtype, d->c, d->n, d->m, 1, d->ldc, d->ldc);
-    return launch_status(fp8 ? launch_pair8(tw, ta, tc, args, static_cast<int>(units), st)
-                             : launch_pair(kind, tw, ta, tc, args, static_cast<int>(units), st),
-                         what);
+    if (fp8)
+        return launch_status(launch_pair8(tw, ta, tc, args, static_cast<int>(units), st), what);
+    CUtensorMap ta128;
+    s = encode_box(&ta128, map_type(d->in_dtype), d->a, d->k, d->m, 1, d->lda * eb, d->lda * eb, bk,
+                   128);
+    if (s != TILES_OK) return s;
+    return launch_status(launch_pair(kind, tw, ta, ta128, tc, args, static_cast<int>(units), st), what);
 }
 
 }  // namespace
@@ -320,7 +324,7 @@ int tiles_grouped_wgrad(const tiles_wgrad_desc* d, void* ws, size_t ws_bytes, vo
     CUtensorMap tc{};
     args.tma_store = encode_out_boxes(&tc, d->out_dtype, d->dw, d->n, d->k, d->groups, d->lddw,
                                       d->groups > 1 ? d->stride_dw : d->lddw);
-    return launch_status(launch_pair(kWeightGrad, tw, ta, tc, args, static_cast<int>(units),
+    return launch_status(launch_pair(kWeightGrad, tw, ta, ta, tc, args, static_cast<int>(units),
                                      static_cast<cudaStream_t>(stream)),
                          "grouped weight gradient");
 }

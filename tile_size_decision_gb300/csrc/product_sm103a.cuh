@@ -140,9 +140,11 @@ int launch_stream(int kind, int tile_rows, const CUtensorMap& weight, const CUte
                   const ProductArgs& args, int64_t units, cudaStream_t st);
 
 // The 16-bit kernel on CTA pairs: tiles of 256 weight columns by up to 256
-// rows (weight gradient: dc's columns by a's); units is an upper bound.
+// rows (weight gradient: dc's columns by a's); units is an upper bound.  rows
+// has boxes of 32 rows, rows128 of 128 (weight gradient: not used).
 int launch_pair(int kind, const CUtensorMap& weight, const CUtensorMap& rows,
-                const CUtensorMap& out, const ProductArgs& args, int units, cudaStream_t st);
+                const CUtensorMap& rows128, const CUtensorMap& out, const ProductArgs& args,
+                int units, cudaStream_t st);
 // The 8-bit kernel on CTA pairs: tiles of 256 rows by args.tile_cols weight
 // rows; units is an upper bound.
 int launch_pair8(const CUtensorMap& weight, const CUtensorMap& rows, const CUtensorMap& out,
