@@ -39,9 +39,8 @@ namespace {
 
 constexpr int kScaleSlots = kSideSlots;
 // K blocks whose scales are on their way in.  The scale warp walks the units
-// that much ahead of the epilogue, and no role is more than two units ahead of
-// another (the answers' ring): with few K blocks a unit it must not wait for
-// more, 2 x K blocks at most.
+// that much ahead of the epilogue, and no role gets more than kAnswers units
+// ahead of another: with few K blocks a unit it must not wait for more.
 constexpr int kScaleLag = 10, kScaleLagShort = 2;
 constexpr int kSlotFloats = 128 + 8;                  // 128 rows, 8 chunks of 32 columns
 constexpr int kScaleBytes = kScaleSlots * kSlotFloats * 4;
