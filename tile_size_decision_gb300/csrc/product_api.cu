@@ -155,7 +155,7 @@ Choice choose(int kind, int64_t m, int64_t n, int64_t k, int64_t groups, int sms
     }
     // Pairs: 8-bit tiles as narrow as the rounds allow, in either kernel.
     struct Pair { int most, least; double start, round, block; };
-    static constexpr Pair pair16[] = {{256, 256, 2940, 1400, 250}};
+    static constexpr Pair pair16[] = {{256, 256, 4400, 1350, 250}};
     static constexpr Pair pair8[] = {{256, 160, 3970, 1620, 460}, {128, 64, 3500, 1100, 300}};
     for (int i = 0; i < (fp8 ? 2 : 1); ++i) {
         const Pair& p = fp8 ? pair8[i] : pair16[i];
