@@ -41,7 +41,10 @@ static_assert(sizeof(PairBarriers) <= kBarrierBytes, "barrier block too large");
 // started yet, which a warp of the leader claims a unit or two ahead.  Every role's warp walks through the
 // same answers.  (The units are uneven where groups
 // are: a fixed assignment left pairs idle for a fifth of the time on the
-// weight gradient of 16 uneven groups.)
+// weight gradient of 16 uneven groups.)  The answers come in no promised order.
+// A walk may end at the first one past the last unit all the same: each is
+// awaited before the next is asked for, so no later one is lost, and clusters
+// that nobody claimed start by themselves.
 struct Walk {
     int unit;
     uint32_t slot = 0, phase = 0;

@@ -9,6 +9,7 @@
 #include "gemm_sm103a.cuh"
 #include "launch_util.h"
 #include "op_ptx.cuh"
+#include "row_tiles.h"
 
 namespace tiles {
 
@@ -51,81 +52,18 @@ __device__ __forceinline__ uint64_t wait_limit(const ProductArgs& a) {
                ? after : a.wait_limit_ns;
 }
 
-// Rows [row0, end) of one tile of `group`.
-struct RowTile { int group, row0, end; };
-
-__device__ __forceinline__ int clamp_offset(int v, int m) { return min(max(v, 0), m); }
-
-// Tile `want` among the groups' tiles of `tile_rows` rows, in group order; a
-// warp looks at 32 groups at a time.  False past the last tile.
-__device__ __forceinline__ bool find_row_tile(const int32_t* offsets, int groups, int m,
-                                              int tile_rows, int want, RowTile* out) {
-    const int lane = threadIdx.x & 31;
-    int base = 0;
-    for (int g0 = 0; g0 < groups; g0 += 32) {
-        const int g = g0 + lane;
-        int lo = 0, hi = 0;
-        if (g < groups) {
-            lo = clamp_offset(offsets[g], m);
-            hi = clamp_offset(offsets[g + 1], m);
-        }
-        const int tiles = hi > lo ? (hi - lo + tile_rows - 1) / tile_rows : 0;
-        int upto = tiles;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += t;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, want < base + upto);
-        if (past) {
-            const int src = __ffs(past) - 1;
-            const int first = base + __shfl_sync(0xffffffffu, upto - tiles, src);
-            out->group = g0 + src;
-            out->row0 = __shfl_sync(0xffffffffu, lo, src) + (want - first) * tile_rows;
-            out->end = __shfl_sync(0xffffffffu, hi, src);
-            return true;
-        }
-        base += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return false;
-}
-
-// The same lookup for increasing `want`: a warp keeps the 32 groups it is at
-// in registers, so that a step costs a vote and shuffles.
-struct RowTileCursor {
-    int base = 0, g0 = -32;           // tiles before the chunk; its first group
-    int lo = 0, hi = 0, upto = 0, tiles = 0, total = 0;
-
-    __device__ __forceinline__ bool seek(const int32_t* offsets, int groups, int m, int tile_rows,
-                                         int want, RowTile* out) {
-        const int lane = threadIdx.x & 31;
-        while (want >= base + total) {
-            g0 += 32;
-            if (g0 >= groups) { g0 = groups; total = 0; return false; }
-            base += total;
-            const int g = g0 + lane;
-            lo = hi = 0;
-            if (g < groups) {
-                lo = clamp_offset(offsets[g], m);
-                hi = clamp_offset(offsets[g + 1], m);
-            }
-            tiles = hi > lo ? (hi - lo + tile_rows - 1) / tile_rows : 0;
-            upto = tiles;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += t;
-            }
-            total = __shfl_sync(0xffffffffu, upto, 31);
-        }
-        const int src = __ffs(__ballot_sync(0xffffffffu, want < base + upto)) - 1;
-        const int first = base + __shfl_sync(0xffffffffu, upto - tiles, src);
-        out->group = g0 + src;
-        out->row0 = __shfl_sync(0xffffffffu, lo, src) + (want - first) * tile_rows;
-        out->end = __shfl_sync(0xffffffffu, hi, src);
-        return true;
-    }
+// The lanes of a warp, as the lookup of a row tile uses them.
+struct WarpLanes {
+    static __device__ __forceinline__ int lane() { return threadIdx.x & 31; }
+    static __device__ __forceinline__ unsigned ballot(bool p) { return __ballot_sync(0xffffffffu, p); }
+    static __device__ __forceinline__ int first(unsigned mask) { return __ffs(mask) - 1; }
+    static __device__ __forceinline__ int shfl(int v, int src) { return __shfl_sync(0xffffffffu, v, src); }
+    static __device__ __forceinline__ int shfl_up(int v, int d) { return __shfl_up_sync(0xffffffffu, v, d); }
 };
+
+// A pair's units come from cluster launch control, which promises a cluster
+// that has not started and no order among them.
+using RowTileCursor = RowTileLookup<WarpLanes>;
 
 // One value in the output's type.
 __device__ __forceinline__ void store_one(void* c, int64_t at, float v, int dtype) {

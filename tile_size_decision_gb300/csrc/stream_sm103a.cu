@@ -131,8 +131,10 @@ __global__ void __launch_bounds__(kThreads)
     if (warp == 2) {
         RowTile rt{0, row_tile * NT, args.m};
         bool found = true;
-        if (args.groups > 0)
-            found = find_row_tile(args.offsets, args.groups, args.m, NT, row_tile, &rt);
+        if (args.groups > 0) {
+            RowTileCursor cursor;
+            found = cursor.seek(args.offsets, args.groups, args.m, NT, row_tile, &rt);
+        }
         if (lane == 0) {
             bar->group = rt.group;
             bar->row0 = rt.row0;
