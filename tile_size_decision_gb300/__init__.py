@@ -194,6 +194,16 @@ def workspace(device=None):
                        device=device if device is not None else "cuda")
 
 
+def _workspace_args(workspace):
+    """Address and bytes of a workspace, which the kernels write: every byte it
+    counts has to be its own, and on the GPU."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.nbytes
+
+
 def _cfg_ptr(cfg):
     return C.byref(cfg) if cfg is not None else None
 
@@ -239,8 +249,7 @@ def gemm(a, b, out=None, out_dtype=None, cfg=None, workspace=None, stream=None):
     if out is None:
         out = _alloc_out((a.shape[0], b.shape[1]), a, out_dtype)
     d = _gemm_desc(a, b, out, batched=False)
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _workspace_args(workspace)
     _check(load().tiles_gemm(C.byref(d), _cfg_ptr(cfg), ws, wsb, _stream_handle(stream)),
            "tiles_gemm")
     return out
@@ -254,8 +263,7 @@ def gemm_autotune(a, b, out, top_k=4, reps=5, workspace=None, stream=None, batch
     if batched is None:
         batched = a.dim() == 3
     d = _gemm_desc(a, b, out, batched=batched)
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _workspace_args(workspace)
     cap = 3 * top_k
     res = (_abi.TuneResult * cap)()
     n = C.c_int(0)
@@ -302,8 +310,7 @@ def gemm_batched(a, b, out=None, out_dtype=None, cfg=None, workspace=None, strea
     if out is None:
         out = _alloc_out((a.shape[0], a.shape[1], b.shape[2]), a, out_dtype)
     d = _gemm_desc(a, b, out, batched=True)
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _workspace_args(workspace)
     _check(load().tiles_gemm_batched(C.byref(d), _cfg_ptr(cfg), ws, wsb, _stream_handle(stream)),
            "tiles_gemm_batched")
     return out
@@ -325,8 +332,7 @@ def gemm_host(a_host, b_host, out_host, a_dev, b_dev, out_dev, cfg=None, workspa
     for h, dv, nm in ((a_host, a_dev, "a"), (b_host, b_dev, "b"), (out_host, out_dev, "out")):
         _mirror(h, dv, nm)
     d = _gemm_desc(*_batched3(a_dev, b_dev, out_dev), batched=True)
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _workspace_args(workspace)
     _check(load().tiles_gemm_host(C.byref(d), _cfg_ptr(cfg), a_host.data_ptr(), b_host.data_ptr(),
                                   out_host.data_ptr(), chunks, ws, wsb, _stream_handle(stream)),
            "tiles_gemm_host")
@@ -342,8 +348,7 @@ def conv2d_host(x_host, w_host, y_host, x_dev, w_dev, y_dev, stride=(1, 1), pad=
     for h, dv, nm in ((x_host, x_dev, "x"), (w_host, w_dev, "w"), (y_host, y_dev, "y")):
         _mirror(h, dv, nm)
     d = _conv_desc(x_dev, w_dev, stride, pad, dil, y_dev, layout)
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _workspace_args(workspace)
     _check(load().tiles_conv2d_host(C.byref(d), tile_oh, _cfg_ptr(cfg), x_host.data_ptr(),
                                     w_host.data_ptr(), y_host.data_ptr(), chunks, ws, wsb,
                                     _stream_handle(stream)),
@@ -431,8 +436,7 @@ def conv2d_htiled(x, w, stride=(1, 1), pad=(0, 0), dil=(1, 1), tile_oh=16, out=N
     if not out.is_contiguous() or tuple(out.shape) != shape:
         raise ValueError("out must be contiguous with shape (n, c_out, oh, ow)")
     d = _conv_desc(x, w, stride, pad, dil, out, layout)
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _workspace_args(workspace)
     _check(load().tiles_conv2d_htiled(C.byref(d), tile_oh, _cfg_ptr(cfg), ws, wsb,
                                       _stream_handle(stream)), "tiles_conv2d_htiled")
     return out
@@ -449,8 +453,7 @@ def conv2d_tiled(x, w, stride=(1, 1), pad=(0, 0), dil=(1, 1), tile_oh=16, tile_o
     if not out.is_contiguous() or tuple(out.shape) != shape:
         raise ValueError("out must be contiguous with shape (n, c_out, oh, ow)")
     d = _conv_desc(x, w, stride, pad, dil, out, layout)
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _workspace_args(workspace)
     _check(load().tiles_conv2d_tiled(C.byref(d), tile_oh, tile_ow, tile_n, _cfg_ptr(cfg), ws,
                                      wsb, _stream_handle(stream)), "tiles_conv2d_tiled")
     return out
@@ -467,7 +470,7 @@ def gemm_schedule(a, b, out, cfg=None, workspace=None):
     tensors count as a batch of one)."""
     d = _gemm_desc(*_batched3(a, b, out), batched=True)
     sch = _abi.Schedule()
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _, wsb = _workspace_args(workspace)
     _check(load().tiles_gemm_schedule(C.byref(d), _cfg_ptr(cfg), wsb, C.byref(sch)),
            "tiles_gemm_schedule")
     return sch
@@ -499,12 +502,12 @@ def gemm_noalloc(a, b, out=None, out_dtype=None, cfg=None, stream=None, wait=Fal
 
 def check(workspace=None, stream=None) -> None:
     """Synchronise and raise TilesError if a kernel's bounded wait expired."""
-    ws = workspace.data_ptr() if workspace is not None else None
+    ws, _ = _workspace_args(workspace)
     _check(load().tiles_check(ws, _stream_handle(stream)), "tiles_check")
 
 
 def selftest_wait_timeout(workspace, limit_ns: int, stream=None) -> None:
-    _check(load().tiles_selftest_wait_timeout(workspace.data_ptr(), limit_ns,
+    _check(load().tiles_selftest_wait_timeout(_workspace_args(workspace)[0], limit_ns,
                                               _stream_handle(stream)),
            "tiles_selftest_wait_timeout")
 
@@ -572,12 +575,6 @@ def _raw_stream(stream):
     if _RAW_STREAM is None:
         _stream_handle(None)
     return _RAW_STREAM()
-
-
-def _workspace_args(workspace):
-    if workspace is None:
-        return None, 0
-    return workspace.data_ptr(), workspace.nbytes
 
 
 def _blocks(n):

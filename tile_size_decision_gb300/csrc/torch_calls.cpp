@@ -124,6 +124,7 @@ struct Workspace {
 
     explicit Workspace(PyObject* o) {
         if (const at::Tensor* t = optional_tensor(o)) {
+            require(t->is_contiguous());           // every byte it counts is its own
             at = t->data_ptr();
             bytes = t->nbytes();
         }
