@@ -36,3 +36,11 @@ def test_the_calls_on_a_workspace_alone_refuse_it_too():
         T.check(t)
     with pytest.raises(ValueError, match="workspace"):
         T.selftest_wait_timeout(t, 1000)
+
+
+def test_a_convolution_writes_to_the_gpu_only():
+    x, w = Stand(torch.zeros(1, 4, 6, 6).half()), Stand(torch.zeros(4, 4, 3, 3).half())
+    y = torch.zeros(1, 4, 4, 4).half()
+    assert T._conv_desc(x, w, (1, 1), (0, 0), (1, 1), Stand(y), "nchw").y == y.data_ptr()
+    with pytest.raises(ValueError, match="out"):
+        T._conv_desc(x, w, (1, 1), (0, 0), (1, 1), y, "nchw")

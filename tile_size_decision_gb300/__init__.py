@@ -403,6 +403,8 @@ def _conv_desc(x, w, stride, pad, dil, out, layout):
     d.x_layout = _abi.LAYOUT_NHWC if layout == "nhwc" else _abi.LAYOUT_NCHW
     d.x, d.wt = x.data_ptr(), w.data_ptr()
     if out is not None:
+        if not out.is_cuda or not out.is_contiguous():
+            raise ValueError("out must be a contiguous CUDA tensor")
         d.y = out.data_ptr()
         d.out_dtype = _dtype_code(out)
     return d
