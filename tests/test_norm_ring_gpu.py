@@ -1,0 +1,61 @@
+"""GPU parity of the norm's kernel for many long 16-bit rows, whose blocks take
+several rows in turn: every output against the float64 definition, at the
+tolerances of test_norm_gpu (derived there), and through the C call where the
+Python one does not go."""
+
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from oracle import operators as OO
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import tile_size_decision_gb300 as T  # noqa: E402
+from tile_size_decision_gb300 import _abi  # noqa: E402
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+CODE = {"f16": _abi.F16, "bf16": _abi.BF16, "f32": _abi.F32}
+
+
+def draw(shape, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(DT[dtype])
+
+
+def c_norm(x, w, residual, h, fp8, dtype):
+    """tiles_rmsnorm with every pointer as given; (y, scales)."""
+    rows, cols = x.shape
+    y = torch.empty((rows, cols), dtype=torch.float8_e4m3fn if fp8 else DT[dtype], device="cuda")
+    s = torch.empty((rows, OO.blocks(cols)), device="cuda")
+    d = _abi.RmsnormDesc(rows=rows, cols=cols, x=x.data_ptr(), weight=w.data_ptr(),
+                         residual=residual.data_ptr() if residual is not None else None,
+                         h=h.data_ptr() if h is not None else None, y=y.data_ptr(),
+                         scales=s.data_ptr() if fp8 else None, ldx=x.stride(0), ldr=cols,
+                         ldh=h.stride(0) if h is not None else 0, ldy=cols,
+                         scale_row=OO.blocks(cols), scale_block=1, eps=1e-6, dtype=CODE[dtype],
+                         weight_dtype=CODE[dtype], out_dtype=_abi.E4M3 if fp8 else CODE[dtype])
+    stream = C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert T.load().tiles_rmsnorm(C.byref(d), stream) == _abi.OK
+    return y, s
+
+
+# Few rows and many, rows that start on 16 bytes and rows that do not, 16 bits
+# and 32: every kernel that may run.
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(3, 1024), (700, 1024), (700, 1001), (700, 8192), (400, 256),
+                                       (2, 40000)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_h_without_a_residual_is_x(rows, cols, dtype, fp8):
+    x, w = draw((rows, cols), dtype, 1), draw((cols,), dtype, 2)
+    want, ws = c_norm(x, w, None, None, fp8, dtype)
+    h = torch.full((rows, cols + 8), 7.0, dtype=DT[dtype], device="cuda")
+    y, s = c_norm(x, w, None, h[:, :cols], fp8, dtype)
+    assert torch.equal(h[:, :cols], x) and bool((h[:, cols:] == 7.0).all())
+    assert torch.equal(y.view(torch.uint8), want.view(torch.uint8))
+    assert not fp8 or torch.equal(s, ws)

@@ -415,8 +415,8 @@ __global__ void __launch_bounds__(kRingThreads)
                 ring.read(slot, 1, j, c < cols, threads, q);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[j][i] += q[i];
-                if (a.h) store8<T, true>(static_cast<T*>(a.h) + row * a.ldh, c, cols, v[j]);
             }
+            if (a.h) store8<T, true>(static_cast<T*>(a.h) + row * a.ldh, c, cols, v[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sum[0] += v[j][i] * v[j][i];
