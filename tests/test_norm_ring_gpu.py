@@ -59,3 +59,21 @@ def test_h_without_a_residual_is_x(rows, cols, dtype, fp8):
     assert torch.equal(h[:, :cols], x) and bool((h[:, cols:] == 7.0).all())
     assert torch.equal(y.view(torch.uint8), want.view(torch.uint8))
     assert not fp8 or torch.equal(s, ws)
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+@pytest.mark.parametrize("norm", ["rmsnorm", "rmsnorm_fp8"])
+def test_h_out_without_a_residual_is_written(norm, compiled, monkeypatch):
+    T._compiled()
+    if not compiled:
+        monkeypatch.setattr(T, "_CALLS", T._NoCalls)
+    x, w = draw((5, 304), "bf16", 3), draw((304,), "bf16", 4)
+    out = torch.full((5, 320), 7.0, dtype=torch.bfloat16, device="cuda")
+    view = out[:, :304]
+    h = getattr(T, norm)(x, w, h_out=view)[-1]
+    assert h is view and torch.equal(h, x) and bool((out[:, 304:] == 7.0).all())
+    assert getattr(T, norm)(x, w)[-1] is x
+    with pytest.raises((ValueError, TypeError)):
+        getattr(T, norm)(x, w, h_out=out)
+    with pytest.raises((ValueError, TypeError)):
+        getattr(T, norm)(x, w, h_out=view.half())

@@ -644,13 +644,15 @@ def _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, fp8):
     if residual is not None:
         _, _, ldr, ur = _matrix(residual, "residual")
         ok = ur == 1 and residual.shape == shape and residual.dtype == dtype and residual.is_cuda
+        pr = residual.data_ptr()
         if h_out is None:
             h, ldh = torch.empty(shape, dtype=dtype, device=device), cols
-        else:
-            h = h_out
-            _, _, ldh, uh = _matrix(h, "h_out")
-            ok = ok and uh == 1 and h.shape == shape and h.dtype == dtype and h.is_cuda
-        pr, ph = residual.data_ptr(), h.data_ptr()
+            ph = h.data_ptr()
+    if h_out is not None:
+        h = h_out
+        _, _, ldh, uh = _matrix(h, "h_out")
+        ok = ok and uh == 1 and h.shape == shape and h.dtype == dtype and h.is_cuda
+        ph = h.data_ptr()
     if given:
         ok = ok and uy == 1 and out.shape == shape and out.is_cuda and \
             out.dtype == (torch.float8_e4m3fn if fp8 else dtype)
@@ -669,7 +671,8 @@ def _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, fp8):
 def rmsnorm(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=None):
     """h = x + residual and y = h * (mean(h^2) + eps)^(-1/2) * weight, row by
     row of a matrix; returns (y, h) in x's type.  Without a residual h is x
-    itself.  h_out may be the residual (updated in place)."""
+    itself, or a copy of it in h_out.  h_out may be the residual (updated in
+    place)."""
     r = (_CALLS or _compiled()).rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
     if r is None:
         r = _rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)

@@ -223,15 +223,15 @@ PyObject* rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
             require(m.like(mx) && residual->scalar_type() == dtype);
             d.residual = residual->data_ptr();
             d.ldr = m.ld;
-            if (h_out) {
-                const Matrix mh(*h_out);
-                require(mh.like(mx) && h_out->scalar_type() == dtype);
-                d.ldh = mh.ld;
-            } else {
-                d.ldh = mx.cols;
+            if (!h_out) {
                 new_h = empty_matrix(x, mx.rows, mx.cols, mx.cols, dtype);
                 h_out = &new_h;
             }
+        }
+        if (h_out) {
+            const Matrix mh(*h_out);
+            require(mh.like(mx) && h_out->scalar_type() == dtype);
+            d.ldh = mh.ld;
             d.h = h_out->data_ptr();
         }
         d.x = x.data_ptr();
@@ -239,9 +239,8 @@ PyObject* rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         d.y = out->data_ptr();
         void* stream = stream_of(args[7]);
         run([&] { return calls.rmsnorm(&d, stream); });
-        PyObject* h = !residual         ? given(args[0])
-                      : new_h.defined() ? THPVariable_Wrap(std::move(new_h))
-                                        : given(args[6]);
+        PyObject* h = new_h.defined() ? THPVariable_Wrap(std::move(new_h))
+                                      : given(h_out ? args[6] : args[0]);
         PyObject* y = new_out.defined() ? THPVariable_Wrap(std::move(new_out)) : given(args[4]);
         PyObject* s = new_scales.defined() ? THPVariable_Wrap(std::move(new_scales)) : given(args[5]);
         PyObject* r = PyTuple_New(3);
