@@ -10,6 +10,7 @@ streams.  Names follow the C ABI without the ``tiles_`` prefix.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import struct
@@ -185,6 +186,17 @@ def _stream_handle(stream):
             cur = _torch().cuda.current_stream
             _RAW_STREAM = lambda: cur().cuda_stream
     return C.c_void_p(_RAW_STREAM())
+
+
+def _on(stream):
+    """New outputs within come from the pool of the stream that a call names, as
+    those of any operation on it do.  (From the current stream's pool they
+    could be memory that work pending there still uses.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    cuda = _torch().cuda
+    return cuda.stream(stream if isinstance(stream, cuda.Stream) else
+                       cuda.ExternalStream(stream.cuda_stream))
 
 
 def workspace(device=None):
@@ -528,6 +540,10 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
 # without Python objects in between), which returns None for what it does not
 # take.  The Python function then makes the same call the long way, where
 # _refuse finds what is wrong with the arguments.
+#
+# A call runs on `stream`, or on the current stream.  Its new outputs belong to
+# that stream, as after any PyTorch operation on it: used on another one, they
+# are the caller's to order (wait_stream, record_stream).
 
 
 class _NoCalls:
@@ -675,7 +691,8 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, out=None, h_out=None, stream=Non
     place)."""
     r = (_CALLS or _compiled()).rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
     if r is None:
-        r = _rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
+        with _on(stream):
+            r = _rmsnorm(x, weight, residual, eps, out, None, h_out, stream, False)
     return r[0], r[2]
 
 
@@ -686,8 +703,10 @@ def rmsnorm_fp8(x, weight, residual=None, eps=1e-6, out=None, scales=None, h_out
     scales are stored block by block (a transposed view, rows x blocks),
     which the products read fastest."""
     r = (_CALLS or _compiled()).rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, True)
-    return r if r is not None else _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream,
-                                            True)
+    if r is None:
+        with _on(stream):
+            r = _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, True)
+    return r
 
 
 def rmsnorm_grad_workspace(x):
@@ -723,12 +742,14 @@ def rmsnorm_grad(dy, h, weight, eps=1e-6, dh=None, dx_out=None, dweight_out=None
         pdh = dh.data_ptr()
     dx, dw = dx_out, dweight_out
     if dx is None:
-        dx, lddx = torch.empty(shape, dtype=dtype, device=h.device), cols
+        with _on(stream):
+            dx, lddx = torch.empty(shape, dtype=dtype, device=h.device), cols
     else:
         _, _, lddx, u = _matrix(dx, "dx_out")
         ok = ok and u == 1 and dx.shape == shape and dx.dtype == dtype and dx.is_cuda
     if dw is None:
-        dw = torch.empty(cols, dtype=torch.float32, device=h.device)
+        with _on(stream):
+            dw = torch.empty(cols, dtype=torch.float32, device=h.device)
     else:
         ok = ok and dw.shape == (cols,) and dw.dtype == torch.float32 and dw.is_cuda and \
             (cols == 1 or dw.stride(0) == 1)
@@ -761,13 +782,14 @@ def quantize_fp8(x, block_rows=1, stream=None):
     *lead, rows, cols = x.shape
     batch = lead[0] if lead else 1
     pitch = (cols + 15) // 16 * 16
-    q = torch.empty((*lead, rows, pitch), dtype=torch.float8_e4m3fn, device=x.device)[..., :cols]
     nb = _blocks(cols)
-    if block_rows == 1:
-        scales = torch.empty((*lead, nb, rows), dtype=torch.float32,
-                             device=x.device).transpose(-1, -2)
-    else:
-        scales = torch.empty((*lead, _blocks(rows), nb), dtype=torch.float32, device=x.device)
+    with _on(stream):
+        q = torch.empty((*lead, rows, pitch), dtype=torch.float8_e4m3fn, device=x.device)[..., :cols]
+        if block_rows == 1:
+            scales = torch.empty((*lead, nb, rows), dtype=torch.float32,
+                                 device=x.device).transpose(-1, -2)
+        else:
+            scales = torch.empty((*lead, _blocks(rows), nb), dtype=torch.float32, device=x.device)
     d = _abi.QuantizeDesc(batch, rows, cols, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
                           x.stride(-2) if rows > 1 else max(x.stride(-2), cols),
                           x.stride(0) if lead else 0, pitch, q.stride(0) if lead else 0,
@@ -851,8 +873,11 @@ def gemm_fp8(a, a_scales, b, b_scales, out=None, out_dtype=None, workspace=None,
     unless out_dtype ("f32", "f16", "bf16") says otherwise."""
     r = (_CALLS or _compiled()).product_fp8(a, a_scales, b, b_scales, None, out, out_dtype,
                                             workspace, stream)
-    return r if r is not None else _product_fp8(a, a_scales, b, b_scales, None, out, out_dtype,
-                                                workspace, stream, "tiles_gemm_fp8")
+    if r is None:
+        with _on(stream):
+            r = _product_fp8(a, a_scales, b, b_scales, None, out, out_dtype, workspace, stream,
+                             "tiles_gemm_fp8")
+    return r
 
 
 def grouped_gemm_fp8(a, a_scales, b, b_scales, offsets, out=None, out_dtype=None, workspace=None,
@@ -862,8 +887,11 @@ def grouped_gemm_fp8(a, a_scales, b, b_scales, offsets, out=None, out_dtype=None
     only the kernel reads.  Rows outside every group are not written."""
     r = (_CALLS or _compiled()).product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype,
                                             workspace, stream)
-    return r if r is not None else _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype,
-                                                workspace, stream, "tiles_grouped_gemm")
+    if r is None:
+        with _on(stream):
+            r = _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype, workspace, stream,
+                             "tiles_grouped_gemm")
+    return r
 
 
 def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspace=None,
@@ -891,7 +919,8 @@ def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspa
     else:
         dt = dtype if out_dtype is None else \
             out_dtype if isinstance(out_dtype, torch.dtype) else _TYPES(torch)[out_dtype]
-        out, ldc = torch.empty((m, n), dtype=dt, device=a.device), n
+        with _on(stream):
+            out, ldc = torch.empty((m, n), dtype=dt, device=a.device), n
     if not (ok and ua == 1 and ub == 1 and bk == k and b.dtype == dtype and dtype in codes and
             a.is_cuda and b.is_cuda and offsets.shape == (groups + 1,) and offsets.is_cuda and
             offsets.dtype == torch.int32 and offsets.stride(0) == 1):
@@ -929,7 +958,8 @@ def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stre
     else:
         dt = dtype if out_dtype is None else \
             out_dtype if isinstance(out_dtype, torch.dtype) else _TYPES(torch)[out_dtype]
-        out = torch.empty((groups, k, n), dtype=dt, device=a.device)
+        with _on(stream):
+            out = torch.empty((groups, k, n), dtype=dt, device=a.device)
         ldw, stride_dw = n, k * n
     if not (ok and ua == 1 and ud == 1 and md == m and dc.dtype == dtype and dtype in codes and
             a.is_cuda and dc.is_cuda and offsets.is_cuda and offsets.dtype == torch.int32 and

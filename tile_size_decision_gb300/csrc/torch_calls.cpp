@@ -11,11 +11,13 @@
 // goes the long way, which names what is wrong.
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
+#include <optional>
 
 #include "tiles.h"
 
@@ -108,15 +110,27 @@ at::Tensor empty_matrix(const at::Tensor& like, int64_t rows, int64_t cols, int6
     return empty(like, {rows, cols}, {ld, 1}, dtype);
 }
 
-void* stream_of(PyObject* o) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-    PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
-    require(v != nullptr);
-    void* s = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
-    require(!PyErr_Occurred());
-    return s;
-}
+// The stream that a call names, or the current one.  While this lives it is
+// the current one: new outputs come from its pool, as those of any operation on
+// it do.  (From another stream's pool they could be memory that work pending
+// there still uses.)
+struct OnStream {
+    void* at;
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+
+    explicit OnStream(PyObject* o) : at(c10::cuda::getCurrentCUDAStream().stream()) {
+        if (o == Py_None) return;
+        PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
+        require(v != nullptr);
+        void* s = PyLong_AsVoidPtr(v);
+        Py_DECREF(v);
+        require(!PyErr_Occurred());
+        if (s == at) return;
+        at = s;
+        guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(s),
+                                                       c10::cuda::current_device()));
+    }
+};
 
 struct Workspace {
     void* at = nullptr;
@@ -182,6 +196,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor *residual = optional_tensor(args[2]), *out = optional_tensor(args[4]),
                          *scales = optional_tensor(args[5]), *h_out = optional_tensor(args[6]);
         const bool fp8 = args[8] == Py_True;
+        const OnStream stream(args[7]);
         const Matrix mx(x);
         const at::ScalarType dtype = x.scalar_type(), out_dtype = fp8 ? kE4m3 : dtype;
         tiles_rmsnorm_desc d{};
@@ -237,8 +252,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         d.x = x.data_ptr();
         d.weight = weight.data_ptr();
         d.y = out->data_ptr();
-        void* stream = stream_of(args[7]);
-        run([&] { return calls.rmsnorm(&d, stream); });
+        run([&] { return calls.rmsnorm(&d, stream.at); });
         PyObject* h = new_h.defined() ? THPVariable_Wrap(std::move(new_h))
                                       : given(h_out ? args[6] : args[0]);
         PyObject* y = new_out.defined() ? THPVariable_Wrap(std::move(new_out)) : given(args[4]);
@@ -258,6 +272,7 @@ PyObject* rmsnorm_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor &dy = tensor(args[0]), &h = tensor(args[1]), &weight = tensor(args[2]);
         const at::Tensor *dh = optional_tensor(args[4]), *dx = optional_tensor(args[5]),
                          *dw = optional_tensor(args[6]);
+        const OnStream stream(args[8]);
         const Matrix mh(h), mdy(dy);
         const at::ScalarType dtype = h.scalar_type();
         require(mdy.like(mh) && dy.scalar_type() == dtype &&
@@ -298,8 +313,7 @@ PyObject* rmsnorm_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
         d.dx = dx->data_ptr();
         d.dweight = static_cast<float*>(dw->data_ptr());
         const Workspace ws(args[7]);
-        void* stream = stream_of(args[8]);
-        run([&] { return calls.rmsnorm_grad(&d, ws.at, ws.bytes, stream); });
+        run([&] { return calls.rmsnorm_grad(&d, ws.at, ws.bytes, stream.at); });
         PyObject* r = PyTuple_New(2);
         PyTuple_SET_ITEM(r, 0, new_dx.defined() ? THPVariable_Wrap(std::move(new_dx)) : given(args[5]));
         PyTuple_SET_ITEM(r, 1, new_dw.defined() ? THPVariable_Wrap(std::move(new_dw)) : given(args[6]));
@@ -339,6 +353,7 @@ PyObject* product_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
         const at::Tensor &a = tensor(args[0]), &as = tensor(args[1]), &b = tensor(args[2]),
                          &bs = tensor(args[3]);
         const bool grouped = args[4] != Py_None;
+        const OnStream stream(args[8]);
         const Matrix ma(a);
         const Weight mb(b, grouped);
         tiles_product_desc d{};
@@ -370,8 +385,7 @@ PyObject* product_fp8(PyObject*, PyObject* const* args, Py_ssize_t n) {
         d.in_dtype = TILES_E4M3;
         d.b_layout = TILES_B_NK;
         const Workspace ws(args[7]);
-        void* stream = stream_of(args[8]);
-        run([&] { return (grouped ? calls.grouped_gemm : calls.gemm_fp8)(&d, ws.at, ws.bytes, stream); });
+        run([&] { return (grouped ? calls.grouped_gemm : calls.gemm_fp8)(&d, ws.at, ws.bytes, stream.at); });
         return made.defined() ? THPVariable_Wrap(std::move(made)) : given(args[5]);
     });
 }
@@ -382,6 +396,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         require(n == 8 && PyBool_Check(args[3]));
         const at::Tensor &a = tensor(args[0]), &b = tensor(args[1]);
         const bool trans = args[3] == Py_True;
+        const OnStream stream(args[7]);
         const Matrix ma(a);
         const Weight mb(b, true);
         const at::ScalarType dtype = a.scalar_type();
@@ -402,8 +417,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         d.stride_b = mb.stride;
         d.b_layout = trans ? TILES_B_NK : TILES_B_KN;
         const Workspace ws(args[6]);
-        void* stream = stream_of(args[7]);
-        run([&] { return calls.grouped_gemm(&d, ws.at, ws.bytes, stream); });
+        run([&] { return calls.grouped_gemm(&d, ws.at, ws.bytes, stream.at); });
         return made.defined() ? THPVariable_Wrap(std::move(made)) : given(args[4]);
     });
 }
@@ -414,6 +428,7 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
         require(n == 7);
         const at::Tensor &a = tensor(args[0]), &dc = tensor(args[1]), &off = tensor(args[2]);
         const at::Tensor* out = optional_tensor(args[3]);
+        const OnStream stream(args[6]);
         const Matrix ma(a), mc(dc);
         const at::ScalarType dtype = a.scalar_type();
         require(mc.rows == ma.rows && dc.scalar_type() == dtype && off.dim() == 1);
@@ -445,8 +460,7 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
         d.lda = ma.ld;
         d.lddc = mc.ld;
         const Workspace ws(args[5]);
-        void* stream = stream_of(args[6]);
-        run([&] { return calls.grouped_wgrad(&d, ws.at, ws.bytes, stream); });
+        run([&] { return calls.grouped_wgrad(&d, ws.at, ws.bytes, stream.at); });
         return made.defined() ? THPVariable_Wrap(std::move(made)) : given(args[3]);
     });
 }
