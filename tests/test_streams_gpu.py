@@ -91,3 +91,22 @@ def test_products(name, compiled, monkeypatch):
     if not compiled:
         monkeypatch.setattr(T, "_CALLS", T._NoCalls)
     check(products, name)
+
+
+def matmuls(**kw):
+    ws = T.workspace()
+    a, b = torch.randn(256, 128, device="cuda").half(), torch.randn(128, 512, device="cuda").half()
+    x, w = torch.randn(2, 16, 20, 20, device="cuda").half(), torch.randn(32, 16, 3, 3, device="cuda").half()
+    return {
+        "gemm": lambda: T.gemm(a, b, workspace=ws, **kw),
+        "gemm_batched": lambda: T.gemm_batched(a[None], b[None], workspace=ws, **kw),
+        "gemm_noalloc": lambda: T.gemm_noalloc(a[None], b[None], **kw),
+        "conv2d_htiled": lambda: T.conv2d_htiled(x, w, workspace=ws, **kw),
+        "conv2d_tiled": lambda: T.conv2d_tiled(x, w, workspace=ws, **kw),
+    }
+
+
+@pytest.mark.parametrize("name", ["gemm", "gemm_batched", "gemm_noalloc", "conv2d_htiled",
+                                  "conv2d_tiled"])
+def test_matrix_products_and_convolutions(name):
+    check(matmuls, name)

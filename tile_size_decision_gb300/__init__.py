@@ -249,17 +249,18 @@ def _gemm_desc(a, b, out, batched: bool) -> _abi.GemmDesc:
     return d
 
 
-def _alloc_out(shape, like, out_dtype):
+def _alloc_out(shape, like, out_dtype, stream):
     torch = _torch()
     dt = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16,
           None: like.dtype}[out_dtype] if not isinstance(out_dtype, torch.dtype) else out_dtype
-    return torch.empty(shape, dtype=dt, device=like.device)
+    with _on(stream):
+        return torch.empty(shape, dtype=dt, device=like.device)
 
 
 def gemm(a, b, out=None, out_dtype=None, cfg=None, workspace=None, stream=None):
     """out = a @ b for 2-D row-major CUDA tensors (fp16/bf16 in)."""
     if out is None:
-        out = _alloc_out((a.shape[0], b.shape[1]), a, out_dtype)
+        out = _alloc_out((a.shape[0], b.shape[1]), a, out_dtype, stream)
     d = _gemm_desc(a, b, out, batched=False)
     ws, wsb = _workspace_args(workspace)
     _check(load().tiles_gemm(C.byref(d), _cfg_ptr(cfg), ws, wsb, _stream_handle(stream)),
@@ -320,7 +321,7 @@ def tuned_clear():
 def gemm_batched(a, b, out=None, out_dtype=None, cfg=None, workspace=None, stream=None):
     """out[t] = a[t] @ b[t] for 3-D CUDA tensors."""
     if out is None:
-        out = _alloc_out((a.shape[0], a.shape[1], b.shape[2]), a, out_dtype)
+        out = _alloc_out((a.shape[0], a.shape[1], b.shape[2]), a, out_dtype, stream)
     d = _gemm_desc(a, b, out, batched=True)
     ws, wsb = _workspace_args(workspace)
     _check(load().tiles_gemm_batched(C.byref(d), _cfg_ptr(cfg), ws, wsb, _stream_handle(stream)),
@@ -446,7 +447,7 @@ def conv2d_htiled(x, w, stride=(1, 1), pad=(0, 0), dil=(1, 1), tile_oh=16, out=N
     size the im2col operand is built by TMA, else gathered by threads."""
     shape = conv_out_shape(x, w, stride, pad, dil, layout)
     if out is None:
-        out = _alloc_out(shape, x, out_dtype)
+        out = _alloc_out(shape, x, out_dtype, stream)
     if not out.is_contiguous() or tuple(out.shape) != shape:
         raise ValueError("out must be contiguous with shape (n, c_out, oh, ow)")
     d = _conv_desc(x, w, stride, pad, dil, out, layout)
@@ -463,7 +464,7 @@ def conv2d_tiled(x, w, stride=(1, 1), pad=(0, 0), dil=(1, 1), tile_oh=16, tile_o
     slicing formulas as the rows); 0 means the whole batch or width."""
     shape = conv_out_shape(x, w, stride, pad, dil, layout)
     if out is None:
-        out = _alloc_out(shape, x, out_dtype)
+        out = _alloc_out(shape, x, out_dtype, stream)
     if not out.is_contiguous() or tuple(out.shape) != shape:
         raise ValueError("out must be contiguous with shape (n, c_out, oh, ow)")
     d = _conv_desc(x, w, stride, pad, dil, out, layout)
@@ -507,7 +508,7 @@ def gemm_noalloc(a, b, out=None, out_dtype=None, cfg=None, stream=None, wait=Fal
     that cannot allocate device memory.  The library's static scratch takes
     the workspace's place; wait=True synchronises and reports a timeout."""
     if out is None:
-        out = _alloc_out((a.shape[0], a.shape[1], b.shape[2]), a, out_dtype)
+        out = _alloc_out((a.shape[0], a.shape[1], b.shape[2]), a, out_dtype, stream)
     d = _gemm_desc(a, b, out, batched=True)
     _check(load().tiles_gemm_noalloc(C.byref(d), _cfg_ptr(cfg), _stream_handle(stream),
                                      1 if wait else 0), "tiles_gemm_noalloc")
