@@ -65,9 +65,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // The tensor map through which the GEMM epilogue's TMA stores write C: a
 // row-major [batch][m][n] array of the output type with row pitch `ldc` and
 // item pitch `sc` (elements), box {128 bytes of columns, 32 rows, 1}, the
-// 128-byte swizzle of the staging boxes.  False when C cannot take TMA
-// stores (base or pitches not 16-byte multiples, or the encoder refuses);
-// the epilogue then writes C from registers.
+// 128-byte swizzle of the staging boxes.  A store clips a row at 16 bytes and
+// not at the element, so the map ends at a row's last whole 16 bytes; the
+// epilogue copies what is behind them.  False when C cannot take TMA stores
+// (base or pitches not 16-byte multiples, rows shorter than 16 bytes, or the
+// encoder refuses); the epilogue then writes C from registers.
 bool encode_c_store(CUtensorMap* map, int dtype, void* base, uint64_t n, uint64_t m,
                     uint64_t batch, uint64_t ldc, uint64_t sc) {
     auto fn = encode_fn();
@@ -76,7 +78,9 @@ bool encode_c_store(CUtensorMap* map, int dtype, void* base, uint64_t n, uint64_
     const CUtensorMapDataType t = dtype == TILES_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                   : dtype == TILES_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    cuuint64_t dims[3] = {n, m, batch};
+    const uint64_t whole = n * eb / 16 * 16 / eb;
+    if (whole == 0) return false;
+    cuuint64_t dims[3] = {whole, m, batch};
     cuuint64_t strides[2] = {ldc * eb, sc * eb};
     cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / eb), 32, 1};
     cuuint32_t estr[3] = {1, 1, 1};

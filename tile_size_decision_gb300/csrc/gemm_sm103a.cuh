@@ -505,6 +505,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int out_bytes = args.c_dtype == TILES_F32 ? 4 : 2;
         uint8_t* box_ptr = staging + quarter * L::EPI_BOX_BYTES;
         const uint32_t box = ptx::smem_addr(box_ptr);
+        // C's columns up to the last whole 16 bytes of a row, and behind them.
+        const int tail = args.n & (out_bytes == 4 ? 3 : 7), whole = args.n - tail;
         // One 128-byte-wide box of the warp's 32 rows (w: this lane's row)
         // goes to C at column x through the staging box.  Lane 0 issues
         // every store, so its bulk groups track them all.
@@ -515,9 +517,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             stage_box_row(box, lane, w);
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && x < args.n && row0 < args.m) {
+            if (lane == 0 && x < whole && row0 < args.m) {
                 ptx::tma_store_3d(&tmC, box_ptr, x, row0, b);
                 ptx::bulk_commit_group();
+            }
+            // A TMA store clips a row at 16 bytes, not at the element: its map
+            // ends at the last whole ones, and each lane copies what its own
+            // row has behind them.
+            const int past = whole - x;                          // columns into the box
+            if (tail != 0 && past >= 0 && past < (out_bytes == 4 ? 32 : 64) &&
+                row0 + lane < args.m) {
+                const uint8_t* from = box_ptr + lane * 128 + (past * out_bytes ^ (lane & 7) << 4);
+                const int64_t at = b * args.stride_c +
+                                   static_cast<int64_t>(row0 + lane) * args.ldc + whole;
+                for (int i = 0; i < tail; ++i) {
+                    if (out_bytes == 4)
+                        static_cast<float*>(args.c)[at + i] = reinterpret_cast<const float*>(from)[i];
+                    else
+                        static_cast<uint16_t*>(args.c)[at + i] =
+                            reinterpret_cast<const uint16_t*>(from)[i];
+                }
             }
         };
         // Whole 128-byte boxes: 32 fp32 or 64 16-bit columns.
