@@ -20,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -89,12 +90,12 @@ def _compile(src: str, obj: str, extra: list, force: bool, verbose: bool) -> str
 
 
 def build_calls(force: bool = False, verbose: bool = False) -> str | None:
-    """Compile the compiled calls (csrc/torch_calls.cpp); None without PyTorch,
-    whose headers and libraries they need."""
+    """Compile the compiled calls (csrc/torch_calls.cpp); None without a PyTorch
+    for CUDA, whose headers and libraries they need."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
+    torch = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+    if torch is None or not os.path.exists(os.path.join(torch, "lib", "libtorch_cuda.so")):
         return None
-    torch = os.path.dirname(spec.origin)
     src = os.path.join(CSRC, "torch_calls.cpp")
     newest = max(os.path.getmtime(f) for f in (src, os.path.join(INCLUDE, "tiles.h"),
                                                os.path.join(torch, "version.py")))
@@ -119,14 +120,15 @@ def build_calls(force: bool = False, verbose: bool = False) -> str | None:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every unit, link libtiles.so and the compiled calls; return
-    libtiles.so's path."""
+    libtiles.so's path.  Where the compiled calls do not compile (another
+    PyTorch's headers, say) the library is there all the same: the package's
+    functions then marshal their arguments in Python."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = min(len(units()) + 1, max(1, os.cpu_count() or 1))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         calls = ex.submit(build_calls, force, verbose)
         futs = [ex.submit(_compile, s, o, e, force, verbose) for s, o, e in units()]
         objs = [f.result() for f in futs]
-        calls.result()
     if force or not os.path.exists(LIB) or \
             os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB + ".tmp"
@@ -136,6 +138,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIB)
+    try:
+        got = calls.result()
+    except (OSError, RuntimeError) as e:
+        got = None
+        warnings.warn(f"the compiled calls were not built: {e}")
+    if got is None and os.path.exists(CALLS):
+        os.remove(CALLS)                 # of other sources, or for another PyTorch
     return LIB
 
 
