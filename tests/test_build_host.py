@@ -4,6 +4,7 @@ the library is built all the same."""
 import importlib.machinery
 import os
 import subprocess
+import sys
 
 import pytest
 
@@ -59,3 +60,16 @@ def test_a_compiler_that_fails_on_the_calls(elsewhere, monkeypatch):
     with pytest.warns(UserWarning, match="no such header"):
         assert build.build() == build.LIB
     assert os.path.exists(build.LIB) and not os.path.exists(build.CALLS)
+
+
+def test_compiled_calls_that_do_not_load(monkeypatch):
+    pytest.importorskip("torch")
+    import tile_size_decision_gb300 as T
+    build.build()
+    monkeypatch.setattr(T, "_CALLS", None)
+    # What the import system does for a library of another PyTorch.
+    monkeypatch.delattr(T, "_calls", raising=False)
+    monkeypatch.setitem(sys.modules, T.__name__ + "._calls", None)
+    with pytest.warns(UserWarning, match="do not load"):
+        assert T._compiled() is T._NoCalls
+    assert T._CALLS is T._NoCalls

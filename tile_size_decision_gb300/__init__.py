@@ -14,6 +14,7 @@ import contextlib
 import ctypes as C
 import os
 import struct
+import warnings
 
 from . import _abi
 from ._abi import TilesError, check as _check
@@ -548,7 +549,7 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
 
 
 class _NoCalls:
-    """Stands in for the compiled calls where they were not built."""
+    """Stands in for the compiled calls where they were not built or do not load."""
 
     rmsnorm = rmsnorm_grad = product_fp8 = grouped_gemm = grouped_wgrad = \
         staticmethod(lambda *args: None)
@@ -561,13 +562,17 @@ def _compiled():
     global _CALLS
     _torch()
     lib = load()
+    calls = _NoCalls
     if os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_calls.so")):
-        from . import _calls
-        _calls.bind(*(C.cast(getattr(lib, "tiles_" + name), C.c_void_p).value for name in
-                      ("rmsnorm", "rmsnorm_grad", "gemm_fp8", "grouped_gemm", "grouped_wgrad")))
-        _CALLS = _calls
-    else:
-        _CALLS = _NoCalls
+        try:
+            from . import _calls as calls
+        except ImportError as e:
+            # Of another PyTorch, say: the long way does the same.
+            warnings.warn(f"the compiled calls do not load, build them again: {e}")
+        else:
+            calls.bind(*(C.cast(getattr(lib, "tiles_" + name), C.c_void_p).value for name in
+                         ("rmsnorm", "rmsnorm_grad", "gemm_fp8", "grouped_gemm", "grouped_wgrad")))
+    _CALLS = calls
     return _CALLS
 
 
