@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import operators as OO
+from oracle import tolerance as OT
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,47 @@ def test_h_out_without_a_residual_is_written(norm, compiled, monkeypatch):
         getattr(T, norm)(x, w, h_out=out)
     with pytest.raises((ValueError, TypeError)):
         getattr(T, norm)(x, w, h_out=view.half())
+
+
+def assert_norm(x, w, r, eps, fp8):
+    """At the tolerances of test_norm_gpu: 2^-18 of y and one spacing of its
+    type; half an 8-bit step and 2^-18; scales within 2^-18."""
+    f64 = lambda t: t.double().cpu().numpy()
+    rel = 2.0 ** -18
+    y64, h64 = OO.rmsnorm(f64(x), f64(w), f64(r) if r is not None else None, eps)
+    if fp8:
+        q, s, h = T.rmsnorm_fp8(x, w, residual=r, eps=eps)
+        want, s = OO.row_scales(y64), f64(s)
+        assert np.all(np.abs(s - want) <= rel * want)
+        sp = OO.spread(s, y64.shape[1], 1)
+        err = np.abs(f64(q) * sp - y64)
+        assert np.all(err <= sp * OO.half_step(y64 / sp) * (1 + 2 ** -8) + rel * np.abs(y64))
+    else:
+        y, h = T.rmsnorm(x, w, residual=r, eps=eps)
+        name = {v: k for k, v in DT.items()}[x.dtype]
+        ok, worst, idx = OT.check(f64(y), y64, np.abs(y64), name, rel)
+        assert ok, (worst, idx)
+    if r is not None:
+        ok, worst, idx = OT.check(f64(h), h64, np.abs(h64), {v: k for k, v in DT.items()}[h.dtype],
+                                  2.0 ** -24)
+        assert ok, (worst, idx)
+
+
+# h * weight leaves fp32's range on either side, the norm's output does not.
+@pytest.mark.parametrize("rows,cols", [(5, 1024), (700, 1024), (700, 2056), (350, 8192)])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("hscale,wscale,eps", [(2.0 ** 20, 2.0 ** 118, 1e-6),
+                                               (2.0 ** -45, 2.0 ** -100, 0.0)])
+def test_norm_whose_products_leave_the_range(rows, cols, fp8, residual, hscale, wscale, eps):
+    # Powers of two: the oracle's inputs are the kernel's.  One block of 128
+    # columns keeps an ordinary weight, one is zero.
+    x = (draw((rows, cols), "f32", 5) * hscale).bfloat16()
+    r = (draw((rows, cols), "f32", 6) * hscale).bfloat16() if residual else None
+    w = draw((cols,), "f32", 7)
+    w = torch.where(w.abs() < 0.1, torch.ones_like(w), w) * wscale
+    w[256:384] /= wscale
+    x[:, 512:640] = 0
+    if residual:
+        r[:, 512:640] = 0
+    assert_norm(x, w, r, eps, fp8)

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "launch_util.h"
 #include "op_ptx.cuh"
@@ -21,6 +22,11 @@ namespace {
 constexpr int kBlock = 128;             // columns that share one scale
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyScale = 0x1p-126f; // keeps the scale of a block of zeros usable
+// The shortcut of the kernel for many long rows (h * weight first) holds from
+// this magnitude of h * weight on, and for zeros of rows that are not quieter
+// than this 1 / rms: there even what fp32 lost below 2^-149 rounds to zero in 8
+// bits.
+constexpr float kQuiet = 0x1p-100f, kZeroRstd = 0x1p13f;
 constexpr int kMaxThreads = 1024;
 
 // fmaxf drops a NaN operand; a scale must keep it, or a row with a NaN would
@@ -28,6 +34,12 @@ constexpr int kMaxThreads = 1024;
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
@@ -369,8 +381,9 @@ __global__ void __launch_bounds__(kMaxThreads)
 // The same with the rows' pieces 16-byte aligned: the block takes rows
 // blockIdx.x, + gridDim.x, ..., the next two of them on their way in while one
 // is worked on.  DRAM bounds it: 16384 x 4096 bf16 rows with a residual, to
-// e4m3, 73.8 us, 94% of the measured copy bandwidth; without a residual the
-// work per byte does (11127 x 2728, 24.2 us, 56%).
+// e4m3, 73.9 us, 94% of the measured copy bandwidth; without a residual the
+// work per byte does (11127 x 2728, 25.8 us, 53%; 25.1 without the check for
+// blocks that take the definition's order).
 template <typename T, int VPT, bool FP8, bool RES>
 __global__ void __launch_bounds__(kRingThreads)
     rmsnorm_ring_kernel(const NormArgs a) {
@@ -403,50 +416,73 @@ __global__ void __launch_bounds__(kRingThreads)
         const int refill = slot == 0 ? kRing - 1 : slot - 1;
         fetch(row + (kRing - 1) * stride, refill);
         ptx::cp_async_wait_groups<kRing - 1>();
-        // What does not need the norm comes before the row's sum: h leaves,
-        // h becomes h * weight, and the blocks' magnitudes are taken of that.
+        // What does not need the norm comes before the row's sum: h leaves and,
+        // on the way to 8 bits, h becomes h * weight, and the blocks'
+        // magnitudes are taken of that.  (16-bit results take h / rms first:
+        // h * weight may be out of fp32's range where y is not.)
         float v[VPT][8], amax[VPT], sum[1] = {0.0f};
+        auto read_h = [&](int j, float (&h)[8]) {
+            const bool in = j * step + tid * 8 < cols;
+            ring.read(slot, 0, j, in, threads, h);
+            if constexpr (RES) {
+                float q[8];
+                ring.read(slot, 1, j, in, threads, q);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] += q[i];
+            }
+        };
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = j * step + tid * 8;
-            ring.read(slot, 0, j, c < cols, threads, v[j]);
-            if constexpr (RES) {
-                float q[8];
-                ring.read(slot, 1, j, c < cols, threads, q);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] += q[i];
-            }
+            read_h(j, v[j]);
             if (a.h) store8<T, true>(static_cast<T*>(a.h) + row * a.ldh, c, cols, v[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sum[0] += v[j][i] * v[j][i];
-                v[j][i] *= w[j][i];
+                if constexpr (FP8) v[j][i] *= w[j][i];
             }
             if constexpr (FP8) amax[j] = block_amax(amax8(v[j]));
         }
         row_sum(sum, slots, turn);
         const float rstd = rsqrtf(sum[0] * inv_n + a.eps);
+        bool again = false;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c = j * step + tid * 8;
-            float s = 0.0f, factor = rstd;
             if constexpr (FP8) {
-                s = block_scale(amax[j] * rstd);
-                factor = rstd * reciprocal(s);
-                if (isinf(factor)) {   // a quiet row over the smallest scale: in two steps
-                    factor = reciprocal(s);
+                const float s = block_scale(amax[j] * rstd);
+                // (The bound is for a block of zeros in a quiet row.)
+                const float factor = min_nan(rstd * reciprocal(s), FLT_MAX);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] *= rstd;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] *= factor;
-            if constexpr (FP8) {
+                for (int i = 0; i < 8; ++i) v[j][i] *= factor;
+                again |= !(amax[j] >= kQuiet && amax[j] <= FLT_MAX) &&
+                         !(amax[j] == 0.0f && rstd <= kZeroRstd);
                 store8_e4m3<true>(static_cast<uint8_t*>(a.y) + row * a.ldy, c, cols, v[j]);
                 if ((tid & 15) == 0 && c < cols)
                     a.scales[row * a.scale_row + c / kBlock * a.scale_block] = s;
             } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * rstd * w[j][i];
                 store8<T, true>(static_cast<T*>(a.y) + row * a.ldy, c, cols, v[j]);
+            }
+        }
+        // Where a block's h * weight left fp32's range, or is so quiet that it
+        // may have, the warp's blocks once more, as they are defined.
+        if (FP8 && __any_sync(0xffffffffu, again)) {
+#pragma unroll 1
+            for (int j = 0; j < VPT; ++j) {
+                const int c = j * step + tid * 8;
+                float y[8], u[8];
+                read_h(j, y);
+                load8_any<true>(a.weight, a.weight_dtype, c, cols, u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = c < cols ? y[i] * rstd * u[i] : 0.0f;
+                const float s = block_scale(block_amax(amax8(y))), inv = reciprocal(s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= inv;
+                store8_e4m3<true>(static_cast<uint8_t*>(a.y) + row * a.ldy, c, cols, y);
+                if ((tid & 15) == 0 && c < cols)
+                    a.scales[row * a.scale_row + c / kBlock * a.scale_block] = s;
             }
         }
         if (++slot == kRing) slot = 0;
