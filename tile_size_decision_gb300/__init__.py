@@ -189,6 +189,24 @@ def _stream_handle(stream):
     return C.c_void_p(_RAW_STREAM())
 
 
+_DEVICES = None
+
+
+def _here(*tensors):
+    """Refuses operands of another GPU than the current one, where the library
+    launches.  (Nothing to ask where there is one GPU: a microsecond a call.)"""
+    global _DEVICES
+    if _DEVICES is None:
+        _DEVICES = _torch().cuda.device_count()
+    if _DEVICES <= 1:
+        return
+    here = _torch().cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"operands must be on the current device, cuda:{here}, not on "
+                             f"cuda:{t.get_device()}")
+
+
 def _on(stream):
     """New outputs within come from the pool of the stream that a call names, as
     those of any operation on it do.  (From the current stream's pool they
@@ -214,6 +232,7 @@ def _workspace_args(workspace):
         return None, 0
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    _here(workspace)
     return workspace.data_ptr(), workspace.nbytes
 
 
@@ -237,6 +256,7 @@ def _gemm_desc(a, b, out, batched: bool) -> _abi.GemmDesc:
     m, k, n = ha[-2], ha[-1], hb[-1]
     if hb[-2] != k or hc[-2] != m or hc[-1] != n:
         raise ValueError(f"shape mismatch: {tuple(ha)} x {tuple(hb)} -> {tuple(hc)}")
+    _here(a, b, out)
     d = _abi.GemmDesc()
     d.m, d.n, d.k = m, n, k
     d.batch = ha[0] if batched else 1
@@ -396,6 +416,7 @@ def _conv_desc(x, w, stride, pad, dil, out, layout):
     for t, nm in ((x, "x"), (w, "w")):
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{nm} must be a contiguous CUDA tensor")
+    _here(x, w)
     if layout == "nchw":
         n, c, h, wd = x.shape
     elif layout == "nhwc":
@@ -419,6 +440,7 @@ def _conv_desc(x, w, stride, pad, dil, out, layout):
     if out is not None:
         if not out.is_cuda or not out.is_contiguous():
             raise ValueError("out must be a contiguous CUDA tensor")
+        _here(out)
         d.y = out.data_ptr()
         d.out_dtype = _dtype_code(out)
     return d
@@ -684,6 +706,7 @@ def _rmsnorm(x, weight, residual, eps, out, scales, h_out, stream, fp8):
                 ("residual", residual, shape, dtype),
                 ("h_out", h_out, shape, dtype),
                 ("out", out if given else None, shape, torch.float8_e4m3fn if fp8 else dtype))
+    _here(x, weight, residual, out, scales, h)
     d = _NORM.pack(rows, cols, x.data_ptr(), pr, weight.data_ptr(), ph, out.data_ptr(), ps, ldx, ldr,
                    ldh, ldy, sr, sb, eps, code, wcode, _abi.E4M3 if fp8 else code)
     _check(load().tiles_rmsnorm(d, _raw_stream(stream)), "tiles_rmsnorm")
@@ -766,6 +789,7 @@ def rmsnorm_grad(dy, h, weight, eps=1e-6, dh=None, dx_out=None, dweight_out=None
                 ("weight", weight, (cols,), set(codes)), ("dh", dh, shape, dtype),
                 ("dx_out", dx_out, shape, dtype),
                 ("dweight_out", dweight_out, (cols,), torch.float32))
+    _here(dy, h, weight, dh, dx, dw)
     d = _NORM_GRAD.pack(rows, cols, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), pdh,
                         dx.data_ptr(), dw.data_ptr(), lddy, ldh, lddh, lddx, eps, code, wcode, 0)
     ws, wsb = _workspace_args(workspace)
@@ -796,6 +820,7 @@ def quantize_fp8(x, block_rows=1, stream=None):
                                  device=x.device).transpose(-1, -2)
         else:
             scales = torch.empty((*lead, _blocks(rows), nb), dtype=torch.float32, device=x.device)
+    _here(x)
     d = _abi.QuantizeDesc(batch, rows, cols, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
                           x.stride(-2) if rows > 1 else max(x.stride(-2), cols),
                           x.stride(0) if lead else 0, pitch, q.stride(0) if lead else 0,
@@ -851,6 +876,7 @@ def _product_fp8(a, a_scales, b, b_scales, offsets, out, out_dtype, workspace, s
         _refuse(("a", a, None, fp8), ("b", b, (*bshape[:-1], k), fp8),
                 ("offsets", offsets, (groups + 1,), torch.int32),
                 ("out", out if given else None, (m, n), set(codes)))
+    _here(a, a_scales, b, b_scales, offsets, out)
     sar, sab = a_scales.stride()
     d = _PRODUCT.pack(m, n, k, groups, off, a.data_ptr(), b.data_ptr(), out.data_ptr(),
                       a_scales.data_ptr(), b_scales.data_ptr(), lda, ldb, ldc, stride_b, sar, sab,
@@ -936,6 +962,7 @@ def grouped_gemm(a, b, offsets, trans_b=False, out=None, out_dtype=None, workspa
                 ("b", b, (groups, n, k) if trans_b else (groups, k, n), dtype),
                 ("offsets", offsets, (groups + 1,), torch.int32),
                 ("out", out if given else None, (m, n), set(codes)))
+    _here(a, b, offsets, out)
     d = _PRODUCT.pack(m, n, k, groups, offsets.data_ptr(), a.data_ptr(), b.data_ptr(),
                       out.data_ptr(), 0, 0, lda, ldb, ldc, stride_b, 0, 0, 0, 0, 0, codes[dtype],
                       codes[out.dtype], _abi.B_NK if trans_b else _abi.B_KN, 0)
@@ -973,6 +1000,7 @@ def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stre
         _refuse(("a", a, None, set(codes)), ("dc", dc, (m, n), dtype),
                 ("offsets", offsets, (groups + 1,), torch.int32),
                 ("out", out if given else None, (groups, k, n), set(codes)))
+    _here(a, dc, offsets, out)
     d = _WGRAD.pack(m, k, n, groups, offsets.data_ptr(), a.data_ptr(), dc.data_ptr(),
                     out.data_ptr(), lda, lddc, ldw, stride_dw, codes[dtype], codes[out.dtype])
     ws, wsb = _workspace_args(workspace)

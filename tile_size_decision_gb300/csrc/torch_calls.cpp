@@ -49,12 +49,18 @@ int code_of(at::ScalarType t) {
     }
 }
 
+bool several_devices() {
+    static const bool yes = c10::cuda::device_count() > 1;
+    return yes;
+}
+
 // Tensors are read where Python holds them: the arguments outlive the call.
+// They are on the current device, where the library launches.
 const at::Tensor* optional_tensor(PyObject* o) {
     if (o == Py_None) return nullptr;
     require(THPVariable_Check(o));
     const at::Tensor* t = &THPVariable_Unpack(o);
-    require(t->is_cuda());
+    require(t->is_cuda() && (!several_devices() || t->get_device() == c10::cuda::current_device()));
     return t;
 }
 
