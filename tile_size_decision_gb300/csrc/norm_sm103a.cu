@@ -868,13 +868,16 @@ int launch_norm_any(const NormArgs& a, bool vec, bool fp8, int sms, cudaStream_t
     // without it, 16384 x 1024: 17.7 against 22.9) and 16-bit (fp32 pieces are
     // half a vector: 8000 x 4096 118 us against 76.7), and where there are more
     // rows than blocks.
-    const int threads = static_cast<int>((a.cols + 32 * 8 * kRingVpt - 1) / (32 * 8 * kRingVpt) * 32);
-    if (vec && sizeof(T) == 2 && threads > 32 && threads <= kRingThreads && a.rows > 2 * sms) {
-        if (a.residual)
-            return fp8 ? launch_norm_ring<T, true, true>(a, threads, sms, st)
-                       : launch_norm_ring<T, false, true>(a, threads, sms, st);
-        return fp8 ? launch_norm_ring<T, true, false>(a, threads, sms, st)
-                   : launch_norm_ring<T, false, false>(a, threads, sms, st);
+    if constexpr (sizeof(T) == 2) {
+        const int threads =
+            static_cast<int>((a.cols + 32 * 8 * kRingVpt - 1) / (32 * 8 * kRingVpt) * 32);
+        if (vec && threads > 32 && threads <= kRingThreads && a.rows > 2 * sms) {
+            if (a.residual)
+                return fp8 ? launch_norm_ring<T, true, true>(a, threads, sms, st)
+                           : launch_norm_ring<T, false, true>(a, threads, sms, st);
+            return fp8 ? launch_norm_ring<T, true, false>(a, threads, sms, st)
+                       : launch_norm_ring<T, false, false>(a, threads, sms, st);
+        }
     }
     if (vec) return fp8 ? launch_norm<T, true, true>(a, st) : launch_norm<T, true, false>(a, st);
     return fp8 ? launch_norm<T, false, true>(a, st) : launch_norm<T, false, false>(a, st);
