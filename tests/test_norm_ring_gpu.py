@@ -122,3 +122,80 @@ def test_norm_whose_products_leave_the_range(rows, cols, fp8, residual, hscale, 
     if residual:
         r[:, 512:640] = 0
     assert_norm(x, w, r, eps, fp8)
+
+
+# Blocks with one row and with dozens, rows of whole and of short last blocks of
+# 128; the last is past 160 MB with a residual (fewer blocks an SM).
+SHAPES = [(305, 520), (700, 1024), (400, 3000), (350, 8192), (12000, 1032), (6000, 4104)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_every_output(shape, dtype, residual, fp8):
+    x, w = draw(shape, dtype, 11), draw((shape[1],), dtype, 12)
+    r = draw(shape, dtype, 13) if residual else None
+    assert_norm(x, w, r, 1e-6, fp8)
+
+
+@pytest.mark.parametrize("shape", [(700, 1024), (12000, 1032), (6000, 4104)], ids=str)
+@pytest.mark.parametrize("over", ["residual", "x"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_h_over_its_input(shape, over, fp8):
+    x, r, w = draw(shape, "bf16", 14), draw(shape, "bf16", 15), draw((shape[1],), "f32", 16)
+    norm = T.rmsnorm_fp8 if fp8 else T.rmsnorm
+    want = norm(x, w, residual=r)
+    target = r if over == "residual" else x
+    got = norm(x, w, residual=r, h_out=target)
+    assert got[-1] is target and torch.equal(target, want[-1])
+    for u, v in zip(got[:-1], want[:-1]):
+        assert torch.equal(u.view(torch.uint8) if fp8 and u.element_size() == 1 else u,
+                           v.view(torch.uint8) if fp8 and v.element_size() == 1 else v)
+
+
+@pytest.mark.parametrize("shift,pitch", [(0, 1040), (8, 1048), (0, 2048)])
+def test_rows_with_a_pitch_keep_what_lies_between(shift, pitch):
+    rows, cols = 2000, 1032
+    full = draw((rows * pitch + shift,), "bf16", 17)
+    x = full[shift:].view(rows, pitch)[:, :cols]
+    w = draw((cols,), "bf16", 18)
+    out = torch.full((rows, pitch), 7.0, dtype=torch.bfloat16, device="cuda")
+    h = torch.full((rows, pitch), 7.0, dtype=torch.bfloat16, device="cuda")
+    want = T.rmsnorm(x.contiguous(), w, residual=x.contiguous())
+    got = T.rmsnorm(x, w, residual=x, out=out[:, :cols], h_out=h[:, :cols])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((out[:, cols:] == 7.0).all()) and bool((h[:, cols:] == 7.0).all())
+
+
+def test_nans_and_infinities_stay_in_their_rows():
+    x, w = draw((2000, 1032), "f16", 19), torch.ones(1032, dtype=torch.float16, device="cuda")
+    plain = T.rmsnorm_fp8(x, w)
+    want = [plain[0].float(), plain[1].clone()]
+    x[7, 5], x[900, 1031], x[1999, 0] = float("nan"), float("inf"), float("-inf")
+    q, s, _ = T.rmsnorm_fp8(x, w)
+    q = q.float()
+    keep = torch.ones(2000, dtype=torch.bool)
+    keep[[7, 900, 1999]] = False
+    assert torch.equal(q[keep], want[0][keep]) and torch.equal(s[keep], want[1][keep])
+    assert bool(q[7].isnan().all()) and bool(s[7].isnan().all())
+    # h / rms is zero but for inf / inf, whose block alone has no scale.
+    for row, col in ((900, 1031), (1999, 0)):
+        block = col // 128
+        assert bool(q[row, col].isnan()) and bool(s[row, block].isnan())
+        others = torch.arange(1032) // 128 != block
+        assert bool((q[row, others] == 0).all())
+        assert bool((s[row, torch.arange(9) != block] == OO.TINY_SCALE).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(9000, 1032), (20000, 264), (1500, 8192)], ids=str)
+def test_gradients_of_many_rows_a_block(shape, dtype):
+    f64 = lambda t: t.double().cpu().numpy()
+    h, dy, dh = (draw(shape, dtype, s) for s in (20, 21, 22))
+    w = draw((shape[1],), "f32", 23)
+    dx, dw = T.rmsnorm_grad(dy, h, w, dh=dh, workspace=T.rmsnorm_grad_workspace(h))
+    rx, rw, bx, bw = OO.rmsnorm_grad(f64(dy), f64(h), f64(w), f64(dh))
+    for got, ref, bound, kind, rel in ((dx, rx, bx, dtype, 2.0 ** -18), (dw, rw, bw, "f32", 2.0 ** -14)):
+        ok, worst, idx = OT.check(f64(got), ref, bound, kind, rel)
+        assert ok, (worst, idx)
