@@ -42,7 +42,8 @@ def assert_close(got, ref, bound, dtype, rel):
 # Few rows: the contraction is split over a cluster.  Many: tiles on CTA pairs.
 @pytest.mark.parametrize("rows,groups,n,k", [
     (1, 32, 136, 4096), (1, 256, 512, 2048), (3, 70, 256, 1024), (16, 256, 136, 2048),
-    (9000, 70, 256, 192), (20000, 256, 264, 128), (12000, 129, 512, 64)])
+    (9000, 70, 256, 192), (20000, 256, 264, 128), (12000, 129, 512, 64),
+    (20000, 4096, 136, 64)])
 @pytest.mark.parametrize("kind", ["16 bits", "transposed", "8 bits"])
 def test_products(rows, groups, n, k, kind):
     off, toff = spread_rows(rows, groups, groups)
