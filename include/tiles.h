@@ -589,7 +589,8 @@ int tiles_selftest_drop_stage(int stage, int64_t limit_ns);
  * blocks works; blocks stored outermost ([blocks][rows]) load fastest.
  * Number of blocks of a length n: ceil(n / 128); the last may be short.
  * A row count of 0 is allowed and does nothing.  An output may not overlap an
- * input, except where a norm's h is stored over x or over the residual. */
+ * input, except where a norm's h is stored over x or over the residual.
+ * All pointers are of the current device. */
 
 /* h = x + residual;  y = h * (mean(h^2) + eps)^(-1/2) * weight,  row by row.
  * The sum, the mean and the norm are fp32 and read the sum before it is
@@ -602,7 +603,8 @@ typedef struct {
     const void* x;                    /* device, rows x cols */
     const void* residual;             /* device, rows x cols, or NULL: h = x */
     const void* weight;               /* device, cols */
-    void* h;                          /* device, rows x cols; NULL: h is not stored */
+    void* h;                          /* device, rows x cols (a copy of x without a residual);
+                                         NULL: h is not stored */
     void* y;                          /* device, rows x cols, out_dtype */
     float* scales;                    /* device, E4M3 only */
     int64_t ldx, ldr, ldh, ldy;       /* row pitches, elements */
@@ -673,13 +675,16 @@ typedef enum { TILES_B_KN = 0, TILES_B_NK = 1 } tiles_b_layout;
  * offsets (groups + 1 int32 on the device, ascending) is read by the kernel
  * only: no copy to the host, so a router's counts can stay on the device.
  * Rows outside every group are not written; offsets outside [0, m] count as
- * the nearer end, and a descending pair as an empty group.
+ * the nearer end, and a descending pair as an empty group (where a later group
+ * then starts before rows of an earlier one, those rows are unspecified).
  * in_dtype F16/BF16: a is m x k, b is k x n (TILES_B_KN) or n x k
  *   (TILES_B_NK: c = a x b^T, the form of the rows' gradient under a KN
  *   weight), grouped only; fp32 accumulation over all of k.
  * in_dtype E4M3: b is n x k (TILES_B_NK), and
  *   c[i][j] = sum over blocks t of as[i][t] * bs[j/128][t] * (sum over k in t of a[i][k] * b[j][k])
- *   with the inner sums in the tensor core and the outer sum in fp32.
+ *   with the inner sums in the tensor core and the outer sum in fp32; the two
+ *   scales are multiplied first, in fp32: terms below 2^-100 lose bits where the
+ *   scales' product is below 2^-126.
  * c is F32, F16 or BF16 (round to nearest even).  a and b need 16-byte
  * aligned bases, row pitches and group strides (TMA); c and the scales only
  * their element's. */

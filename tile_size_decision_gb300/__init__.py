@@ -567,7 +567,8 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
 #
 # A call runs on `stream`, or on the current stream.  Its new outputs belong to
 # that stream, as after any PyTorch operation on it: used on another one, they
-# are the caller's to order (wait_stream, record_stream).
+# are the caller's to order (wait_stream, record_stream).  Outputs that the
+# caller gives may not overlap an input, but for a norm's h_out.
 
 
 class _NoCalls:

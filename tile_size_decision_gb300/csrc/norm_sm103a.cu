@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(kMaxThreads)
 // The same with the rows' pieces 16-byte aligned: the block takes rows
 // blockIdx.x, + gridDim.x, ..., the next two of them on their way in while one
 // is worked on.  DRAM bounds it: 16384 x 4096 bf16 rows with a residual, to
-// e4m3, 73.9 us, 94% of the measured copy bandwidth; without a residual the
-// work per byte does (11127 x 2728, 25.8 us, 53%; 25.1 without the check for
+// e4m3, 72.6 us, 95% of the measured copy bandwidth; without a residual the
+// work per byte does (11127 x 2728, 25.9 us, 53%; 25.1 without the check for
 // blocks that take the definition's order).
 template <typename T, int VPT, bool FP8, bool RES>
 __global__ void __launch_bounds__(kRingThreads)
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(512, 2)
         for (int i = 0; i < 8; ++i) past[i] = 0.0f;
         // dh with the others where it is one load (8192 x 4096 fp32: 88 us
         // against 95), after the sums where it is eight (3000 x 3001: 40
-        // against 45; the registers spill otherwise).
+        // against 45: these instances spill 48 to 80 bytes a thread as it is).
         if (VEC && dh) load8<T, VEC>(dh, c, cols, past);
         load8_any<VEC>(a.weight, a.weight_dtype, c, cols, w);
         float s[2] = {0.0f, 0.0f};                 // sum h^2, sum dy w h
@@ -829,9 +829,9 @@ int launch_norm_ring(const NormArgs& a, int threads, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return static_cast<int>(e);
     // Blocks an SM: as many as it holds, but where residual rows stream through
     // DRAM only 512 threads, whose copies in flight saturate it with fewer
-    // rows open at once: 16384 x 4096 bf16 rows (470 MB) 73.8 us against 85.9,
-    // 8000 x 8192 69.9 against 82.0, while 16384 x 1024 (117 MB, an L2's worth)
-    // takes 18.9 us against 17.7.
+    // rows open at once: 16384 x 4096 bf16 rows (470 MB) 73.9 us against 86.9,
+    // 8000 x 8192 71.9 against 82.8, while 11127 x 2728 (212 MB) takes 42.6
+    // against 41.2.
     const bool stream = RES && a.rows * a.cols * static_cast<int64_t>(3 * sizeof(T) + 1) > (160ll << 20);
     const int per_sm = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(
         (stream ? 512 : 1536) / threads, 220 * 1024 / static_cast<int64_t>(smem + 1024))));

@@ -16,7 +16,7 @@
 // multiple of 32, half of them loaded by each CTA).  Wide tiles (up to 256) have
 // two buffers in tensor memory, narrow ones (up to 128) four; the host picks
 // the width and with it the kernel (for few tiles the narrow one: 1024 x 1024 x
-// 4096 14.1 us against 19.8, while 4096^3 takes 75.5 against 67.7).
+// 4096 14.1 us against 19.8, while 4096^3 takes 75.5 against 67.9).
 //
 // Roles (384 threads): warp 0 TMA, warp 1 MMA (leader), warp 2 scales (a small
 // ring in shared memory, filled by asynchronous copies ten K blocks ahead), warp
@@ -26,7 +26,7 @@
 // The reading back bounds it: a K block of a wide tile takes about 860 clocks
 // (512 of them MMA), of a narrow one 570 (256).  The epilogue warps never wait
 // for a sum; of their time some 250 clocks a K block go to the two waits, the
-// scales and the first load, the rest to loads and additions.  4096^3 67.7 us
+// scales and the first load, the rest to loads and additions.  4096^3 67.9 us
 // (54% of twice the 16-bit rate), 8192 rows in 32 uneven groups by 4096 x 2048
 // 88 us (55% of the DRAM floor).  Slower when measured: halves of a tile handed
 // over apart (102 us on the groups), 16 epilogue warps (75 on 4096^3), wider

@@ -23,14 +23,15 @@
 // then transposes it: a row of c is a TMEM column.
 //
 // The tensor cores bound long contractions, the results' way out short ones.
-// 32768 rows in 16 uneven groups, 1024 x 2048 bf16: products 85 us (86% of the
-// measured rate), the rows' gradient 84 (87%), the weight gradient 91 (80%).
-// What made the products faster than 95: the next units asked for by a warp of
-// its own, and a stage's rows in one load (the TMA warp, with six loads a stage,
-// had been the slowest role: 650 clocks a K block).  Measured before that on
-// 30000 x 1024 x 2048 (83.5 us): without the stores 74.9, without the
-// transposition 83.9, through registers instead of TMA 84.9, with two boxes a
-// warp and the TMEM loads a chunk ahead 84.3.
+// 32768 rows in 16 uneven groups, 1024 x 2048 bf16: products and the rows'
+// gradient 83 us (88% of the measured rate), the weight gradient 90 (81%), from a
+// graph with pauses; called back to back the power cap makes it 95 to 98 and 99
+// to 103.  What made the products faster (95 us from a graph): the next units
+// asked for by a warp of its own, and a stage's rows in one load (the TMA warp,
+// with six loads a stage, had been the slowest role: 650 clocks a K block).
+// Measured before that on 30000 x 1024 x 2048 (83.5 us): without the stores
+// 74.9, without the transposition 83.9, through registers instead of TMA 84.9,
+// with two boxes a warp and the TMEM loads a chunk ahead 84.3.
 #include "pair_sm103a.cuh"
 
 namespace tiles {
@@ -248,9 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (!GRAD && warp == 3 && leader) {
         // ---------------- the next units ----------------
         // (Asking takes the TMA warp 1200 clocks a unit, which the products' loads
-        // do not have: 32768 rows in 16 uneven groups, 1024 x 2048, 84 us against
-        // 95.  The weight gradient asks there, which measured better: 91 against
-        // 94.)
+        // do not have: 95 us for the products above, 88 without it.  The weight
+        // gradient asks there, which measured better: 90 against 94.)
         Asker asker;
         do {
             if (!asker.ask(bar, abort, limit)) {

@@ -19,10 +19,10 @@
 //
 // Roles as in the GEMM: warp 0 TMA, warp 1 MMA, warps 2-5 epilogue.
 //
-// 64 rows over 15 of 16 groups, 2048 x 2048 bf16 weights (126 MB): 22.0 us, 84%
-// of the measured copy bandwidth.  16 rows by a 4096 x 4096 e4m3 weight: 5.4 us
-// where the weight's bytes take 2.5; the rest is the chain of one CTA's loads,
-// K blocks and the cluster's addition, as latency.
+// 64 rows over 15 of 16 groups, 2048 x 2048 bf16 weights (126 MB): 22.8 us, 82%
+// of the measured copy bandwidth.  16 rows by a 4096 x 4096 e4m3 weight: 7.5 us
+// where the weight's bytes take 2.5 (5.4 with the weight in L2); the rest is the
+// chain of one CTA's loads, K blocks and the cluster's addition, as latency.
 #include "product_sm103a.cuh"
 
 namespace tiles {
