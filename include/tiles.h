@@ -3,8 +3,9 @@
  * the GB300 (sm_103a) kernels it drives: a tiled dense GEMM C = A x B with
  * fp16/bf16 inputs and fp32 accumulation, optionally batched, and an NCHW
  * conv2d run as an implicit GEMM tiled over the output height; and the
- * operators that surround the GEMM in a transformer block: root-mean-square
- * norms, 8-bit products with block scales, and products grouped by expert.
+ * operators that surround the GEMM in a transformer block: norms, 8-bit
+ * products with block scales, products grouped by expert, the rows' way to
+ * the experts and back, and the clipping of gradients.
  *
  * Sources of the operations (pages of the tile-size-decision material):
  *   - constraint procedure: page "04-tile-size-decision/tile_decision.py"
@@ -731,6 +732,178 @@ typedef struct {
 
 int tiles_grouped_wgrad(const tiles_wgrad_desc* desc, void* workspace, size_t ws_bytes,
                         void* stream);
+
+/* ---- Layer norm ----------------------------------------------------------- */
+
+/* h = x + residual;  d = h - mean(h);
+ * y = d * (mean(d^2) + eps)^(-1/2) * weight + bias,  row by row.
+ * Sums and statistics are fp32 and read the sum before it is rounded into h;
+ * the mean is corrected by the mean of what is left after it, so that rows
+ * far from zero keep their spread.  out_dtype is dtype or E4M3, with the
+ * scales of tiles_rmsnorm.  A NaN or an infinity in a row makes the row's y (or
+ * its scales) NaN. */
+typedef struct {
+    int64_t rows, cols;               /* rows >= 0, cols >= 1 */
+    const void* x;                    /* device, rows x cols */
+    const void* residual;             /* device, rows x cols, or NULL: h = x */
+    const void* weight;               /* device, cols */
+    const void* bias;                 /* device, cols, of the weight's type, or NULL: none */
+    void* h;                          /* device, rows x cols (a copy of x without a residual);
+                                         NULL: h is not stored */
+    void* y;                          /* device, rows x cols, out_dtype */
+    float* scales;                    /* device, E4M3 only */
+    int64_t ldx, ldr, ldh, ldy;       /* row pitches, elements */
+    int64_t scale_row, scale_block;   /* scale of (row, block) at row*scale_row + block*scale_block */
+    float eps;
+    int32_t dtype;                    /* of x, residual and h: F16, BF16 or F32 */
+    int32_t weight_dtype;             /* F16, BF16 or F32 */
+    int32_t out_dtype;                /* dtype or E4M3 */
+} tiles_layernorm_desc;
+
+/* Alignment as tiles_rmsnorm; no workspace. */
+int tiles_layernorm(const tiles_layernorm_desc* desc, void* stream);
+
+/* Gradients of tiles_layernorm at h, with d = h - mean(h), u = mean(d^2) + eps,
+ * g = dy * weight:
+ *   dx = (g - mean(g)) u^(-1/2) - d mean(g d) u^(-3/2) + dh
+ *   dweight_j = sum over rows of dy_j d_j u^(-1/2),  dbias_j = sum over rows of dy_j
+ * dx is the gradient of x and of the residual alike; dh, the gradient that
+ * reaches h past the norm, may be NULL.  dweight and dbias are fp32; the sums
+ * over rows run in a fixed order for given sizes and device. */
+typedef struct {
+    int64_t rows, cols;
+    const void* dy;
+    const void* h;
+    const void* weight;
+    const void* dh;                   /* or NULL */
+    void* dx;
+    float* dweight;                   /* cols; zeros when rows == 0 */
+    float* dbias;                     /* likewise */
+    int64_t lddy, ldh, lddh, lddx;    /* row pitches, elements */
+    float eps;
+    int32_t dtype;                    /* of dy, h, dh and dx */
+    int32_t weight_dtype;
+    int32_t pad0;
+} tiles_layernorm_grad_desc;
+
+/* Workspace bytes of the gradient, as tiles_rmsnorm_grad_workspace_bytes. */
+size_t tiles_layernorm_grad_workspace_bytes(int64_t rows, int64_t cols);
+
+int tiles_layernorm_grad(const tiles_layernorm_grad_desc* desc, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/* ---- Rows to the experts and back -------------------------------------------
+ * A router gives every token k experts.  tiles_expert_sort gives each of these
+ * (token, choice) pairs a row in expert order, tiles_expert_dispatch lays the
+ * tokens' rows out in that order, tiles_grouped_gemm multiplies them (its
+ * offsets are the sort's), and tiles_expert_combine adds the results up by
+ * token.  Nothing is copied to the host. */
+
+/* The stable sort of the pairs (t, j) by experts[t][j]: rows of expert g are
+ * offsets[g] .. offsets[g+1] - 1, its pairs in the order of t * k + j.
+ *   slots[t][j]  the pair's row, or -1 where its id is outside [0, groups)
+ *                (padding, or an expert that is not here)
+ *   order[row]   the pair t * k + j of a row; -1 for rows past the last expert's
+ * At most 4096 groups and 2^24 pairs.  Groups without pairs are empty. */
+typedef struct {
+    int64_t tokens, k;                /* tokens >= 0, k >= 1 */
+    int64_t groups;
+    const void* experts;              /* device, tokens x k integers */
+    int64_t ld;                       /* row pitch of experts, elements */
+    int32_t* slots;                   /* device, tokens x k, no pitch */
+    int32_t* offsets;                 /* device, groups + 1 */
+    int32_t* order;                   /* device, tokens * k, or NULL */
+    int32_t index_bytes;              /* of an id: 4 or 8 */
+    int32_t pad0;
+} tiles_expert_sort_desc;
+
+/* Workspace bytes of the sort: the 256-byte header (left alone) and the counts
+ * of its blocks (0 on invalid arguments).  16-byte aligned; its contents do not
+ * matter.  Host only. */
+size_t tiles_expert_sort_workspace_bytes(int64_t tokens, int64_t k, int64_t groups);
+
+int tiles_expert_sort(const tiles_expert_sort_desc* desc, void* workspace, size_t ws_bytes,
+                      void* stream);
+
+/* out[slots[t][j]] = x[t] for every pair whose slot lies in [0, rows); other rows
+ * of out are not written.  The slots are different from one another.  With
+ * scales (8-bit rows) out_scales[slots[t][j]] = scales[t] for the ceil(cols / 128)
+ * blocks.  The gradient of x is tiles_expert_combine of out's, without weights. */
+typedef struct {
+    int64_t tokens, k;
+    int64_t rows, cols;               /* of out; rows >= 0, cols >= 1 */
+    const int32_t* slots;             /* device, tokens x k */
+    const void* x;                    /* device, tokens x cols */
+    void* out;                        /* device, rows x cols */
+    const float* scales;              /* device, or NULL */
+    float* out_scales;
+    int64_t ld_slots, ldx, ld_out;    /* row pitches, elements */
+    int64_t scale_row, scale_block;   /* scale of (row, block) at row*scale_row + block*scale_block */
+    int64_t out_scale_row, out_scale_block;
+    int32_t dtype;                    /* F16, BF16, F32 or E4M3 */
+    int32_t pad0;
+} tiles_dispatch_desc;
+
+/* Pointers need only their element's alignment; rows that start on 16 bytes and
+ * end there move in 16-byte pieces.  No workspace. */
+int tiles_expert_dispatch(const tiles_dispatch_desc* desc, void* stream);
+
+/* One descriptor for the sum and its gradients.
+ *   tiles_expert_combine:       out[t] = sum over j of weights[t][j] * in[slots[t][j]]
+ *     out is tokens x cols; the sum is fp32, in the order of j.  A slot outside
+ *     [0, rows) adds nothing, whatever its weight is; a token without any is 0.
+ *   tiles_expert_combine_grad:  out[slots[t][j]] = weights[t][j] * dy[t]
+ *                               dweights[t][j] = sum over columns of dy[t] * in[slots[t][j]]
+ *     out is rows x cols, of which the rows that no slot names are not written;
+ *     a slot outside [0, rows) has dweights 0.  The slots are different from one
+ *     another. */
+typedef struct {
+    int64_t tokens, k;
+    int64_t rows, cols;               /* of the rows in expert order */
+    const int32_t* slots;             /* device, tokens x k */
+    const void* weights;              /* device, tokens x k; NULL: ones (not for the gradient) */
+    const void* in;                   /* device, rows x cols, in expert order */
+    const void* dy;                   /* the gradient only: tokens x cols */
+    void* out;
+    float* dweights;                  /* the gradient only: tokens x k */
+    int64_t ld_slots, ld_weights, ld_in, ld_dy, ld_out, ld_dweights;   /* row pitches, elements */
+    int32_t dtype;                    /* of in, dy and out: F16, BF16 or F32 */
+    int32_t weight_dtype;             /* F16, BF16 or F32 */
+} tiles_combine_desc;
+
+/* Alignment as tiles_expert_dispatch; no workspace. */
+int tiles_expert_combine(const tiles_combine_desc* desc, void* stream);
+int tiles_expert_combine_grad(const tiles_combine_desc* desc, void* stream);
+
+/* ---- Norm and clipping of gradients ------------------------------------------- */
+
+/* One gradient: `count` elements that lie together. */
+typedef struct {
+    const void* grad;                 /* device */
+    void* out;                        /* device, or NULL: scaled in place (the norm ignores it) */
+    int64_t count;                    /* >= 0 */
+    int32_t dtype;                    /* F16, BF16 or F32 */
+    int32_t pad0;
+} tiles_grad_tensor;
+
+/* Workspace bytes of the norm of so many tensors: the 256-byte header (left
+ * alone) and the partial sums.  16-byte aligned; its contents do not matter. */
+size_t tiles_grad_norm_workspace_bytes(int64_t tensors);
+
+/* *norm = the square root of the sum of all elements' squares (0 without any).
+ * The array of tensors is the host's and may go when the call returns.  Squares
+ * are fp32 where its range holds them, the sums above a thread's few elements
+ * fp64, in a fixed order for given sizes and device. */
+int tiles_grad_norm(const tiles_grad_tensor* tensors, int64_t n, float* norm, void* workspace,
+                    size_t ws_bytes, void* stream);
+
+/* The same norm, and out = grad * min(1, max_norm / (norm + eps)) for every
+ * tensor, rounded once.  Where the factor is 1 gradients scaled in place are not
+ * touched.  An infinite norm leaves zeros and NaNs (0 times infinity), a NaN
+ * leaves NaNs.  No output may lie over another tensor (INVALID_ARG), so a tensor
+ * may not be given twice.  max_norm and eps >= 0. */
+int tiles_clip_grads(const tiles_grad_tensor* tensors, int64_t n, float max_norm, float eps,
+                     float* norm, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -122,3 +122,88 @@ def wgrad(a64, dc64, offsets):
         dw[g] = a64[r].T @ dc64[r]
         s[g] = np.abs(a64[r]).T @ np.abs(dc64[r])
     return dw, s
+
+
+# ---- layer norm -----------------------------------------------------------------------
+
+
+def layernorm(x64, w64, b64=None, r64=None, eps=1e-5):
+    """(y, h): h = x + r, y = (h - mean) / sqrt(var + eps) * w + b."""
+    h = x64 if r64 is None else x64 + r64
+    d = h - np.mean(h, axis=1, keepdims=True)
+    y = d / np.sqrt(np.mean(d * d, axis=1, keepdims=True) + eps) * w64
+    return (y if b64 is None else y + b64), h
+
+
+def layernorm_grad(dy64, h64, w64, dh64=None, eps=1e-5):
+    """(dx, dw, db)."""
+    d = h64 - np.mean(h64, axis=1, keepdims=True)
+    u = np.mean(d * d, axis=1, keepdims=True) + eps
+    g = dy64 * w64
+    dx = (g - np.mean(g, axis=1, keepdims=True)) / np.sqrt(u) - \
+        d * np.mean(g * d, axis=1, keepdims=True) / (u * np.sqrt(u))
+    if dh64 is not None:
+        dx = dx + dh64
+    return dx, (dy64 * d / np.sqrt(u)).sum(0), dy64.sum(0)
+
+
+# ---- rows to the experts and back -------------------------------------------------------
+
+
+def expert_sort(experts, groups):
+    """(slots, offsets, order) of the pairs' experts, pair by pair."""
+    tokens, k = experts.shape
+    rows = [[] for _ in range(groups)]
+    for p, e in enumerate(experts.reshape(-1).tolist()):
+        if 0 <= e < groups:
+            rows[e].append(p)
+    offsets = np.cumsum([0] + [len(r) for r in rows])
+    order = np.full(tokens * k, -1, np.int64)
+    slots = np.full(tokens * k, -1, np.int64)
+    placed = [p for r in rows for p in r]
+    order[:len(placed)] = placed
+    slots[placed] = np.arange(len(placed))
+    return slots.reshape(tokens, k), offsets, order
+
+
+def expert_dispatch(x64, slots, rows, fill=np.nan):
+    """Rows in expert order; those that no slot names hold `fill`."""
+    out = np.full((rows, x64.shape[1]), fill)
+    for t, j in np.ndindex(slots.shape):
+        if 0 <= slots[t, j] < rows:
+            out[slots[t, j]] = x64[t]
+    return out
+
+
+def expert_combine(rows64, slots, w64=None):
+    """(y, sum of magnitudes)."""
+    y = np.zeros((slots.shape[0], rows64.shape[1]))
+    s = np.zeros_like(y)
+    for t, j in np.ndindex(slots.shape):
+        if 0 <= slots[t, j] < rows64.shape[0]:
+            part = rows64[slots[t, j]] * (1.0 if w64 is None else w64[t, j])
+            y[t] += part
+            s[t] += np.abs(part)
+    return y, s
+
+
+def expert_combine_grad(dy64, rows64, slots, w64, fill=np.nan):
+    """(drows, dw, the magnitudes that dw sums); rows that no slot names hold `fill`."""
+    drows = np.full(rows64.shape, fill)
+    dw, s = np.zeros(slots.shape), np.zeros(slots.shape)
+    for t, j in np.ndindex(slots.shape):
+        if 0 <= slots[t, j] < rows64.shape[0]:
+            each = dy64[t] * rows64[slots[t, j]]
+            drows[slots[t, j]] = w64[t, j] * dy64[t]
+            dw[t, j], s[t, j] = each.sum(), np.abs(each).sum()
+    return drows, dw, s
+
+
+# ---- clipping ------------------------------------------------------------------------
+
+
+def clip(grads64, max_norm, eps=1e-6):
+    """(norm, scaled gradients)."""
+    norm = np.sqrt(sum(np.sum(g * g) for g in grads64))
+    scale = min(1.0, max_norm / (norm + eps)) if norm + eps > 0 else 1.0
+    return norm, [g * scale for g in grads64]

@@ -1,6 +1,7 @@
 """tile_size_decision_gb300 — constraint-planned tiled GEMM and H-tiled
 convolution for NVIDIA GB300 (sm_103a), with the norms, 8-bit products and
-expert-grouped products that surround the GEMM in a transformer block.
+expert-grouped products that surround the GEMM in a transformer block, the
+rows' way to the experts and back, and the clipping of gradients.
 
 A thin Python binding over libtiles.so (C ABI in include/tiles.h).  The
 binding only marshals arguments: planning (C0-C4), tensor-map encoding and
@@ -31,6 +32,9 @@ __all__ = [
     "make_config",
     "rmsnorm", "rmsnorm_fp8", "rmsnorm_grad", "rmsnorm_grad_workspace", "quantize_fp8",
     "gemm_fp8", "grouped_gemm", "grouped_gemm_fp8", "grouped_wgrad",
+    "layernorm", "layernorm_fp8", "layernorm_grad", "layernorm_grad_workspace",
+    "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_grad",
+    "grad_norm", "clip_grads",
 ]
 
 
@@ -556,7 +560,7 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
     _check(load().tiles_selftest_drop_stage(stage, limit_ns), "tiles_selftest_drop_stage")
 
 
-# ---- norms, 8-bit products and products grouped by expert ------------------------
+# ---- norms, 8-bit products, products grouped by expert, routing, clipping ---------
 #
 # These calls are short: a decoding step's norm or product takes a few
 # microseconds on the GPU, less than a dozen Python calls take.  So each one
@@ -575,7 +579,15 @@ class _NoCalls:
     """Stands in for the compiled calls where they were not built or do not load."""
 
     rmsnorm = rmsnorm_grad = product_fp8 = grouped_gemm = grouped_wgrad = \
-        staticmethod(lambda *args: None)
+        layernorm = layernorm_grad = expert_sort = expert_dispatch = expert_combine = \
+        expert_combine_grad = clip_grads = staticmethod(lambda *args: None)
+
+
+# Those that the compiled calls make, in the order in which they take their addresses.
+_BOUND = ("rmsnorm", "rmsnorm_grad", "gemm_fp8", "grouped_gemm", "grouped_wgrad", "layernorm",
+          "layernorm_grad", "layernorm_grad_workspace_bytes", "expert_sort",
+          "expert_sort_workspace_bytes", "expert_dispatch", "expert_combine",
+          "expert_combine_grad", "grad_norm", "clip_grads", "grad_norm_workspace_bytes")
 
 
 _CALLS = None
@@ -593,8 +605,8 @@ def _compiled():
             # Of another PyTorch, say: the long way does the same.
             warnings.warn(f"the compiled calls do not load, build them again: {e}")
         else:
-            calls.bind(*(C.cast(getattr(lib, "tiles_" + name), C.c_void_p).value for name in
-                         ("rmsnorm", "rmsnorm_grad", "gemm_fp8", "grouped_gemm", "grouped_wgrad")))
+            calls.bind(*(C.cast(getattr(lib, "tiles_" + name), C.c_void_p).value
+                         for name in _BOUND))
     _CALLS = calls
     return _CALLS
 
@@ -606,6 +618,12 @@ _NORM = struct.Struct("2q6Q6qf3i")
 _NORM_GRAD = struct.Struct("2q6Q4qf3i")
 _PRODUCT = struct.Struct("4q6Q9q4i")
 _WGRAD = struct.Struct("4q4Q4q2i")
+_LAYERNORM = struct.Struct("2q7Q6qf3i")
+_LAYERNORM_GRAD = struct.Struct("2q7Q4qf3i")
+_SORT = struct.Struct("3qQq3Q2i")
+_DISPATCH = struct.Struct("4q5Q7q2i")
+_COMBINE = struct.Struct("4q6Q6q2i")
+_GRAD_TENSOR = struct.Struct("2Qq2i")
 
 
 def _codes():
@@ -628,10 +646,10 @@ def _blocks(n):
     return (n + SCALE_BLOCK - 1) // SCALE_BLOCK
 
 
-def _refuse(*rules):
+def _demand(*rules):
     """Raises for the first (name, tensor, shape, dtype) that is not a CUDA tensor
     of that shape and type with unit stride in its last dimension (shape:
-    any where None; dtype: a type or several)."""
+    any where None; dtype: a type or several).  A tensor of None is not there."""
     for name, t, shape, dtype in rules:
         if t is None:
             continue
@@ -644,6 +662,11 @@ def _refuse(*rules):
         kinds = dtype if isinstance(dtype, (tuple, set)) else (dtype,)
         if t.dtype not in kinds:
             raise TypeError(f"{name} must be {' or '.join(sorted(map(str, kinds)))}, not {t.dtype}")
+
+
+def _refuse(*rules):
+    """_demand, of arguments that have something wrong with them."""
+    _demand(*rules)
     raise ValueError("unsupported arguments")
 
 
@@ -1007,3 +1030,336 @@ def grouped_wgrad(a, dc, offsets, out=None, out_dtype=None, workspace=None, stre
     ws, wsb = _workspace_args(workspace)
     _check(load().tiles_grouped_wgrad(d, ws, wsb, _raw_stream(stream)), "tiles_grouped_wgrad")
     return out
+
+
+def _pitch(t):
+    """Row pitch of a matrix; of a single row, which nothing uses, whole 16-byte pieces."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _scratch(workspace, nbytes, where, device):
+    """A call's workspace: the caller's, or memory of the call's own from the
+    current stream's pool (nothing then outlives the call, and calls on other
+    streams and captured graphs have theirs).  The kernels do not care what it
+    holds."""
+    if nbytes == 0:
+        raise TilesError(_abi.ERR_INVALID_ARG, where)
+    if workspace is None:
+        workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+    return (workspace, *_workspace_args(workspace))
+
+
+def _matrices(*named):
+    for name, t in named:
+        if t is not None and t.dim() != 2:
+            raise ValueError(f"{name} must be a matrix")
+
+
+def _fp8_scales(name, t, rows, nb):
+    if t.shape != (rows, nb) or t.dtype != _torch().float32 or not t.is_cuda:
+        raise ValueError(f"{name} must be a float32 CUDA tensor of shape {(rows, nb)}")
+
+
+def _layernorm(x, weight, bias, residual, eps, out, scales, h_out, stream, fp8):
+    torch, codes = _torch(), _codes()
+    _matrices(("x", x), ("residual", residual), ("out", out), ("h_out", h_out))
+    rows, cols = x.shape
+    y_type = torch.float8_e4m3fn if fp8 else x.dtype
+    _demand(("x", x, None, set(codes)), ("weight", weight, (cols,), set(codes)),
+            ("bias", bias, (cols,), weight.dtype), ("residual", residual, x.shape, x.dtype),
+            ("h_out", h_out, x.shape, x.dtype), ("out", out, x.shape, y_type))
+    if out is None:
+        # 8-bit rows: whole 16-byte pieces, as the products need.
+        pitch = (cols + 15) // 16 * 16 if fp8 else cols
+        out = torch.empty_strided((rows, cols), (pitch, 1), dtype=y_type, device=x.device)
+    sr = sb = 0
+    if fp8:
+        if scales is None:                    # stored block by block: the products' fastest order
+            scales = torch.empty_strided((rows, _blocks(cols)), (1, rows or 1),
+                                         dtype=torch.float32, device=x.device)
+        _fp8_scales("scales", scales, rows, _blocks(cols))
+        sr, sb = scales.stride()
+    if residual is not None and h_out is None:
+        h_out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    _here(x, weight, bias, residual, out, scales, h_out)
+    d = _LAYERNORM.pack(rows, cols, x.data_ptr(), _at(residual), weight.data_ptr(), _at(bias),
+                        _at(h_out), out.data_ptr(), _at(scales), _pitch(x),
+                        0 if residual is None else _pitch(residual),
+                        0 if h_out is None else _pitch(h_out), _pitch(out), sr, sb, eps,
+                        codes[x.dtype], codes[weight.dtype], _abi.E4M3 if fp8 else codes[x.dtype])
+    _check(load().tiles_layernorm(d, _raw_stream(stream)), "tiles_layernorm")
+    return out, scales, x if h_out is None else h_out
+
+
+def layernorm(x, weight, bias=None, residual=None, eps=1e-5, out=None, h_out=None, stream=None):
+    """h = x + residual and y = (h - mean(h)) * (var(h) + eps)^(-1/2) * weight +
+    bias, row by row of a matrix; returns (y, h) in x's type.  Without a
+    residual h is x itself, or a copy of it in h_out.  h_out may be the
+    residual (updated in place)."""
+    r = (_CALLS or _compiled()).layernorm(x, weight, bias, residual, eps, out, None, h_out, stream,
+                                          False)
+    if r is None:
+        with _on(stream):
+            r = _layernorm(x, weight, bias, residual, eps, out, None, h_out, stream, False)
+    return r[0], r[2]
+
+
+def layernorm_fp8(x, weight, bias=None, residual=None, eps=1e-5, out=None, scales=None, h_out=None,
+                  stream=None):
+    """The norm of layernorm with y in 8 bits: returns (q, scales, h) as
+    rmsnorm_fp8 does, for gemm_fp8 and grouped_gemm_fp8."""
+    r = (_CALLS or _compiled()).layernorm(x, weight, bias, residual, eps, out, scales, h_out,
+                                          stream, True)
+    if r is None:
+        with _on(stream):
+            r = _layernorm(x, weight, bias, residual, eps, out, scales, h_out, stream, True)
+    return r
+
+
+def layernorm_grad_workspace(x):
+    """A workspace for layernorm_grad on matrices of x's shape."""
+    rows, cols = x.shape
+    n = int(load().tiles_layernorm_grad_workspace_bytes(rows, cols))
+    if n == 0:
+        raise TilesError(_abi.ERR_INVALID_ARG, "tiles_layernorm_grad_workspace_bytes")
+    return _torch().zeros(n, dtype=_torch().uint8, device=x.device)
+
+
+def layernorm_grad(dy, h, weight, eps=1e-5, dh=None, dx_out=None, dweight_out=None, dbias_out=None,
+                   workspace=None, stream=None):
+    """Gradients of layernorm at h, given those of y (dy) and, where h is used
+    past the norm, of h (dh): returns (dx, dweight, dbias).  dx, in h's type,
+    is the gradient of x and of the residual alike; dweight and dbias are
+    fp32.  Without a workspace the call takes memory of its own."""
+    r = (_CALLS or _compiled()).layernorm_grad(dy, h, weight, eps, dh, dx_out, dweight_out,
+                                               dbias_out, workspace, stream)
+    if r is not None:
+        return r
+    torch, codes = _torch(), _codes()
+    _matrices(("h", h), ("dy", dy), ("dh", dh), ("dx_out", dx_out))
+    rows, cols = h.shape
+    f32 = torch.float32
+    _demand(("h", h, None, set(codes)), ("dy", dy, h.shape, h.dtype),
+            ("weight", weight, (cols,), set(codes)), ("dh", dh, h.shape, h.dtype),
+            ("dx_out", dx_out, h.shape, h.dtype), ("dweight_out", dweight_out, (cols,), f32),
+            ("dbias_out", dbias_out, (cols,), f32))
+    _here(dy, h, weight, dh, dx_out, dweight_out, dbias_out)
+    with _on(stream):
+        dx = torch.empty((rows, cols), dtype=h.dtype, device=h.device) if dx_out is None else dx_out
+        dw, db = (torch.empty(cols, dtype=f32, device=h.device) if t is None else t
+                  for t in (dweight_out, dbias_out))
+        n = int(load().tiles_layernorm_grad_workspace_bytes(rows, cols))
+        keep, ws, wsb = _scratch(workspace, n, "tiles_layernorm_grad_workspace_bytes", h.device)
+    d = _LAYERNORM_GRAD.pack(rows, cols, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _at(dh),
+                             dx.data_ptr(), dw.data_ptr(), db.data_ptr(), _pitch(dy), _pitch(h),
+                             0 if dh is None else _pitch(dh), _pitch(dx), eps, codes[h.dtype],
+                             codes[weight.dtype], 0)
+    _check(load().tiles_layernorm_grad(d, ws, wsb, _raw_stream(stream)), "tiles_layernorm_grad")
+    return dx, dw, db
+
+
+def expert_sort(experts, groups, workspace=None, stream=None):
+    """The stable sort of a router's choices by expert.  experts: an int32 or
+    int64 matrix, tokens x k, of ids.  Returns int32 tensors (slots, offsets,
+    order): slots[t, j] is the row of the pair (t, j) in expert order, offsets
+    (groups + 1) the experts' first rows, as the grouped products take them,
+    and order[row] the pair t * k + j of a row.  A pair whose id is outside
+    [0, groups), as padding's -1, has the slot -1 and no row: the rows past
+    offsets[groups] are nobody's, and their order is -1."""
+    r = (_CALLS or _compiled()).expert_sort(experts, groups, workspace, stream)
+    if r is not None:
+        return r
+    torch = _torch()
+    _matrices(("experts", experts))
+    _demand(("experts", experts, None, (torch.int32, torch.int64)))
+    _here(experts)
+    tokens, k = experts.shape
+    n = int(load().tiles_expert_sort_workspace_bytes(tokens, k, groups))
+    with _on(stream):
+        keep, ws, wsb = _scratch(workspace, n, "tiles_expert_sort", experts.device)
+        slots = torch.empty((tokens, k), dtype=torch.int32, device=experts.device)
+        offsets = torch.empty(groups + 1, dtype=torch.int32, device=experts.device)
+        order = torch.empty(tokens * k, dtype=torch.int32, device=experts.device)
+    d = _SORT.pack(tokens, k, groups, experts.data_ptr(), _pitch(experts), slots.data_ptr(),
+                   offsets.data_ptr(), order.data_ptr(), experts.element_size(), 0)
+    _check(load().tiles_expert_sort(d, ws, wsb, _raw_stream(stream)), "tiles_expert_sort")
+    return slots, offsets, order
+
+
+def expert_dispatch(x, slots, scales=None, out=None, scales_out=None, stream=None):
+    """Rows in expert order: out[slots[t, j]] = x[t] for fp16, bf16, fp32 or
+    e4m3 rows; slots (tokens x k) as expert_sort gives them.  out has a row for
+    every pair unless it is given; rows that no slot names are not written.
+    With the scales of 8-bit rows (tokens x blocks) returns (out, their scales
+    in expert order, stored block by block); else out.  Its gradient is
+    expert_combine without weights."""
+    r = (_CALLS or _compiled()).expert_dispatch(x, slots, scales, out, scales_out, stream)
+    if r is not None:
+        return r
+    torch, codes = _torch(), _codes()
+    fp8 = torch.float8_e4m3fn
+    _matrices(("x", x), ("slots", slots), ("out", out))
+    tokens, cols = x.shape
+    _demand(("x", x, None, {*codes, fp8}), ("slots", slots, (tokens, slots.shape[1]), torch.int32),
+            ("out", out, None if out is None else (out.shape[0], cols), x.dtype))
+    if scales is None and scales_out is not None:
+        raise ValueError("scales_out goes with scales")
+    k, nb = slots.shape[1], _blocks(cols)
+    rows = tokens * k if out is None else out.shape[0]
+    with _on(stream):
+        if out is None:
+            pitch = (cols + 15) // 16 * 16 if x.dtype == fp8 else cols
+            out = torch.empty_strided((rows, cols), (pitch, 1), dtype=x.dtype, device=x.device)
+        if scales is not None and scales_out is None:
+            scales_out = torch.empty_strided((rows, nb), (1, rows or 1), dtype=torch.float32,
+                                             device=x.device)
+    strides = (0, 0, 0, 0)
+    if scales is not None:
+        _fp8_scales("scales", scales, tokens, nb)
+        _fp8_scales("scales_out", scales_out, rows, nb)
+        strides = (*scales.stride(), *scales_out.stride())
+    _here(x, slots, scales, out, scales_out)
+    d = _DISPATCH.pack(tokens, k, rows, cols, slots.data_ptr(), x.data_ptr(), out.data_ptr(),
+                       _at(scales), _at(scales_out), _pitch(slots), _pitch(x), _pitch(out),
+                       *strides, _abi.E4M3 if x.dtype == fp8 else codes[x.dtype], 0)
+    _check(load().tiles_expert_dispatch(d, _raw_stream(stream)), "tiles_expert_dispatch")
+    return out if scales is None else (out, scales_out)
+
+
+def expert_combine(rows, slots, weights=None, out=None, stream=None):
+    """Rows back to their tokens: out[t] = sum over j of weights[t, j] *
+    rows[slots[t, j]], in fp32, rounded once to the rows' type (fp16, bf16 or
+    fp32).  Slots of -1 add nothing; a token without any is zero.  Without
+    weights it is the plain sum, the gradient of expert_dispatch."""
+    r = (_CALLS or _compiled()).expert_combine(rows, slots, weights, out, stream)
+    if r is not None:
+        return r
+    torch, codes = _torch(), _codes()
+    _matrices(("rows", rows), ("slots", slots))
+    (n, cols), (tokens, k) = rows.shape, slots.shape
+    _demand(("rows", rows, None, set(codes)), ("slots", slots, None, torch.int32),
+            ("weights", weights, (tokens, k), set(codes)), ("out", out, (tokens, cols), rows.dtype))
+    if out is None:
+        with _on(stream):
+            out = torch.empty((tokens, cols), dtype=rows.dtype, device=rows.device)
+    _here(rows, slots, weights, out)
+    d = _COMBINE.pack(tokens, k, n, cols, slots.data_ptr(), _at(weights), rows.data_ptr(), 0,
+                      out.data_ptr(), 0, _pitch(slots), 0 if weights is None else _pitch(weights),
+                      _pitch(rows), 0, _pitch(out), 0, codes[rows.dtype],
+                      0 if weights is None else codes[weights.dtype])
+    _check(load().tiles_expert_combine(d, _raw_stream(stream)), "tiles_expert_combine")
+    return out
+
+
+def expert_combine_grad(dy, rows, slots, weights, drows_out=None, dweights_out=None, stream=None):
+    """Gradients of expert_combine, given that of its output: returns (drows,
+    dweights) with drows[slots[t, j]] = weights[t, j] * dy[t] in the rows' type
+    (rows that no slot names are not written) and dweights[t, j] = dy[t] .
+    rows[slots[t, j]] in fp32 (0 for slots of -1)."""
+    r = (_CALLS or _compiled()).expert_combine_grad(dy, rows, slots, weights, drows_out,
+                                                    dweights_out, stream)
+    if r is not None:
+        return r
+    torch, codes = _torch(), _codes()
+    _matrices(("rows", rows), ("slots", slots))
+    (n, cols), (tokens, k) = rows.shape, slots.shape
+    _demand(("rows", rows, None, set(codes)), ("dy", dy, (tokens, cols), rows.dtype),
+            ("slots", slots, None, torch.int32), ("weights", weights, (tokens, k), set(codes)),
+            ("drows_out", drows_out, rows.shape, rows.dtype),
+            ("dweights_out", dweights_out, (tokens, k), torch.float32))
+    with _on(stream):
+        drows = torch.empty((n, cols), dtype=rows.dtype, device=rows.device) \
+            if drows_out is None else drows_out
+        dw = torch.empty((tokens, k), dtype=torch.float32, device=rows.device) \
+            if dweights_out is None else dweights_out
+    _here(dy, rows, slots, weights, drows, dw)
+    d = _COMBINE.pack(tokens, k, n, cols, slots.data_ptr(), weights.data_ptr(), rows.data_ptr(),
+                      dy.data_ptr(), drows.data_ptr(), dw.data_ptr(), _pitch(slots),
+                      _pitch(weights), _pitch(rows), _pitch(dy), _pitch(drows), _pitch(dw),
+                      codes[rows.dtype], codes[weights.dtype])
+    _check(load().tiles_expert_combine_grad(d, _raw_stream(stream)), "tiles_expert_combine_grad")
+    return drows, dw
+
+
+def _dense(t):
+    """Whether a tensor's elements fill one run of memory, each once, in any order."""
+    step = 1
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1),
+                               key=lambda p: p[1]):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _clip(grads, max_norm, eps, out, workspace, stream):
+    torch, codes = _torch(), _codes()
+    if not grads:
+        raise ValueError("there are no gradients")
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
+    packed = bytearray()
+    for i, g in enumerate(grads):
+        o = None if out is None else out[i]
+        for name, t in ((f"grads[{i}]", g), (f"out[{i}]", o))[:1 if out is None else 2]:
+            if not hasattr(t, "data_ptr"):
+                raise TypeError(f"{name} must be a tensor")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dtype not in codes:
+                raise TypeError(f"{name} must be {' or '.join(sorted(map(str, codes)))}, "
+                                f"not {t.dtype}")
+            if t.numel() and not _dense(t):
+                raise ValueError(f"{name}: its elements must lie together")
+        if o is not None:
+            if o.shape != g.shape or o.dtype != g.dtype or \
+                    (g.numel() and any(a != b for n, a, b in zip(g.shape, g.stride(), o.stride())
+                                       if n > 1)):
+                raise ValueError(f"out[{i}] must have the shape, the type and the strides of its "
+                                 "gradient")
+        _here(g, o)
+        packed += _GRAD_TENSOR.pack(g.data_ptr(), _at(o), g.numel(), codes[g.dtype], 0)
+    n = int(load().tiles_grad_norm_workspace_bytes(len(grads)))
+    where = "tiles_grad_norm" if max_norm is None else "tiles_clip_grads"
+    with _on(stream):
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        keep, ws, wsb = _scratch(workspace, n, where, grads[0].device)
+    if max_norm is None:
+        s = load().tiles_grad_norm(bytes(packed), len(grads), norm.data_ptr(), ws, wsb,
+                                   _raw_stream(stream))
+    else:
+        s = load().tiles_clip_grads(bytes(packed), len(grads), max_norm, eps, norm.data_ptr(), ws,
+                                    wsb, _raw_stream(stream))
+    _check(s, where)
+    return norm
+
+
+def _listed(tensors):
+    """A list of tensors: of one, of any iterable."""
+    return [tensors] if hasattr(tensors, "data_ptr") else list(tensors)
+
+
+def grad_norm(grads, workspace=None, stream=None):
+    """The square root of the sum of all elements' squares over a list of
+    gradients (fp16, bf16, fp32, mixed as they come; elements that lie together,
+    in any order): an fp32 tensor without dimensions, which stays on the
+    device."""
+    grads = _listed(grads)
+    r = (_CALLS or _compiled()).clip_grads(grads, None, 0.0, None, workspace, stream)
+    return _clip(grads, None, 0.0, None, workspace, stream) if r is None else r
+
+
+def clip_grads(grads, max_norm, eps=1e-6, out=None, workspace=None, stream=None):
+    """Scales a list of gradients by min(1, max_norm / (norm + eps)), with norm as
+    grad_norm gives it, in place or into the tensors of out; returns the norm
+    before.  Nothing waits for the device.  No tensor may come twice or overlap
+    another.  An infinite norm leaves zeros and NaNs, a NaN leaves NaNs."""
+    grads, out = _listed(grads), None if out is None else _listed(out)
+    if max_norm is None:
+        raise TypeError("max_norm must be a number")
+    r = (_CALLS or _compiled()).clip_grads(grads, max_norm, eps, out, workspace, stream)
+    return _clip(grads, float(max_norm), float(eps), out, workspace, stream) if r is None else r

@@ -166,6 +166,35 @@ class WgradDesc(C.Structure):
                        "i32 in_dtype out_dtype")
 
 
+class LayernormDesc(C.Structure):
+    _fields_ = _fields("i64 rows cols; ptr x residual weight bias h y scales; i64 ldx ldr ldh ldy "
+                       "scale_row scale_block; f32 eps; i32 dtype weight_dtype out_dtype")
+
+
+class LayernormGradDesc(C.Structure):
+    _fields_ = _fields("i64 rows cols; ptr dy h weight dh dx dweight dbias; i64 lddy ldh lddh lddx; "
+                       "f32 eps; i32 dtype weight_dtype pad0")
+
+
+class ExpertSortDesc(C.Structure):
+    _fields_ = _fields("i64 tokens k groups; ptr experts; i64 ld; ptr slots offsets order; "
+                       "i32 index_bytes pad0")
+
+
+class DispatchDesc(C.Structure):
+    _fields_ = _fields("i64 tokens k rows cols; ptr slots x out scales out_scales; i64 ld_slots ldx "
+                       "ld_out scale_row scale_block out_scale_row out_scale_block; i32 dtype pad0")
+
+
+class CombineDesc(C.Structure):
+    _fields_ = _fields("i64 tokens k rows cols; ptr slots weights in_ dy out dweights; i64 ld_slots "
+                       "ld_weights ld_in ld_dy ld_out ld_dweights; i32 dtype weight_dtype")
+
+
+class GradTensor(C.Structure):
+    _fields_ = _fields("ptr grad out; i64 count; i32 dtype pad0")
+
+
 B_KN, B_NK = 0, 1
 
 
@@ -230,6 +259,19 @@ SIGNATURES = {
     "tiles_gemm_fp8": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "tiles_grouped_gemm": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
     "tiles_grouped_wgrad": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_layernorm": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "tiles_layernorm_grad_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "tiles_layernorm_grad": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_expert_sort_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64]),
+    "tiles_expert_sort": (C.c_int, [C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "tiles_expert_dispatch": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "tiles_expert_combine": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "tiles_expert_combine_grad": (C.c_int, [C.c_void_p, C.c_void_p]),
+    "tiles_grad_norm_workspace_bytes": (C.c_size_t, [C.c_int64]),
+    "tiles_grad_norm": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_size_t,
+                                  C.c_void_p]),
+    "tiles_clip_grads": (C.c_int, [C.c_void_p, C.c_int64, C.c_float, C.c_float, C.c_void_p,
+                                   C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 _lib = None

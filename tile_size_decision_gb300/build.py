@@ -52,6 +52,9 @@ def units():
         ("conv_tma_sm103a.cu", "conv_tma_sm103a.o", []),
         ("host_pipeline.cu", "host_pipeline.o", []),
         ("norm_sm103a.cu", "norm_sm103a.o", []),
+        ("layernorm_sm103a.cu", "layernorm_sm103a.o", []),
+        ("route_sm103a.cu", "route_sm103a.o", []),
+        ("clip_sm103a.cu", "clip_sm103a.o", []),
         ("stream_sm103a.cu", "stream_sm103a.o", []),
         ("pair_sm103a.cu", "pair_sm103a.o", []),
         ("pair8_sm103a.cu", "pair8_sm103a.o", []),

@@ -1,5 +1,5 @@
-// The short calls on PyTorch tensors (norms, 8-bit and grouped products), as a
-// Python module.  A decoding step's norm or product takes a few microseconds
+// The short calls on PyTorch tensors (norms, 8-bit and grouped products, routing,
+// clipping), as a Python module.  A decoding step's norm or product takes a few microseconds
 // on the GPU, and marshalling it in Python takes more: here the arguments are
 // read, checked, the outputs allocated and the C call made without going
 // through Python objects.  (Per call on the host: the norm of one row of 4096
@@ -18,6 +18,7 @@
 
 #include <cstring>
 #include <optional>
+#include <vector>
 
 #include "tiles.h"
 
@@ -36,6 +37,17 @@ struct Calls {
     int (*gemm_fp8)(const tiles_product_desc*, void*, size_t, void*);
     int (*grouped_gemm)(const tiles_product_desc*, void*, size_t, void*);
     int (*grouped_wgrad)(const tiles_wgrad_desc*, void*, size_t, void*);
+    int (*layernorm)(const tiles_layernorm_desc*, void*);
+    int (*layernorm_grad)(const tiles_layernorm_grad_desc*, void*, size_t, void*);
+    size_t (*layernorm_grad_workspace_bytes)(int64_t, int64_t);
+    int (*expert_sort)(const tiles_expert_sort_desc*, void*, size_t, void*);
+    size_t (*expert_sort_workspace_bytes)(int64_t, int64_t, int64_t);
+    int (*expert_dispatch)(const tiles_dispatch_desc*, void*);
+    int (*expert_combine)(const tiles_combine_desc*, void*);
+    int (*expert_combine_grad)(const tiles_combine_desc*, void*);
+    int (*grad_norm)(const tiles_grad_tensor*, int64_t, float*, void*, size_t, void*);
+    int (*clip_grads)(const tiles_grad_tensor*, int64_t, float, float, float*, void*, size_t, void*);
+    size_t (*grad_norm_workspace_bytes)(int64_t);
 } calls;
 
 constexpr auto kE4m3 = at::ScalarType::Float8_e4m3fn;
@@ -471,18 +483,409 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
     });
 }
 
-// The five addresses, in the order of Calls.
+// A call's workspace: the caller's, or memory of the call's own from the current
+// stream's pool (call under OnStream), which goes back there when the call is
+// made: whatever takes it next on the stream runs after the call's kernels.
+struct Scratch {
+    Workspace given;
+    at::Tensor own;
+
+    Scratch(PyObject* o, size_t bytes, const at::Tensor& like) : given(o) {
+        require(bytes > 0);
+        if (given.at) return;
+        own = empty(like, {static_cast<int64_t>(bytes)}, {1}, at::ScalarType::Byte);
+        given.at = own.data_ptr();
+        given.bytes = bytes;
+    }
+};
+
+// A new output, or the caller's argument.
+PyObject* made_or(at::Tensor& made, PyObject* arg) {
+    return made.defined() ? THPVariable_Wrap(std::move(made)) : given(arg);
+}
+
+// x, weight, bias, residual, eps, out, scales, h_out, stream, fp8 -> (y, scales, h)
+PyObject* layernorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        require(n == 10);
+        const at::Tensor &x = tensor(args[0]), &weight = tensor(args[1]);
+        const at::Tensor *bias = optional_tensor(args[2]), *residual = optional_tensor(args[3]),
+                         *out = optional_tensor(args[5]), *scales = optional_tensor(args[6]),
+                         *h_out = optional_tensor(args[7]);
+        const bool fp8 = args[9] == Py_True;
+        const OnStream stream(args[8]);
+        const Matrix mx(x);
+        const at::ScalarType dtype = x.scalar_type(), out_dtype = fp8 ? kE4m3 : dtype;
+        tiles_layernorm_desc d{};
+        d.rows = mx.rows;
+        d.cols = mx.cols;
+        d.ldx = mx.ld;
+        d.dtype = code_of(dtype);
+        d.weight_dtype = code_of(weight.scalar_type());
+        d.out_dtype = fp8 ? TILES_E4M3 : d.dtype;
+        d.eps = number(args[4]);
+        require(is_vector(weight, mx.cols, weight.scalar_type()) &&
+                (!bias || is_vector(*bias, mx.cols, weight.scalar_type())));
+        at::Tensor new_out, new_scales, new_h;
+        if (out) {
+            const Matrix m(*out);
+            require(m.like(mx) && out->scalar_type() == out_dtype);
+            d.ldy = m.ld;
+        } else {
+            d.ldy = fp8 ? (mx.cols + 15) / 16 * 16 : mx.cols;
+            new_out = empty_matrix(x, mx.rows, mx.cols, d.ldy, out_dtype);
+            out = &new_out;
+        }
+        if (fp8) {
+            const int64_t nb = (mx.cols + 127) / 128;
+            if (scales) {
+                require(scales->dim() == 2 && scales->size(0) == mx.rows && scales->size(1) == nb &&
+                        scales->scalar_type() == at::ScalarType::Float);
+            } else {
+                new_scales = empty(x, {mx.rows, nb}, {1, mx.rows > 0 ? mx.rows : 1},
+                                   at::ScalarType::Float);
+                scales = &new_scales;
+            }
+            d.scale_row = scales->stride(0);
+            d.scale_block = scales->stride(1);
+            d.scales = static_cast<float*>(scales->data_ptr());
+        }
+        if (residual) {
+            const Matrix m(*residual);
+            require(m.like(mx) && residual->scalar_type() == dtype);
+            d.residual = residual->data_ptr();
+            d.ldr = m.ld;
+            if (!h_out) {
+                new_h = empty_matrix(x, mx.rows, mx.cols, mx.cols, dtype);
+                h_out = &new_h;
+            }
+        }
+        if (h_out) {
+            const Matrix mh(*h_out);
+            require(mh.like(mx) && h_out->scalar_type() == dtype);
+            d.ldh = mh.ld;
+            d.h = h_out->data_ptr();
+        }
+        d.x = x.data_ptr();
+        d.weight = weight.data_ptr();
+        d.bias = bias ? bias->data_ptr() : nullptr;
+        d.y = out->data_ptr();
+        run([&] { return calls.layernorm(&d, stream.at); });
+        PyObject* h = new_h.defined() ? THPVariable_Wrap(std::move(new_h))
+                                      : given(h_out ? args[7] : args[0]);
+        PyObject* r = PyTuple_New(3);
+        PyTuple_SET_ITEM(r, 0, made_or(new_out, args[5]));
+        PyTuple_SET_ITEM(r, 1, made_or(new_scales, args[6]));
+        PyTuple_SET_ITEM(r, 2, h);
+        return r;
+    });
+}
+
+// dy, h, weight, eps, dh, dx_out, dweight_out, dbias_out, workspace, stream
+// -> (dx, dweight, dbias)
+PyObject* layernorm_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        require(n == 10);
+        const at::Tensor &dy = tensor(args[0]), &h = tensor(args[1]), &weight = tensor(args[2]);
+        const at::Tensor *dh = optional_tensor(args[4]), *dx = optional_tensor(args[5]);
+        const OnStream stream(args[9]);
+        const Matrix mh(h), mdy(dy);
+        const at::ScalarType dtype = h.scalar_type();
+        require(mdy.like(mh) && dy.scalar_type() == dtype &&
+                is_vector(weight, mh.cols, weight.scalar_type()));
+        tiles_layernorm_grad_desc d{};
+        d.rows = mh.rows;
+        d.cols = mh.cols;
+        d.ldh = mh.ld;
+        d.lddy = mdy.ld;
+        d.dtype = code_of(dtype);
+        d.weight_dtype = code_of(weight.scalar_type());
+        d.eps = number(args[3]);
+        if (dh) {
+            const Matrix m(*dh);
+            require(m.like(mh) && dh->scalar_type() == dtype);
+            d.dh = dh->data_ptr();
+            d.lddh = m.ld;
+        }
+        at::Tensor new_dx, new_sum[2];
+        if (dx) {
+            const Matrix m(*dx);
+            require(m.like(mh) && dx->scalar_type() == dtype);
+            d.lddx = m.ld;
+        } else {
+            d.lddx = mh.cols;
+            new_dx = empty_matrix(h, mh.rows, mh.cols, mh.cols, dtype);
+            dx = &new_dx;
+        }
+        float* sums[2];
+        for (int i = 0; i < 2; ++i) {
+            const at::Tensor* t = optional_tensor(args[6 + i]);
+            if (t) {
+                require(is_vector(*t, mh.cols, at::ScalarType::Float));
+            } else {
+                new_sum[i] = empty(h, {mh.cols}, {1}, at::ScalarType::Float);
+                t = &new_sum[i];
+            }
+            sums[i] = static_cast<float*>(t->data_ptr());
+        }
+        d.dy = dy.data_ptr();
+        d.h = h.data_ptr();
+        d.weight = weight.data_ptr();
+        d.dx = dx->data_ptr();
+        d.dweight = sums[0];
+        d.dbias = sums[1];
+        const Scratch ws(args[8], calls.layernorm_grad_workspace_bytes(d.rows, d.cols), h);
+        run([&] { return calls.layernorm_grad(&d, ws.given.at, ws.given.bytes, stream.at); });
+        PyObject* r = PyTuple_New(3);
+        PyTuple_SET_ITEM(r, 0, made_or(new_dx, args[5]));
+        PyTuple_SET_ITEM(r, 1, made_or(new_sum[0], args[6]));
+        PyTuple_SET_ITEM(r, 2, made_or(new_sum[1], args[7]));
+        return r;
+    });
+}
+
+// experts, groups, workspace, stream -> (slots, offsets, order)
+PyObject* expert_sort(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        require(n == 4);
+        const at::Tensor& experts = tensor(args[0]);
+        const OnStream stream(args[3]);
+        const Matrix m(experts);
+        const at::ScalarType dtype = experts.scalar_type();
+        require(dtype == at::ScalarType::Int || dtype == at::ScalarType::Long);
+        tiles_expert_sort_desc d{};
+        d.tokens = m.rows;
+        d.k = m.cols;
+        d.groups = PyLong_AsLongLong(args[1]);
+        require(!PyErr_Occurred());
+        d.experts = experts.data_ptr();
+        d.ld = m.ld;
+        d.index_bytes = dtype == at::ScalarType::Long ? 8 : 4;
+        const Scratch ws(args[2], calls.expert_sort_workspace_bytes(d.tokens, d.k, d.groups), experts);
+        const auto type = at::ScalarType::Int;
+        at::Tensor slots = empty_matrix(experts, m.rows, m.cols, m.cols, type);
+        at::Tensor offsets = empty(experts, {d.groups + 1}, {1}, type);
+        at::Tensor order = empty(experts, {m.rows * m.cols}, {1}, type);
+        d.slots = static_cast<int32_t*>(slots.data_ptr());
+        d.offsets = static_cast<int32_t*>(offsets.data_ptr());
+        d.order = static_cast<int32_t*>(order.data_ptr());
+        run([&] { return calls.expert_sort(&d, ws.given.at, ws.given.bytes, stream.at); });
+        PyObject* r = PyTuple_New(3);
+        PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(slots)));
+        PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(offsets)));
+        PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(order)));
+        return r;
+    });
+}
+
+// The slots of `tokens` tokens (any number where tokens < 0).
+Matrix slots_of(const at::Tensor& t, int64_t tokens) {
+    const Matrix m(t);
+    require(t.scalar_type() == at::ScalarType::Int && (tokens < 0 || m.rows == tokens));
+    return m;
+}
+
+// x, slots, scales, out, scales_out, stream -> out, or (out, scales)
+PyObject* expert_dispatch(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        require(n == 6);
+        const at::Tensor &x = tensor(args[0]), &slots = tensor(args[1]);
+        const at::Tensor *scales = optional_tensor(args[2]), *out = optional_tensor(args[3]),
+                         *scales_out = optional_tensor(args[4]);
+        const OnStream stream(args[5]);
+        const Matrix mx(x), ms = slots_of(slots, mx.rows);
+        const at::ScalarType dtype = x.scalar_type();
+        const bool fp8 = dtype == kE4m3;
+        tiles_dispatch_desc d{};
+        d.tokens = mx.rows;
+        d.cols = mx.cols;
+        d.k = ms.cols;
+        d.ldx = mx.ld;
+        d.ld_slots = ms.ld;
+        d.dtype = fp8 ? TILES_E4M3 : code_of(dtype);
+        at::Tensor new_out, new_scales;
+        if (out) {
+            const Matrix m(*out);
+            require(m.cols == mx.cols && out->scalar_type() == dtype);
+            d.rows = m.rows;
+            d.ld_out = m.ld;
+        } else {
+            d.rows = d.tokens * d.k;
+            d.ld_out = fp8 ? (mx.cols + 15) / 16 * 16 : mx.cols;
+            new_out = empty_matrix(x, d.rows, mx.cols, d.ld_out, dtype);
+            out = &new_out;
+        }
+        require(scales || !scales_out);
+        if (scales) {
+            const int64_t nb = (mx.cols + 127) / 128;
+            if (!scales_out) {
+                new_scales = empty(x, {d.rows, nb}, {1, d.rows > 0 ? d.rows : 1}, at::ScalarType::Float);
+                scales_out = &new_scales;
+            }
+            require(scales->dim() == 2 && scales->size(0) == d.tokens && scales->size(1) == nb &&
+                    scales->scalar_type() == at::ScalarType::Float && scales_out->dim() == 2 &&
+                    scales_out->size(0) == d.rows && scales_out->size(1) == nb &&
+                    scales_out->scalar_type() == at::ScalarType::Float);
+            d.scales = static_cast<const float*>(scales->data_ptr());
+            d.out_scales = static_cast<float*>(scales_out->data_ptr());
+            d.scale_row = scales->stride(0);
+            d.scale_block = scales->stride(1);
+            d.out_scale_row = scales_out->stride(0);
+            d.out_scale_block = scales_out->stride(1);
+        }
+        d.x = x.data_ptr();
+        d.slots = static_cast<const int32_t*>(slots.data_ptr());
+        d.out = out->data_ptr();
+        run([&] { return calls.expert_dispatch(&d, stream.at); });
+        if (!scales) return made_or(new_out, args[3]);
+        PyObject* r = PyTuple_New(2);
+        PyTuple_SET_ITEM(r, 0, made_or(new_out, args[3]));
+        PyTuple_SET_ITEM(r, 1, made_or(new_scales, args[4]));
+        return r;
+    });
+}
+
+// What the sum and its gradients have in common.
+tiles_combine_desc combine_of(const at::Tensor& rows, const at::Tensor& slots,
+                              const at::Tensor* weights) {
+    const Matrix mr(rows), ms = slots_of(slots, -1);
+    tiles_combine_desc d{};
+    d.tokens = ms.rows;
+    d.k = ms.cols;
+    d.rows = mr.rows;
+    d.cols = mr.cols;
+    d.ld_slots = ms.ld;
+    d.ld_in = mr.ld;
+    d.dtype = code_of(rows.scalar_type());
+    d.slots = static_cast<const int32_t*>(slots.data_ptr());
+    d.in = rows.data_ptr();
+    if (weights) {
+        const Matrix m(*weights);
+        require(m.like(ms));
+        d.weights = weights->data_ptr();
+        d.ld_weights = m.ld;
+        d.weight_dtype = code_of(weights->scalar_type());
+    }
+    return d;
+}
+
+// rows, slots, weights, out, stream -> out
+PyObject* expert_combine(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        require(n == 5);
+        const at::Tensor& rows = tensor(args[0]);
+        const at::Tensor* out = optional_tensor(args[3]);
+        const OnStream stream(args[4]);
+        tiles_combine_desc d = combine_of(rows, tensor(args[1]), optional_tensor(args[2]));
+        at::Tensor made;
+        if (out) {
+            const Matrix m(*out);
+            require(m.rows == d.tokens && m.cols == d.cols && out->scalar_type() == rows.scalar_type());
+            d.ld_out = m.ld;
+        } else {
+            d.ld_out = d.cols;
+            made = empty_matrix(rows, d.tokens, d.cols, d.cols, rows.scalar_type());
+            out = &made;
+        }
+        d.out = out->data_ptr();
+        run([&] { return calls.expert_combine(&d, stream.at); });
+        return made_or(made, args[3]);
+    });
+}
+
+// dy, rows, slots, weights, drows_out, dweights_out, stream -> (drows, dweights)
+PyObject* expert_combine_grad(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        require(n == 7);
+        const at::Tensor &dy = tensor(args[0]), &rows = tensor(args[1]), &weights = tensor(args[3]);
+        const at::Tensor *drows = optional_tensor(args[4]), *dweights = optional_tensor(args[5]);
+        const OnStream stream(args[6]);
+        tiles_combine_desc d = combine_of(rows, tensor(args[2]), &weights);
+        const Matrix mdy(dy);
+        const at::ScalarType dtype = rows.scalar_type();
+        require(mdy.rows == d.tokens && mdy.cols == d.cols && dy.scalar_type() == dtype);
+        d.dy = dy.data_ptr();
+        d.ld_dy = mdy.ld;
+        at::Tensor new_rows, new_weights;
+        if (drows) {
+            const Matrix m(*drows);
+            require(m.rows == d.rows && m.cols == d.cols && drows->scalar_type() == dtype);
+            d.ld_out = m.ld;
+        } else {
+            d.ld_out = d.cols;
+            new_rows = empty_matrix(rows, d.rows, d.cols, d.cols, dtype);
+            drows = &new_rows;
+        }
+        if (dweights) {
+            const Matrix m(*dweights);
+            require(m.rows == d.tokens && m.cols == d.k && dweights->scalar_type() == at::ScalarType::Float);
+            d.ld_dweights = m.ld;
+        } else {
+            d.ld_dweights = d.k;
+            new_weights = empty_matrix(rows, d.tokens, d.k, d.k, at::ScalarType::Float);
+            dweights = &new_weights;
+        }
+        d.out = drows->data_ptr();
+        d.dweights = static_cast<float*>(dweights->data_ptr());
+        run([&] { return calls.expert_combine_grad(&d, stream.at); });
+        PyObject* r = PyTuple_New(2);
+        PyTuple_SET_ITEM(r, 0, made_or(new_rows, args[4]));
+        PyTuple_SET_ITEM(r, 1, made_or(new_weights, args[5]));
+        return r;
+    });
+}
+
+// grads (a list), max_norm (None: the norm alone), eps, out (a list or None),
+// workspace, stream -> norm
+PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        require(n == 6 && PyList_Check(args[0]) && (args[3] == Py_None || PyList_Check(args[3])));
+        const Py_ssize_t count = PyList_GET_SIZE(args[0]);
+        const bool apart = args[3] != Py_None;
+        require(count > 0 && (!apart || PyList_GET_SIZE(args[3]) == count));
+        const OnStream stream(args[5]);
+        std::vector<tiles_grad_tensor> tensors(static_cast<size_t>(count));
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const at::Tensor& g = tensor(PyList_GET_ITEM(args[0], i));
+            require(g.is_non_overlapping_and_dense());
+            tiles_grad_tensor& t = tensors[static_cast<size_t>(i)];
+            t = {g.data_ptr(), nullptr, g.numel(), code_of(g.scalar_type()), 0};
+            if (apart) {
+                const at::Tensor& o = tensor(PyList_GET_ITEM(args[3], i));
+                require(o.scalar_type() == g.scalar_type() && o.sizes() == g.sizes() &&
+                        o.strides() == g.strides());
+                t.out = o.data_ptr();
+            }
+        }
+        const at::Tensor& like = tensor(PyList_GET_ITEM(args[0], 0));
+        const Scratch ws(args[4], calls.grad_norm_workspace_bytes(count), like);
+        at::Tensor norm = empty(like, {}, {}, at::ScalarType::Float);
+        float* at = static_cast<float*>(norm.data_ptr());
+        if (args[1] == Py_None) {
+            run([&] { return calls.grad_norm(tensors.data(), count, at, ws.given.at, ws.given.bytes, stream.at); });
+        } else {
+            const float max_norm = number(args[1]), eps = number(args[2]);
+            run([&] {
+                return calls.clip_grads(tensors.data(), count, max_norm, eps, at, ws.given.at,
+                                        ws.given.bytes, stream.at);
+            });
+        }
+        return THPVariable_Wrap(std::move(norm));
+    });
+}
+
+// The addresses, in the order of Calls.
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
+    constexpr int kCalls = sizeof(calls) / sizeof(void*);
+    if (n != kCalls) {
+        PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kCalls);
         return nullptr;
     }
-    void* at[5];
-    for (int i = 0; i < 5; ++i) {
+    void* at[kCalls];
+    for (int i = 0; i < kCalls; ++i) {
         at[i] = PyLong_AsVoidPtr(args[i]);
         if (PyErr_Occurred()) return nullptr;
     }
-    static_assert(sizeof(calls) == sizeof(at), "one address a call");
     std::memcpy(&calls, at, sizeof(at));
     Py_RETURN_NONE;
 }
@@ -490,7 +893,10 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define TILES_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {TILES_METHOD(bind), TILES_METHOD(rmsnorm), TILES_METHOD(rmsnorm_grad),
                          TILES_METHOD(product_fp8), TILES_METHOD(grouped_gemm),
-                         TILES_METHOD(grouped_wgrad), {nullptr, nullptr, 0, nullptr}};
+                         TILES_METHOD(grouped_wgrad), TILES_METHOD(layernorm),
+                         TILES_METHOD(layernorm_grad), TILES_METHOD(expert_sort),
+                         TILES_METHOD(expert_dispatch), TILES_METHOD(expert_combine),
+                         TILES_METHOD(expert_combine_grad), TILES_METHOD(clip_grads), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
