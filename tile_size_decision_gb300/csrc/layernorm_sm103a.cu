@@ -1,16 +1,135 @@
 // Layer norm with the residual's addition (16-bit, fp32 or scaled 8-bit
 // output) and its gradients.
 //
-// As the root-mean-square norm, both read and write every element once and
-// compute a few operations per byte: DRAM bounds them.  The row's sums are
-// taken twice from registers: first a mean m in fp32, then the sums of d = h - m
-// and of d^2, which give what m was off by, c = mean(d), and the variance
-// mean(d^2) - c^2.  So a row whose mean is far larger than its spread loses
-// nothing (with c left out the error of m, 2^-24 |m|, would shift all of y).
+// As the root-mean-square norm, both read and write every element once: DRAM
+// bounds them, if the instructions do not, of which there are more (the mean
+// comes first, then what is left after it).  So the arithmetic is done on pairs
+// of fp32, and several sums of a row go through its lanes together.
+//
+// A row's elements are taken about a mean m in fp32, d = h - m; the sums of d
+// and d^2 give what m was off by, off = mean(d), and var = mean(d^2) - off^2: a
+// row whose mean is far larger than its spread loses nothing (without off the
+// error of m, up to 2^-20 |m|, would shift all of y).
 #include "row_ops.cuh"
 
 namespace tiles {
 namespace {
+
+// Eight columns as four pairs.
+struct Eight {
+    uint64_t p[4];
+
+    __device__ __forceinline__ void fill(float v) {
+        const uint64_t q = ptx::pair(v, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = q;
+    }
+    __device__ __forceinline__ void from(const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = ptx::pair(v[2 * i], v[2 * i + 1]);
+    }
+    __device__ __forceinline__ void to(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = ptx::unpair(p[i]);
+            v[2 * i] = t.x;
+            v[2 * i + 1] = t.y;
+        }
+    }
+    // The sum of all eight.
+    __device__ __forceinline__ float sum() const {
+        const float2 t = ptx::unpair(ptx::add2(ptx::add2(p[0], p[1]), ptx::add2(p[2], p[3])));
+        return t.x + t.y;
+    }
+};
+
+// Where the columns are all inside the row (VEC: eight together), v; else zeros
+// for those past its end.
+template <bool VEC>
+__device__ __forceinline__ void keep(Eight& v, int c, int cols) {
+    if constexpr (VEC) {
+        if (c >= cols) v.fill(0.0f);
+    } else {
+        if ((c | 127) < cols) return;
+        float t[8];
+        v.to(t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = column<false>(c, i) < cols ? t[i] : 0.0f;
+        v.from(t);
+    }
+}
+
+// Lane l's share of the warp's sums of s[0 .. N): that of s[l % N].  Each exchange
+// halves what a lane is responsible for; of the N values the last N - USED
+// are zeros.
+template <int N, int USED>
+__device__ __forceinline__ float fold(float (&s)[N]) {
+    const int lane = threadIdx.x & 31;
+    int live = USED;
+#pragma unroll
+    for (int bit = 1; bit < N; bit <<= 1) {
+#pragma unroll
+        for (int i = 0; i < N / 2 / bit; ++i)
+            if (2 * i < live) {
+                const float lo = s[2 * i], hi = 2 * i + 1 < live ? s[2 * i + 1] : 0.0f;
+                s[i] = (lane & bit ? hi : lo) + __shfl_xor_sync(0xffffffffu, lane & bit ? lo : hi, bit);
+            }
+        live = (live + 1) / 2;
+    }
+    float x = s[0];
+#pragma unroll
+    for (int d = N; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// Sums of USED values over the threads of one row (blockDim.x of them, whole
+// warps, at most W); every thread gets them.  N is the power of two over USED:
+// five values take 8 shuffles in a warp (not 25) and 7 among the warps.  `slot`
+// holds W N floats; between two uses of the same the row's threads meet at a
+// barrier.  RING: the row's own barrier, and slots that hold zeros where the row
+// has fewer warps (kernels of one row a block would pay for that each time).
+template <int N, int USED, int W, bool RING>
+__device__ __forceinline__ void row_sums(float (&s)[N], float* slot) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    float x = fold<N, USED>(s);
+    if (blockDim.x > 32) {
+        const int values = (blockDim.x >> 5) * N;
+        if (lane < N) slot[(threadIdx.x >> 5) * N + lane] = x;
+        if constexpr (RING) ptx::named_barrier(1 + threadIdx.y, blockDim.x);
+        else __syncthreads();
+        x = lane < (RING ? W * N : values) ? slot[lane] : 0.0f;
+#pragma unroll
+        for (int i = 32; i < W * N; i *= 2)
+            if (values > i)
+#pragma unroll
+                for (int k = i; k < 2 * i; k += 32)
+                    x += RING || lane + k < values ? slot[lane + k] : 0.0f;
+#pragma unroll
+        for (int d = 16; d >= N; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+    }
+    if constexpr (N == 1) {
+        s[0] = x;
+    } else {
+#pragma unroll
+        for (int j = 0; j < USED; ++j) s[j] = __shfl_sync(kAll, x, j);
+    }
+}
+
+// Zeros in the slots, by all threads of the block, before their first use (which
+// comes after a barrier).
+__device__ __forceinline__ void clear_slots(float* slots, int n) {
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < n; i += blockDim.x * blockDim.y)
+        slots[i] = 0.0f;
+    __syncthreads();
+}
+
+// (var + eps)^(-1/2) from the mean of d^2 and of d.  The variance is no less
+// than 0, whatever the two roundings leave; a NaN stays one.
+__device__ __forceinline__ float inverse_root(float square, float off, float eps) {
+    const float var = square - off * off;
+    return rsqrtf((var < 0.0f ? 0.0f : var) + eps);
+}
 
 struct LayerArgs {
     int64_t rows, cols;
@@ -26,11 +145,46 @@ struct LayerArgs {
     int32_t weight_dtype;
 };
 
-// (var + eps)^(-1/2) from the mean of d^2 and of d.  The variance is no less
-// than 0, whatever the two roundings leave; a NaN stays one.
-__device__ __forceinline__ float inverse_root(float square, float off, float eps) {
-    const float var = square - off * off;
-    return rsqrtf((var < 0.0f ? 0.0f : var) + eps);
+// d times rstd, times w plus b, to y: `shift` is -off rstd.  All lanes of the
+// 16 that hold a block of 128 columns come here together.
+template <typename T, bool VEC, bool FP8>
+__device__ __forceinline__ void emit(const LayerArgs& a, int64_t row, int c, int cols, const Eight& d,
+                                     uint64_t rstd, uint64_t shift, const Eight& w, const Eight& b) {
+    Eight y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y.p[i] = ptx::fma2(ptx::fma2(d.p[i], rstd, shift), w.p[i], b.p[i]);
+    if constexpr (FP8) {
+        // What lies past the row's end must not reach the short last block's
+        // scale (it may be a NaN by now).
+        keep<VEC>(y, c, cols);
+        float v[8];
+        y.to(v);
+        const float s = block_scale(block_amax(amax8(v))), inv = reciprocal(s);
+        const uint64_t inv2 = ptx::pair(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.p[i] = ptx::mul2(y.p[i], inv2);
+        y.to(v);
+        store8_e4m3<VEC>(static_cast<uint8_t*>(a.y) + row * a.ldy, c, cols, v);
+        if ((threadIdx.x & 15) == 0 && c < cols)
+            a.scales[row * a.scale_row + c / kBlock * a.scale_block] = s;
+    } else {
+        float v[8];
+        y.to(v);
+        store8<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, cols, v);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_affine(const LayerArgs& a, int c, int cols, Eight& w, Eight& b) {
+    float t[8];
+    load8_any<VEC>(a.weight, a.weight_dtype, c, cols, t);
+    w.from(t);
+    b.fill(0.0f);
+    if (a.bias) {
+        load8_any<VEC>(a.bias, a.weight_dtype, c, cols, t);
+        b.from(t);
+    }
 }
 
 // One row per blockDim.x threads, blockDim.y rows per block; the layout of
@@ -38,9 +192,9 @@ __device__ __forceinline__ float inverse_root(float square, float off, float eps
 // any length: it reads h again from x and the residual for the variance and
 // for the output.
 template <typename T, int VPT, bool VEC, bool FP8>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, VPT == 1 && VEC ? 2 : 1)
     layernorm_kernel(const LayerArgs a) {
-    __shared__ float slots[64 + 128];
+    __shared__ float slots[32 + 64];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
@@ -50,110 +204,244 @@ __global__ void __launch_bounds__(kMaxThreads)
     T* h = a.h ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
     const int cols = static_cast<int>(a.cols);
     const float inv_n = 1.0f / static_cast<float>(cols);
-    auto load_h = [&](int c, float (&v)[8]) {
-        load8<T, VEC>(x, c, cols, v);
+    auto load_h = [&](int c, Eight& v) {
+        float t[8];
+        load8<T, VEC>(x, c, cols, t);
+        v.from(t);
         if (r) {
-            float q[8];
-            load8<T, VEC>(r, c, cols, q);
+            load8<T, VEC>(r, c, cols, t);
+            Eight q;
+            q.from(t);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += q[i];
+            for (int i = 0; i < 4; ++i) v.p[i] = ptx::add2(v.p[i], q.p[i]);
         }
     };
-    // v - mean; columns past the row's end stay zero.
-    auto centre = [&](int c, float (&v)[8], float mean) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = column<VEC>(c, i) < cols ? v[i] - mean : 0.0f;
+    auto store_h = [&](int c, const Eight& v) {
+        if (!h) return;
+        float t[8];
+        v.to(t);
+        store8<T, VEC>(h, c, cols, t);
     };
-    auto emit = [&](int c, const float (&v)[8], float rstd) {
-        float w[8], y[8];
-        load8_any<VEC>(a.weight, a.weight_dtype, c, cols, w);
+    // d = v - mean (zeros past the row's end); its sums are added to sq.
+    float sum[1] = {0.0f}, sq[2] = {0.0f, 0.0f};
+    auto centre = [&](int c, Eight& v, float mean) {
+        const uint64_t less = ptx::pair(-mean, -mean);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = v[i] * rstd * w[i];
-        if (a.bias) {
-            load8_any<VEC>(a.bias, a.weight_dtype, c, cols, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += w[i];
-        }
-        if constexpr (FP8) {
-            // Zeros past the row's end times rstd may be NaN; they must not
-            // reach the short last block's scale.
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (column<VEC>(c, i) >= cols) y[i] = 0.0f;
-            const float s = block_scale(block_amax(amax8(y))), inv = reciprocal(s);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= inv;
-            store8_e4m3<VEC>(static_cast<uint8_t*>(a.y) + row * a.ldy, c, cols, y);
-            if ((threadIdx.x & 15) == 0 && c < cols)
-                a.scales[row * a.scale_row + c / kBlock * a.scale_block] = s;
-        } else {
-            store8<T, VEC>(static_cast<T*>(a.y) + row * a.ldy, c, cols, y);
-        }
+        for (int i = 0; i < 4; ++i) v.p[i] = ptx::add2(v.p[i], less);
+        keep<VEC>(v, c, cols);
     };
-    const int step = blockDim.x * 8;
-    float sum[1] = {0.0f}, sq[2] = {0.0f, 0.0f};   // sum h; sums of d, d^2
+    auto squares = [&](const Eight& v) {
+        Eight q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q.p[i] = ptx::mul2(v.p[i], v.p[i]);
+        sq[0] += v.sum();
+        sq[1] += q.sum();
+    };
+    const int step = blockDim.x * 8, tid = threadIdx.x;
+    Eight w, b;
     if constexpr (VPT > 0) {
-        float v[VPT][8];
+        Eight v[VPT];
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) load_h(j * step + threadIdx.x * 8, v[j]);
+        for (int j = 0; j < VPT; ++j) load_h(j * step + tid * 8, v[j]);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (h) store8<T, VEC>(h, j * step + threadIdx.x * 8, cols, v[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[0] += v[j][i];
+            store_h(j * step + tid * 8, v[j]);
+            sum[0] += v[j].sum();
         }
-        row_sum(sum, slots, 0);
+        row_sums<1, 1, 32, false>(sum, slots);
         const float mean = sum[0] * inv_n;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            centre(j * step + threadIdx.x * 8, v[j], mean);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sq[0] += v[j][i];
-                sq[1] += v[j][i] * v[j][i];
-            }
+            centre(j * step + tid * 8, v[j], mean);
+            squares(v[j]);
         }
-        row_sum(sq, slots + 64, 0);
+        row_sums<2, 2, 32, false>(sq, slots + 32);
         const float off = sq[0] * inv_n, rstd = inverse_root(sq[1] * inv_n, off, a.eps);
+        const uint64_t rstd2 = ptx::pair(rstd, rstd), shift = ptx::pair(-off * rstd, -off * rstd);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] -= off;
-            emit(j * step + threadIdx.x * 8, v[j], rstd);
+            const int c = j * step + tid * 8;
+            load_affine<VEC>(a, c, cols, w, b);
+            emit<T, VEC, FP8>(a, row, c, cols, v[j], rstd2, shift, w, b);
         }
     } else {
+        Eight v;
         for (int c0 = 0; c0 < cols; c0 += step) {
-            float v[8];
-            load_h(c0 + threadIdx.x * 8, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[0] += v[i];
+            load_h(c0 + tid * 8, v);
+            sum[0] += v.sum();
         }
-        row_sum(sum, slots, 0);
+        row_sums<1, 1, 32, false>(sum, slots);
         const float mean = sum[0] * inv_n;
         for (int c0 = 0; c0 < cols; c0 += step) {
-            const int c = c0 + threadIdx.x * 8;
-            float v[8];
-            load_h(c, v);
-            centre(c, v, mean);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sq[0] += v[i];
-                sq[1] += v[i] * v[i];
-            }
+            load_h(c0 + tid * 8, v);
+            centre(c0 + tid * 8, v, mean);
+            squares(v);
         }
-        row_sum(sq, slots + 64, 0);
+        row_sums<2, 2, 32, false>(sq, slots + 32);
         const float off = sq[0] * inv_n, rstd = inverse_root(sq[1] * inv_n, off, a.eps);
+        const uint64_t rstd2 = ptx::pair(rstd, rstd), shift = ptx::pair(-off * rstd, -off * rstd);
         for (int c0 = 0; c0 < cols; c0 += step) {
-            const int c = c0 + threadIdx.x * 8;
-            float v[8];
+            const int c = c0 + tid * 8;
             load_h(c, v);
             // h may be stored over x or the residual: after its own read.
-            if (h) store8<T, VEC>(h, c, cols, v);
+            store_h(c, v);
             centre(c, v, mean);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] -= off;
-            emit(c, v, rstd);
+            load_affine<VEC>(a, c, cols, w, b);
+            emit<T, VEC, FP8>(a, row, c, cols, v, rstd2, shift, w, b);
         }
+    }
+}
+
+// ---- rows on their way in ---------------------------------------------------------
+//
+// As the root-mean-square norm's ring, for one block of up to kRows threads an
+// SM, blockDim.x of them a row: the pitch of the ring is a constant, the
+// addresses of a thread's rows are kept and advanced, and what lies past a row's
+// end is zeroed once and never copied, so that reads ask nothing.  (These
+// kernels are near their instructions' limit.)
+constexpr int kRows = 512;
+constexpr int kStages = 3;
+
+template <typename T, int N, int VPT>
+struct Ring {
+    static constexpr int PIECES = static_cast<int>(sizeof(T)) / 2;   // 16-byte pieces of a vector
+    static constexpr int STAGE = N * VPT * PIECES * kRows;           // pieces a stage
+    static constexpr size_t BYTES = static_cast<size_t>(kStages) * STAGE * 16;
+
+    uint4* at;
+    bool in[VPT];                              // whether the thread's vector lies in the row
+
+    __device__ __forceinline__ Ring(uint4* smem, int step, int cols) {
+        at = smem + threadIdx.y * blockDim.x + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            in[j] = j * step + static_cast<int>(threadIdx.x) * 8 < cols;
+            if (in[j]) continue;
+            for (int s = 0; s < kStages; ++s)
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p)
+                        at[s * STAGE + ((n * VPT + j) * PIECES + p) * kRows] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    // Start the copies of matrix n's vectors (from its first one) into `stage`.
+    __device__ __forceinline__ void copy(int stage, int n, const T* from, int step) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (in[j])
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p)
+                    ptx::cp_async_16(at + stage * STAGE + ((n * VPT + j) * PIECES + p) * kRows,
+                                     reinterpret_cast<const uint4*>(from + j * step) + p);
+    }
+    __device__ __forceinline__ void read(int stage, int n, int j, Eight& v) const {
+        uint4 q[PIECES];
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) q[p] = at[stage * STAGE + ((n * VPT + j) * PIECES + p) * kRows];
+        float t[8];
+        widen8<T>(q, t);
+        v.from(t);
+    }
+};
+
+// The same with the rows' pieces 16-byte aligned: one block an SM, blockDim.y
+// rows at a time (their threads meet at barriers of their own), the next two on
+// their way in.  The sums of one row go together with the mean of the next, so
+// that a row costs one barrier.  16384 x 4096 bf16 rows with residual 86.2 us,
+// 93% of the measured copy bandwidth (to e4m3 80.2); one row at a time without
+// the ring 110.
+template <typename T, int VPT, bool FP8, bool RES>
+__global__ void __launch_bounds__(kRows)
+    layernorm_ring_kernel(const LayerArgs a) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float slots[8][2][16 * 4];          // rows of several warps: at most 8
+    float(*const mine)[16 * 4] = slots[blockDim.x > 32 ? threadIdx.y : 0];
+    clear_slots(&slots[0][0][0], sizeof(slots) / 4);
+    const int step = blockDim.x * 8, tid = threadIdx.x, cols = static_cast<int>(a.cols);
+    Ring<T, RES ? 2 : 1, VPT> ring(ring_smem, step, cols);
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y, ahead = row;
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx + tid * 8;
+    const T* r = RES ? static_cast<const T*>(a.residual) + row * a.ldr + tid * 8 : nullptr;
+    T* h = a.h ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
+    auto fetch = [&](int stage) {
+        if (ahead < a.rows) {
+            ring.copy(stage, 0, x, step);
+            if constexpr (RES) ring.copy(stage, 1, r, step);
+        }
+        ptx::cp_async_commit();
+        ahead += stride;
+        x += stride * a.ldx;
+        if constexpr (RES) r += stride * a.ldr;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    Eight w[VPT], b[VPT], v[VPT];
+    float mask[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        load_affine<true>(a, j * step + tid * 8, cols, w[j], b[j]);
+        mask[j] = ring.in[j] ? -1.0f / static_cast<float>(cols) : 0.0f;
+    }
+    const float inv_n = 1.0f / static_cast<float>(cols);
+    // h of a row that has arrived, in v; stored; its sum.
+    auto take = [&](int stage) {
+        Eight all;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            ring.read(stage, 0, j, v[j]);
+            if constexpr (RES) {
+                Eight q;
+                ring.read(stage, 1, j, q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j].p[i] = ptx::add2(v[j].p[i], q.p[i]);
+            }
+            if (h) {
+                float t[8];
+                v[j].to(t);
+                store8<T, true>(h, j * step + tid * 8, cols, t);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) all.p[i] = j ? ptx::add2(all.p[i], v[j].p[i]) : v[j].p[i];
+        }
+        if (h) h += stride * a.ldh;
+        return all.sum();
+    };
+    ptx::cp_async_wait_groups<kStages - 2>();
+    float s[4];
+    s[0] = row < a.rows ? take(0) : 0.0f;
+    row_sums<4, 1, 16, true>(s, mine[1]);
+    float total = s[0];
+    int stage = 0, turn = 0;
+    for (; row < a.rows; row += stride, turn ^= 1) {
+        fetch(stage == 0 ? kStages - 1 : stage - 1);
+        Eight d[VPT], d1, d2;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const uint64_t less = ptx::pair(total * mask[j], total * mask[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                d[j].p[i] = ptx::add2(v[j].p[i], less);
+                d1.p[i] = j ? ptx::add2(d1.p[i], d[j].p[i]) : d[j].p[i];
+                d2.p[i] = j ? ptx::fma2(d[j].p[i], d[j].p[i], d2.p[i]) : ptx::mul2(d[j].p[i], d[j].p[i]);
+            }
+        }
+        s[0] = d1.sum();
+        s[1] = d2.sum();
+        s[2] = 0.0f;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        ptx::cp_async_wait_groups<kStages - 2>();
+        if (row + stride < a.rows) s[2] = take(stage);
+        row_sums<4, 3, 16, true>(s, mine[turn]);
+        total = s[2];
+        const float off = s[0] * inv_n, rstd = inverse_root(s[1] * inv_n, off, a.eps);
+        const uint64_t rstd2 = ptx::pair(rstd, rstd), shift = ptx::pair(-off * rstd, -off * rstd);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            emit<T, true, FP8>(a, row, j * step + tid * 8, cols, d[j], rstd2, shift, w[j], b[j]);
     }
 }
 
@@ -170,6 +458,72 @@ struct LayerGradArgs {
     int32_t weight_dtype;
 };
 
+// What a row's four sums (of d, d^2, g = dy w and g d) make of its gradients:
+//   dx = g rstd - level - (d - off) back,   dweight += dy (d - off) rstd.
+struct RowFactors {
+    uint64_t off, rstd, level, back;           // -off, rstd, -level, -back in pairs
+
+    __device__ __forceinline__ RowFactors(const float* s, float inv_n, float eps) {
+        const float o = s[0] * inv_n, r = inverse_root(s[1] * inv_n, o, eps);
+        const float l = s[2] * inv_n * r, k = (s[3] - o * s[2]) * inv_n * r * r * r;
+        off = ptx::pair(-o, -o);
+        rstd = ptx::pair(r, r);
+        level = ptx::pair(-l, -l);
+        back = ptx::pair(-k, -k);
+    }
+};
+
+// The sums that a vector adds (columns past the row's end hold zeros in d and g).
+__device__ __forceinline__ void grad_sums(const Eight& d, const Eight& g, const Eight& w, float (&s)[4]) {
+    Eight q, e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q.p[i] = ptx::mul2(d.p[i], d.p[i]);
+        e.p[i] = ptx::mul2(g.p[i], w.p[i]);
+    }
+    s[0] += d.sum();
+    s[1] += q.sum();
+    s[2] += e.sum();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q.p[i] = ptx::mul2(e.p[i], d.p[i]);
+    s[3] += q.sum();
+}
+
+// The same, kept in pairs until a thread's last vector: its first one, and the
+// others.
+__device__ __forceinline__ void first_sums(const Eight& d, const Eight& g, const Eight& w, Eight (&s)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[0].p[i] = d.p[i];
+        s[1].p[i] = ptx::mul2(d.p[i], d.p[i]);
+        s[2].p[i] = ptx::mul2(g.p[i], w.p[i]);
+        s[3].p[i] = ptx::mul2(s[2].p[i], d.p[i]);
+    }
+}
+
+__device__ __forceinline__ void grad_sums(const Eight& d, const Eight& g, const Eight& w, Eight (&s)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t gw = ptx::mul2(g.p[i], w.p[i]);
+        s[0].p[i] = ptx::add2(s[0].p[i], d.p[i]);
+        s[1].p[i] = ptx::fma2(d.p[i], d.p[i], s[1].p[i]);
+        s[2].p[i] = ptx::add2(s[2].p[i], gw);
+        s[3].p[i] = ptx::fma2(gw, d.p[i], s[3].p[i]);
+    }
+}
+
+// A vector's dx (in o), and its parts of the weight's and the bias's gradient.
+__device__ __forceinline__ void grad_vector(const RowFactors& f, const Eight& d, const Eight& g,
+                                            const Eight& w, Eight& o, Eight& dw, Eight& db) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t e = ptx::add2(d.p[i], f.off), gr = ptx::mul2(g.p[i], f.rstd);
+        db.p[i] = ptx::add2(db.p[i], g.p[i]);
+        dw.p[i] = ptx::fma2(gr, e, dw.p[i]);
+        o.p[i] = ptx::fma2(e, f.back, ptx::fma2(gr, w.p[i], f.level));
+    }
+}
+
 // Each block sweeps rows, gridDim.x * blockDim.y apart; a thread keeps the same
 // columns throughout, so its parts of the weight's and the bias's gradient
 // stay in registers until the block's one write to `partials` (rows short
@@ -178,9 +532,9 @@ struct LayerGradArgs {
 // (a vector a thread): each span then reads the whole row for the sums and
 // writes its own columns.
 template <typename T, bool VEC, bool SPANS>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, 2)
     layernorm_grad_kernel(const LayerGradArgs a) {
-    __shared__ float slots[64 + 256];
+    __shared__ float slots[16 + 64];
     extern __shared__ float side[];                // blockDim.y > 1: the other warps' parts
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
@@ -189,102 +543,258 @@ __global__ void __launch_bounds__(512)
     const int first = static_cast<int>(blockIdx.y) * step;
     const int c = first + threadIdx.x * 8;
     const float inv_n = 1.0f / static_cast<float>(a.cols);
-    float dw[8], db[8];
+    Eight dw, db;
+    dw.fill(0.0f);
+    db.fill(0.0f);
+    auto load = [&](const T* p, int at, Eight& v) {
+        float t[8];
+        load8<T, VEC>(p, at, cols, t);
+        v.from(t);
+    };
+    auto load_weight = [&](int at, Eight& v) {
+        float t[8];
+        load8_any<VEC>(a.weight, a.weight_dtype, at, cols, t);
+        v.from(t);
+    };
+    auto centre = [&](int at, Eight& v, float mean) {
+        const uint64_t less = ptx::pair(-mean, -mean);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.0f;
+        for (int i = 0; i < 4; ++i) v.p[i] = ptx::add2(v.p[i], less);
+        keep<VEC>(v, at, cols);
+    };
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y; row < a.rows;
          row += static_cast<int64_t>(gridDim.x) * blockDim.y) {
         const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
         const T* h = static_cast<const T*>(a.h) + row * a.ldh;
         const T* dh = a.dh ? static_cast<const T*>(a.dh) + row * a.lddh : nullptr;
-        float g[8], v[8], w[8], past[8];
-        load8<T, VEC>(dy, c, cols, g);
-        load8<T, VEC>(h, c, cols, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) past[i] = 0.0f;
-        if (VEC && dh) load8<T, VEC>(dh, c, cols, past);
-        load8_any<VEC>(a.weight, a.weight_dtype, c, cols, w);
-        float m[1] = {0.0f};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m[0] += v[i];
+        Eight g, d, w, past;
+        load(dy, c, g);
+        load(h, c, d);
+        // dh with the others where it is one load, after the sums where it is eight.
+        if (VEC && dh) load(dh, c, past);
+        load_weight(c, w);
+        float m[1] = {d.sum()}, s[4];
         if constexpr (SPANS) {
             for (int c0 = 0; c0 < cols; c0 += step) {
                 if (c0 == first) continue;
-                float q[8];
-                load8<T, VEC>(h, c0 + threadIdx.x * 8, cols, q);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m[0] += q[i];
+                Eight q;
+                load(h, c0 + threadIdx.x * 8, q);
+                m[0] += q.sum();
             }
         }
-        row_sum(m, slots, 0);
+        row_sums<1, 1, 16, false>(m, slots);
         const float mean = m[0] * inv_n;
-        // Sums of d, d^2, g = dy w and g d; columns past the row's end have g = 0
-        // and are kept out of d.
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        centre(c, d, mean);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = column<VEC>(c, i) < cols ? v[i] - mean : 0.0f;
-            s[0] += v[i];
-            s[1] += v[i] * v[i];
-            s[2] += g[i] * w[i];
-            s[3] += g[i] * w[i] * v[i];
-        }
+        for (int j = 0; j < 4; ++j) s[j] = 0.0f;
+        grad_sums(d, g, w, s);
         if constexpr (SPANS) {
             for (int c0 = 0; c0 < cols; c0 += step) {
                 if (c0 == first) continue;
                 const int at = c0 + threadIdx.x * 8;
-                float p[8], q[8], u[8];
-                load8<T, VEC>(dy, at, cols, p);
-                load8<T, VEC>(h, at, cols, q);
-                load8_any<VEC>(a.weight, a.weight_dtype, at, cols, u);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = column<VEC>(at, i) < cols ? q[i] - mean : 0.0f;
-                    s[0] += d;
-                    s[1] += d * d;
-                    s[2] += p[i] * u[i];
-                    s[3] += p[i] * u[i] * d;
-                }
+                Eight p, q, u;
+                load(dy, at, p);
+                load(h, at, q);
+                load_weight(at, u);
+                centre(at, q, mean);
+                grad_sums(q, p, u, s);
             }
         }
-        row_sum(s, slots + 64, 0);
-        const float off = s[0] * inv_n, rstd = inverse_root(s[1] * inv_n, off, a.eps);
-        const float level = s[2] * inv_n * rstd;
-        const float back = (s[3] - off * s[2]) * inv_n * rstd * rstd * rstd;
-        if (!VEC && dh) load8<T, VEC>(dh, c, cols, past);
-        float o[8];
+        row_sums<4, 4, 16, false>(s, slots + 16);
+        const RowFactors f(s, inv_n, a.eps);
+        load_weight(c, w);
+        if (!VEC && dh) load(dh, c, past);
+        Eight o;
+        grad_vector(f, d, g, w, o, dw, db);
+        if (dh)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] -= off;
-            o[i] = g[i] * w[i] * rstd - level - v[i] * back + past[i];
-            dw[i] += g[i] * v[i] * rstd;
-            db[i] += g[i];
-        }
-        store8<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx, c, cols, o);
+            for (int i = 0; i < 4; ++i) o.p[i] = ptx::add2(o.p[i], past.p[i]);
+        float t[8];
+        o.to(t);
+        store8<T, VEC>(static_cast<T*>(a.dx) + row * a.lddx, c, cols, t);
     }
+    float tw[8], tb[8];
+    dw.to(tw);
+    db.to(tb);
     if (blockDim.y > 1) {                          // then blockDim.x == 32: one warp a row
         if (threadIdx.y > 0)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                side[(threadIdx.y - 1) * 512 + i * 32 + threadIdx.x] = dw[i];
-                side[(threadIdx.y - 1) * 512 + 256 + i * 32 + threadIdx.x] = db[i];
+                side[(threadIdx.y - 1) * 512 + i * 32 + threadIdx.x] = tw[i];
+                side[(threadIdx.y - 1) * 512 + 256 + i * 32 + threadIdx.x] = tb[i];
             }
         __syncthreads();
         if (threadIdx.y > 0) return;
         for (int y = 0; y < static_cast<int>(blockDim.y) - 1; ++y)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                dw[i] += side[y * 512 + i * 32 + threadIdx.x];
-                db[i] += side[y * 512 + 256 + i * 32 + threadIdx.x];
+                tw[i] += side[y * 512 + i * 32 + threadIdx.x];
+                tb[i] += side[y * 512 + 256 + i * 32 + threadIdx.x];
             }
     }
     float* out = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (column<VEC>(c, i) < cols) {
-            out[column<VEC>(c, i)] = dw[i];
-            out[a.cols + column<VEC>(c, i)] = db[i];
+            out[column<VEC>(c, i)] = tw[i];
+            out[a.cols + column<VEC>(c, i)] = tb[i];
         }
+}
+
+// The same with the rows' pieces 16-byte aligned and the whole row among
+// blockDim.x threads (gridDim.y == 1): one block an SM, blockDim.y rows at a
+// time (their threads meet at barriers of their own, and add their parts of the
+// gradients in the end), the next two on their way in.  The sums of one row go
+// together with the mean of the next, so that a row costs one barrier.
+// 8192 x 4096 bf16 rows with dh 57 us, the reduction's launch included: 70% of
+// the measured copy bandwidth.  The instructions bound it (a vector a thread and
+// twice the threads: 77.6 us; single fp32 additions instead of pairs: 60.6).
+template <typename T, int VPT>
+__global__ void __launch_bounds__(kRows)
+    layernorm_grad_ring_kernel(const LayerGradArgs a) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float slots[8][2][16 * 8];          // rows of several warps: at most 8
+    float(*const mine)[16 * 8] = slots[blockDim.x > 32 ? threadIdx.y : 0];
+    clear_slots(&slots[0][0][0], sizeof(slots) / 4);
+    const int step = blockDim.x * 8, tid = threadIdx.x, cols = static_cast<int>(a.cols);
+    Ring<T, 3, VPT> ring(ring_smem, step, cols);
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y, ahead = row;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy + tid * 8;
+    const T* h = static_cast<const T*>(a.h) + row * a.ldh + tid * 8;
+    const T* dh = a.dh ? static_cast<const T*>(a.dh) + row * a.lddh + tid * 8 : nullptr;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+    auto fetch = [&](int stage) {
+        if (ahead < a.rows) {
+            ring.copy(stage, 0, dy, step);
+            ring.copy(stage, 1, h, step);
+            if (dh) ring.copy(stage, 2, dh, step);
+        }
+        ptx::cp_async_commit();
+        ahead += stride;
+        dy += stride * a.lddy;
+        h += stride * a.ldh;
+        if (dh) dh += stride * a.lddh;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    Eight dw[VPT], db[VPT], w[VPT];
+    float mask[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        float t[8];
+        load8_any<true>(a.weight, a.weight_dtype, j * step + tid * 8, cols, t);
+        w[j].from(t);
+        dw[j].fill(0.0f);
+        db[j].fill(0.0f);
+        mask[j] = ring.in[j] ? -1.0f / static_cast<float>(cols) : 0.0f;
+    }
+    const float inv_n = 1.0f / static_cast<float>(cols);
+    auto sum_of = [&](int stage) {
+        Eight all, v;
+        ring.read(stage, 1, 0, all);
+#pragma unroll
+        for (int j = 1; j < VPT; ++j) {
+            ring.read(stage, 1, j, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) all.p[i] = ptx::add2(all.p[i], v.p[i]);
+        }
+        return all.sum();
+    };
+    ptx::cp_async_wait_groups<kStages - 2>();
+    float s[8];
+    s[0] = row < a.rows ? sum_of(0) : 0.0f;
+    row_sums<8, 1, 16, true>(s, mine[1]);
+    float total = s[0];
+    int stage = 0, turn = 0;
+    for (; row < a.rows; row += stride, turn ^= 1) {
+        fetch(stage == 0 ? kStages - 1 : stage - 1);
+        Eight d[VPT], g[VPT];
+        {
+            Eight sums[4];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const uint64_t less = ptx::pair(total * mask[j], total * mask[j]);
+                ring.read(stage, 1, j, d[j]);
+                ring.read(stage, 0, j, g[j]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[j].p[i] = ptx::add2(d[j].p[i], less);
+                if (j == 0) first_sums(d[j], g[j], w[j], sums);
+                else grad_sums(d[j], g[j], w[j], sums);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = sums[j].sum();
+        }
+        const int next = stage + 1 == kStages ? 0 : stage + 1;
+        ptx::cp_async_wait_groups<kStages - 2>();
+        s[4] = row + stride < a.rows ? sum_of(next) : 0.0f;
+        row_sums<8, 5, 16, true>(s, mine[turn]);
+        total = s[4];
+        const RowFactors f(s, inv_n, a.eps);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            Eight o;
+            float t[8];
+            grad_vector(f, d[j], g[j], w[j], o, dw[j], db[j]);
+            if (a.dh) {
+                Eight q;
+                ring.read(stage, 2, j, q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o.p[i] = ptx::add2(o.p[i], q.p[i]);
+            }
+            o.to(t);
+            store8<T, true>(dx, j * step + tid * 8, cols, t);
+        }
+        dx += stride * a.lddx;
+        stage = next;
+    }
+    float tw[VPT][8], tb[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        dw[j].to(tw[j]);
+        db[j].to(tb[j]);
+    }
+    if (blockDim.y > 1) {
+        // The ring's memory takes the other rows' parts (it holds more).
+        float* side = reinterpret_cast<float*>(ring_smem);
+        const int pitch = blockDim.x, part = VPT * 16 * pitch;
+        __syncthreads();
+        if (threadIdx.y > 0)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float* at = side + (threadIdx.y - 1) * part + (j * 8 + i) * 2 * pitch + tid;
+                    at[0] = tw[j][i];
+                    at[pitch] = tb[j][i];
+                }
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+        for (int y = 0; y < static_cast<int>(blockDim.y) - 1; ++y)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float* at = side + y * part + (j * 8 + i) * 2 * pitch + tid;
+                    tw[j][i] += at[0];
+                    tb[j][i] += at[pitch];
+                }
+    }
+    float* out = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = j * step + tid * 8;
+        if (c < cols)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                *reinterpret_cast<float4*>(out + c + i) =
+                    make_float4(tw[j][i], tw[j][i + 1], tw[j][i + 2], tw[j][i + 3]);
+                *reinterpret_cast<float4*>(out + a.cols + c + i) =
+                    make_float4(tb[j][i], tb[j][i + 1], tb[j][i + 2], tb[j][i + 3]);
+            }
+    }
 }
 
 template <typename T, bool VEC, bool FP8>
@@ -308,15 +818,57 @@ int launch_layer(const LayerArgs& a, cudaStream_t st) {
     }
 }
 
+constexpr int kLayerVpt = 2;
+
+// Rows at a time of a block with the ring, and blocks: one an SM.
+struct RingGeometry { int threads, per_block, blocks; };
+
+RingGeometry ring_geometry(int64_t rows, int64_t cols, int sms, int vpt) {
+    RingGeometry g;
+    g.threads = static_cast<int>((cols + 32 * 8 * vpt - 1) / (32 * 8 * vpt) * 32);
+    g.per_block = std::max(1, kRows / g.threads);
+    g.blocks = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>((rows + g.per_block - 1) / g.per_block, sms)));
+    return g;
+}
+
+template <typename T, bool FP8, bool RES>
+int launch_layer_ring(const LayerArgs& a, const RingGeometry& g, cudaStream_t st) {
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(layernorm_ring_kernel<T, kLayerVpt, FP8, RES>, kRingBytesMost, &opted);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    const size_t smem = std::max(Ring<T, RES ? 2 : 1, kLayerVpt>::BYTES, exact_smem(1));
+    return launch(layernorm_ring_kernel<T, kLayerVpt, FP8, RES>, dim3(g.blocks),
+                  dim3(g.threads, g.per_block), smem, st, a);
+}
+
 template <typename T>
-int launch_layer_any(const LayerArgs& a, bool vec, bool fp8, cudaStream_t st) {
+int launch_layer_any(const LayerArgs& a, bool vec, bool fp8, int sms, cudaStream_t st) {
+    if constexpr (sizeof(T) == 2) {
+        const RingGeometry g = ring_geometry(a.rows, a.cols, sms, kLayerVpt);
+        // The ring pays where a row is more than a warp's vectors (16384 x 512
+        // with residual 14.6 us against 18.9 without it, 16384 x 256 9.1
+        // against 8.5), 16-bit (fp32: below), and where every row of a block
+        // has a successor (2000 x 600: 5.8 against 4.8; 600 x 4096 6.9 against 7.8).
+        if (vec && a.cols > 256 && g.threads <= kRows &&
+            a.rows >= 2 * static_cast<int64_t>(g.per_block) * sms) {
+            if (a.residual)
+                return fp8 ? launch_layer_ring<T, true, true>(a, g, st)
+                           : launch_layer_ring<T, false, true>(a, g, st);
+            return fp8 ? launch_layer_ring<T, true, false>(a, g, st)
+                       : launch_layer_ring<T, false, false>(a, g, st);
+        }
+    }
     if (vec) return fp8 ? launch_layer<T, true, true>(a, st) : launch_layer<T, true, false>(a, st);
     return fp8 ? launch_layer<T, false, true>(a, st) : launch_layer<T, false, false>(a, st);
 }
 
+// Vectors a thread in the ring: of fp32 one, whose two pieces fill as much of it.
+constexpr int grad_vpt(int elem_bytes) { return elem_bytes == 2 ? 2 : 1; }
+
 struct LayerGradGeometry { int threads, per_block, blocks, spans; };
 
-// The blocks that sweep the rows, each of which writes one partial.
+// Without the ring: as many blocks as 1024 threads an SM allow.
 LayerGradGeometry layer_grad_geometry(int64_t rows, int64_t cols, int sms) {
     LayerGradGeometry g;
     const int64_t vectors = (cols + 7) / 8;
@@ -330,13 +882,28 @@ LayerGradGeometry layer_grad_geometry(int64_t rows, int64_t cols, int sms) {
     return g;
 }
 
+// The 256-byte header and the partials of whichever form runs.
 size_t layer_grad_bytes(int64_t rows, int64_t cols, int sms) {
-    return kConvMinWorkspaceBytes + static_cast<size_t>(layer_grad_geometry(rows, cols, sms).blocks) *
-                                        static_cast<size_t>(cols) * 8;
+    const int blocks = std::max(layer_grad_geometry(rows, cols, sms).blocks,
+                                static_cast<int>(std::min<int64_t>(rows, sms)));
+    return kConvMinWorkspaceBytes + static_cast<size_t>(std::max(1, blocks)) * static_cast<size_t>(cols) * 8;
 }
 
 template <typename T>
 int launch_layer_grad(const LayerGradArgs& a, bool vec, int sms, int* parts, cudaStream_t st) {
+    constexpr int VPT = grad_vpt(sizeof(T));
+    // fp32 rows fill the ring with half the threads' work: only while there are
+    // few (300 x 4096: 14.3 us against 21.1 without it, 1500 x 4096 35.8 against
+    // 37.5, 8192 x 4096 148 against 117).
+    if (vec && a.cols <= kRows * 8 * VPT && (sizeof(T) == 2 || a.rows <= 10 * sms)) {
+        const RingGeometry g = ring_geometry(a.rows, a.cols, sms, VPT);
+        static std::atomic<uint64_t> opted{0};
+        const cudaError_t e = opt_in_smem(layernorm_grad_ring_kernel<T, VPT>, kRingBytesMost, &opted);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        *parts = g.blocks;
+        return launch(layernorm_grad_ring_kernel<T, VPT>, dim3(*parts), dim3(g.threads, g.per_block),
+                      std::max(Ring<T, 3, VPT>::BYTES, exact_smem(1)), st, a);
+    }
     const LayerGradGeometry g = layer_grad_geometry(a.rows, a.cols, sms);
     *parts = g.blocks;
     const dim3 grid(g.blocks, g.spans), block(g.threads, g.per_block);
@@ -383,10 +950,12 @@ int tiles_layernorm(const tiles_layernorm_desc* d, void* stream) {
                      whole16(d->weight, 0, 1) && whole16(d->bias, 0, 1) &&
                      (fp8 ? whole8(d->y, d->ldy) : whole16(d->y, d->ldy, eb));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    if ((s = current_sm_count(&sms)) != TILES_OK) return s;
     int e;
-    if (d->dtype == TILES_BF16) e = launch_layer_any<__nv_bfloat16>(a, vec, fp8, st);
-    else if (d->dtype == TILES_F16) e = launch_layer_any<__half>(a, vec, fp8, st);
-    else e = launch_layer_any<float>(a, vec, fp8, st);
+    if (d->dtype == TILES_BF16) e = launch_layer_any<__nv_bfloat16>(a, vec, fp8, sms, st);
+    else if (d->dtype == TILES_F16) e = launch_layer_any<__half>(a, vec, fp8, sms, st);
+    else e = launch_layer_any<float>(a, vec, fp8, sms, st);
     return launch_status(e, "layer norm");
 }
 

@@ -1,7 +1,7 @@
 // Inline-PTX building blocks of the norm and product operators, beyond those
 // of the GEMM: cluster launch control, distributed shared memory, register
-// budgets, the 8-bit MMA, further tensor-memory loads, and asynchronous copies
-// in groups.
+// budgets, the 8-bit MMA, further tensor-memory loads, asynchronous copies
+// in groups, and fp32 arithmetic in pairs.
 #pragma once
 
 #include "sm103_ptx.cuh"
@@ -195,6 +195,47 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_groups() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- fp32 in pairs ------------------------------------------------------------
+//
+// One instruction for two additions, products or fused multiply-adds, each
+// rounded as on its own.
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+
+__device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
+    return p;
+}
+
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 }  // namespace ptx
