@@ -831,7 +831,7 @@ int tiles_expert_sort(const tiles_expert_sort_desc* desc, void* workspace, size_
  * blocks.  The gradient of x is tiles_expert_combine of out's, without weights. */
 typedef struct {
     int64_t tokens, k;
-    int64_t rows, cols;               /* of out; rows >= 0, cols >= 1 */
+    int64_t rows, cols;               /* of out; 0 <= rows < 2^31, 1 <= cols <= 2^28 */
     const int32_t* slots;             /* device, tokens x k */
     const void* x;                    /* device, tokens x cols */
     void* out;                        /* device, rows x cols */
@@ -859,7 +859,7 @@ int tiles_expert_dispatch(const tiles_dispatch_desc* desc, void* stream);
  *     another. */
 typedef struct {
     int64_t tokens, k;
-    int64_t rows, cols;               /* of the rows in expert order */
+    int64_t rows, cols;               /* of the rows in expert order; limits as above */
     const int32_t* slots;             /* device, tokens x k */
     const void* weights;              /* device, tokens x k; NULL: ones (not for the gradient) */
     const void* in;                   /* device, rows x cols, in expert order */

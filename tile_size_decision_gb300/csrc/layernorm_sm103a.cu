@@ -59,29 +59,6 @@ __device__ __forceinline__ void keep(Eight& v, int c, int cols) {
     }
 }
 
-// Lane l's share of the warp's sums of s[0 .. N): that of s[l % N].  Each exchange
-// halves what a lane is responsible for; of the N values the last N - USED
-// are zeros.
-template <int N, int USED>
-__device__ __forceinline__ float fold(float (&s)[N]) {
-    const int lane = threadIdx.x & 31;
-    int live = USED;
-#pragma unroll
-    for (int bit = 1; bit < N; bit <<= 1) {
-#pragma unroll
-        for (int i = 0; i < N / 2 / bit; ++i)
-            if (2 * i < live) {
-                const float lo = s[2 * i], hi = 2 * i + 1 < live ? s[2 * i + 1] : 0.0f;
-                s[i] = (lane & bit ? hi : lo) + __shfl_xor_sync(0xffffffffu, lane & bit ? lo : hi, bit);
-            }
-        live = (live + 1) / 2;
-    }
-    float x = s[0];
-#pragma unroll
-    for (int d = N; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
-}
-
 // Sums of USED values over the threads of one row (blockDim.x of them, whole
 // warps, at most W); every thread gets them.  N is the power of two over USED:
 // five values take 8 shuffles in a warp (not 25) and 7 among the warps.  `slot`

@@ -221,66 +221,238 @@ int launch_sort(const SortArgs& a, const SortGeometry& g, cudaStream_t st) {
 }
 
 // ---- rows to the experts --------------------------------------------------------
+//
+// The kernels below that need no sum over a row see all tokens' rows as one run
+// of pieces (16 bytes, or less where rows start anywhere): a thread takes the
+// pieces u, u + stride, ..., whatever a row's length is, and no lane idles at a
+// row's end.
+
+// A thread's place in the run, advanced without a division.
+struct Place {
+    int64_t token;
+    int32_t piece;
+
+    __device__ __forceinline__ Place(int64_t u, int32_t pieces) {
+        if (u >> 32) {
+            token = u / pieces;
+            piece = static_cast<int32_t>(u - token * pieces);
+        } else {
+            const uint32_t v = static_cast<uint32_t>(u), n = static_cast<uint32_t>(pieces);
+            token = v / n;
+            piece = static_cast<int32_t>(v - static_cast<uint32_t>(token) * n);
+        }
+    }
+    __device__ __forceinline__ void advance(int64_t tokens, int32_t by, int32_t pieces) {
+        token += tokens;
+        piece += by;
+        if (piece >= pieces) {
+            piece -= pieces;
+            ++token;
+        }
+    }
+};
+
+constexpr int kChoices = 8;                   // slots in registers at a time
+
+// A token's slots j0 .. j0 + K - 1 as they are, -1 for those past the last.
+// Nothing here looks at them: a loop that asks for the next token's while it
+// works on one would wait for them at once.
+template <int K>
+__device__ __forceinline__ void load_slots(const int32_t* slots, int64_t ld, int64_t token, int j0, int k,
+                                           bool live, int32_t (&row)[K]) {
+    const int32_t* at = slots + token * ld + j0;
+#pragma unroll
+    for (int j = 0; j < K; ++j) row[j] = live && j0 + j < k ? at[j] : -1;
+}
+
+// Whether a slot is one of the rows.
+__device__ __forceinline__ bool names(int32_t row, int64_t rows) {
+    return static_cast<uint32_t>(row) < static_cast<uint32_t>(rows);   // rows are at most 2^31 - 1
+}
+
+// Rows that start anywhere.  What is written is cut into pieces that start on 16
+// bytes of its own row (the first and the last may be part of one); what is read
+// for a piece starts anywhere, and is put together from the two aligned pieces
+// that hold it.
+struct Extent {                               // of a matrix that is read
+    const char* from;
+    const char* to;                           // past its last byte
+};
+
+__device__ __forceinline__ uint4 unaligned16(const char* p, const Extent& e, int elem_bytes) {
+    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+    const char* base = p - s;
+    if (s == 0) return *reinterpret_cast<const uint4*>(p);
+    uint32_t w[8];
+    if (base >= e.from && base + 32 <= e.to) {
+        const uint4 a = *reinterpret_cast<const uint4*>(base), b = *reinterpret_cast<const uint4*>(base + 16);
+        w[0] = a.x;
+        w[1] = a.y;
+        w[2] = a.z;
+        w[3] = a.w;
+        w[4] = b.x;
+        w[5] = b.y;
+        w[6] = b.z;
+        w[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+        const int bits = (s & 3) * 8;
+        return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+    }
+    // At the matrix's ends the aligned pieces may reach out of it.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (elem_bytes == 4) {
+            w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        } else if (elem_bytes == 2) {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 16;
+        } else {
+            const uint8_t* q = reinterpret_cast<const uint8_t*>(p) + 4 * i;
+            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 8 | static_cast<uint32_t>(q[2]) << 16 |
+                   static_cast<uint32_t>(q[3]) << 24;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Piece c of a row of `bytes` (16 at least) that is written at `row`: the bytes
+// [from, to) of the row, which may be none, and the 16 bytes of the row, from
+// `window` on, that hold them.
+struct Cut {
+    int32_t from, to, window;
+
+    __device__ __forceinline__ Cut(const void* row, int32_t bytes, int32_t c) {
+        const int32_t first = c * 16 - static_cast<int32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+        from = max(first, 0);
+        to = min(first + 16, bytes);
+        window = min(from, bytes - 16);
+    }
+    __device__ __forceinline__ bool none() const { return from >= to; }
+    __device__ __forceinline__ bool whole() const { return to - from == 16; }
+    // Whether byte b of the window is one of the piece's.
+    __device__ __forceinline__ bool has(int b) const { return window + b >= from && window + b < to; }
+};
 
 struct DispatchArgs {
     int64_t tokens, rows, ld_slots;
     int32_t k;
+    int32_t pieces;                           // of sizeof(V) bytes, a row
     const int32_t* slots;
     const char* x;
     char* out;
     int64_t pitch_x, pitch_out;               // bytes
-    int64_t pieces;                           // of sizeof(V) bytes, a row
     const float* scales;
     float* out_scales;
     int64_t scale_row, scale_block, out_scale_row, out_scale_block;
     int32_t blocks;                           // scales a row
     uint32_t row_grid;                        // blocks of the launch that move rows; the rest move scales
+    int32_t row_bytes, elem_bytes;
+    int64_t near_tokens, step_tokens;         // what a thread advances by: to its next piece of
+    int32_t near_pieces, step_pieces;         // the block's, and from past the last to the next round
 };
 
-constexpr int kChoices = 8;                   // slots in registers at a time
+constexpr int kMoveThreads = 256;
 
-// A token's row is read once and written to each of its slots.
-template <typename V>
-__global__ void __launch_bounds__(512) dispatch_kernel(const DispatchArgs a) {
+// Scales of 8-bit rows, by the blocks of a launch past those that move rows:
+// neighbours along whichever of rows and blocks lies together in the output.
+__device__ __forceinline__ void dispatch_scales(const DispatchArgs& a) {
+    const int64_t n = a.tokens * a.blocks;
+    const int64_t step = static_cast<int64_t>(gridDim.x - a.row_grid) * kMoveThreads;
+    const bool along = a.out_scale_block == 1;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x - a.row_grid) * kMoveThreads + threadIdx.x; i < n;
+         i += step) {
+        const int64_t t = along ? i / a.blocks : i % a.tokens;
+        const int64_t b = along ? i - t * a.blocks : i / a.tokens;
+        const float s = a.scales[t * a.scale_row + b * a.scale_block];
+        for (int j = 0; j < a.k; ++j) {
+            const int32_t row = a.slots[t * a.ld_slots + j];
+            if (names(row, a.rows)) a.out_scales[row * a.out_scale_row + b * a.out_scale_block] = s;
+        }
+    }
+}
+
+// Rows that start and end on 16 bytes: a token's is read once and written to each
+// of its slots; K: choices at a time, U: pieces of a thread in flight.
+template <int K, int U>
+__global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const DispatchArgs a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    if (blockIdx.x >= a.row_grid) {
-        // Scales: neighbours along whichever of rows and blocks lies together in
-        // the output.
-        const int64_t n = a.tokens * a.blocks;
-        const int64_t step = static_cast<int64_t>(gridDim.x - a.row_grid) * blockDim.x * blockDim.y;
-        for (int64_t i = (static_cast<int64_t>(blockIdx.x - a.row_grid) * blockDim.y + threadIdx.y) *
-                             blockDim.x + threadIdx.x;
-             i < n; i += step) {
-            const bool along = a.out_scale_block == 1;
-            const int64_t t = along ? i / a.blocks : i % a.tokens;
-            const int64_t b = along ? i - t * a.blocks : i / a.tokens;
-            const float s = a.scales[t * a.scale_row + b * a.scale_block];
-            for (int j = 0; j < a.k; ++j) {
-                const int32_t row = a.slots[t * a.ld_slots + j];
-                if (row >= 0 && row < a.rows)
-                    a.out_scales[row * a.out_scale_row + b * a.out_scale_block] = s;
-            }
+    if (blockIdx.x >= a.row_grid) return dispatch_scales(a);
+    // A block takes U kMoveThreads pieces that lie together, then the same
+    // gridDim.x times as far.
+    Place at(static_cast<int64_t>(blockIdx.x) * (U * kMoveThreads) + threadIdx.x, a.pieces);
+    while (at.token < a.tokens) {
+        uint4 v[U];
+        int32_t row[U][K], piece[U];
+        int64_t token[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool live = at.token < a.tokens;
+            token[u] = at.token;
+            piece[u] = at.piece;
+            load_slots<K>(a.slots, a.ld_slots, at.token, 0, a.k, live, row[u]);
+            if (live) v[u] = reinterpret_cast<const uint4*>(a.x + at.token * a.pitch_x)[at.piece];
+            at.advance(a.near_tokens, a.near_pieces, a.pieces);
         }
+        at.advance(a.step_tokens, a.step_pieces, a.pieces);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (names(row[u][j], a.rows))
+                    reinterpret_cast<uint4*>(a.out + row[u][j] * a.pitch_out)[piece[u]] = v[u];
+            if (K == kChoices && token[u] < a.tokens)
+                for (int j = K; j < a.k; ++j) {        // more than eight choices
+                    const int32_t r = a.slots[token[u] * a.ld_slots + j];
+                    if (names(r, a.rows)) reinterpret_cast<uint4*>(a.out + r * a.pitch_out)[piece[u]] = v[u];
+                }
+        }
+    }
+}
+
+// The same for rows that start anywhere: a thread takes one piece of one (token,
+// choice) pair's row (a token's pairs are neighbours: x comes from L1 and L2).
+__global__ void __launch_bounds__(kMoveThreads) dispatch_odd_kernel(const DispatchArgs a) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    if (blockIdx.x >= a.row_grid) return dispatch_scales(a);
+    const Place at(static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x, a.pieces);
+    const int64_t pair = at.token, token = pair / a.k;
+    if (token >= a.tokens) return;
+    const int32_t row = a.slots[token * a.ld_slots + (pair - token * a.k)];
+    if (!names(row, a.rows)) return;
+    char* out = a.out + row * a.pitch_out;
+    const char* x = a.x + token * a.pitch_x;
+    if (a.row_bytes < 16) {                    // (then the row is one thread's)
+        for (int b = at.piece == 0 ? 0 : 16; b < a.row_bytes; ++b) out[b] = x[b];
         return;
     }
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (token >= a.tokens) return;
-    const int32_t* slots = a.slots + token * a.ld_slots;
-    const V* x = reinterpret_cast<const V*>(a.x + token * a.pitch_x);
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-        V* to[kChoices];
+    const Cut c(out, a.row_bytes, at.piece);
+    if (c.none()) return;
+    const Extent e{a.x, a.x + (a.tokens - 1) * a.pitch_x + a.row_bytes};
+    const uint4 v = unaligned16(x + c.window, e, a.elem_bytes);
+    if (c.whole()) {
+        *reinterpret_cast<uint4*>(out + c.window) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    out += c.window;
+    if (a.elem_bytes == 4) {
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j) {
-            const int32_t row = j0 + j < a.k ? slots[j0 + j] : -1;
-            to[j] = row >= 0 && row < a.rows ? reinterpret_cast<V*>(a.out + row * a.pitch_out) : nullptr;
-        }
-        for (int64_t c = threadIdx.x; c < a.pieces; c += blockDim.x) {
-            const V v = x[c];
+        for (int i = 0; i < 4; ++i)
+            if (c.has(4 * i)) reinterpret_cast<uint32_t*>(out)[i] = w[i];
+    } else if (a.elem_bytes == 2) {
 #pragma unroll
-            for (int j = 0; j < kChoices; ++j)
-                if (to[j]) to[j][c] = v;
-        }
+        for (int i = 0; i < 8; ++i)
+            if (c.has(2 * i)) reinterpret_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(w[i / 2] >> 16 * (i & 1));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c.has(i)) out[i] = static_cast<char>(w[i / 4] >> 8 * (i & 3));
     }
 }
 
@@ -301,33 +473,37 @@ struct CombineArgs {
     int64_t ld_out;
     float* dweights;
     int64_t ld_dweights;
+    int64_t step_tokens;                      // what a thread advances by (the sum's)
+    int32_t step_pieces, pieces;
 };
 
-__device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
-    if (dtype == TILES_F32) return static_cast<const float*>(p)[i];
-    if (dtype == TILES_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    return __half2float(static_cast<const __half*>(p)[i]);
+// A token's weights j0 .. j0 + K - 1 (asked for beside its slots, not after them)
+// as they lie in memory, and one of them as a number.
+template <int K>
+__device__ __forceinline__ void load_weights(const CombineArgs& a, int64_t token, int j0, bool live,
+                                             uint32_t (&w)[K]) {
+    const int64_t at = token * a.ld_weights + j0;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        w[j] = 0x3f800000u;                                    // 1
+        if (a.weights && live && j0 + j < a.k)
+            w[j] = a.weight_dtype == TILES_F32 ? static_cast<const uint32_t*>(a.weights)[at + j]
+                                               : static_cast<const uint16_t*>(a.weights)[at + j];
+    }
 }
 
-// Elements a thread moves at a time: 16 bytes, or one where rows start anywhere.
-template <typename T, bool VEC>
-struct Piece {
-    static constexpr int N = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
-    uint4 q;
-    T one;
+__device__ __forceinline__ float weight_of(const CombineArgs& a, uint32_t bits) {
+    if (!a.weights || a.weight_dtype == TILES_F32) return __uint_as_float(bits);
+    return a.weight_dtype == TILES_BF16 ? unpack2<__nv_bfloat16>(bits).x : unpack2<__half>(bits).x;
+}
 
-    __device__ __forceinline__ void load(const T* p) {
-        if constexpr (VEC) q = *reinterpret_cast<const uint4*>(p);
-        else one = *p;
-    }
-    __device__ __forceinline__ void clear() {
-        if constexpr (VEC) q = make_uint4(0, 0, 0, 0);
-        else one = from_float<T>(0.0f);
-    }
-    __device__ __forceinline__ void get(float (&v)[N]) const {
-        if constexpr (!VEC) {
-            v[0] = to_float(one);
-        } else if constexpr (sizeof(T) == 4) {
+// 16 bytes of elements.
+template <typename T>
+struct Piece {
+    static constexpr int N = 16 / static_cast<int>(sizeof(T));
+
+    static __device__ __forceinline__ void widen(const uint4& q, float (&v)[N]) {
+        if constexpr (sizeof(T) == 4) {
             v[0] = __uint_as_float(q.x);
             v[1] = __uint_as_float(q.y);
             v[2] = __uint_as_float(q.z);
@@ -338,117 +514,269 @@ struct Piece {
         }
     }
     static __device__ __forceinline__ void store(T* p, const float (&v)[N]) {
-        if constexpr (!VEC) {
-            *p = from_float<T>(v[0]);
-        } else if constexpr (sizeof(T) == 4) {
+        if constexpr (sizeof(T) == 4)
             *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
+        else
             *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
                                                       pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
-        }
     }
 };
 
-// y[t] = the sum over the token's choices, in their order, in fp32.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(512) combine_kernel(const CombineArgs a) {
-    using P = Piece<T, VEC>;
+// The bytes of a matrix's rows that are read.
+template <typename T>
+__device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t ld, int64_t cols) {
+    const char* at = static_cast<const char*>(p);
+    return {at, at + ((rows - 1) * ld + cols) * static_cast<int64_t>(sizeof(T))};
+}
+
+// y[t] = the sum over the token's choices, in their order, in fp32.  One piece a
+// thread, its choices' loads in flight together.  K: choices at
+// a time.  ODD: rows that start anywhere.
+template <typename T, bool ODD, int K>
+__global__ void __launch_bounds__(kMoveThreads) combine_kernel(const CombineArgs a) {
+    using P = Piece<T>;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (token >= a.tokens) return;
-    const int32_t* slots = a.slots + token * a.ld_slots;
+    const Place at(static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x, a.pieces);
+    if (at.token >= a.tokens) return;
     const T* in = static_cast<const T*>(a.in);
-    T* y = static_cast<T*>(a.out) + token * a.ld_out;
-    for (int64_t c = threadIdx.x * P::N; c < a.cols; c += blockDim.x * P::N) {
+    T* y = static_cast<T*>(a.out) + at.token * a.ld_out;
+    int64_t c = static_cast<int64_t>(at.piece) * P::N;
+    constexpr int64_t kSize = sizeof(T);
+    const bool small = ODD && a.cols * kSize < 16;             // (then the row is one thread's)
+    const Cut cut(y, small ? 16 : static_cast<int32_t>(a.cols * kSize), at.piece);
+    if constexpr (ODD) {
+        if (small) {
+            for (int64_t i = at.piece == 0 ? 0 : a.cols; i < a.cols; ++i) {
+                float sum = 0.0f;
+                for (int j = 0; j < a.k; ++j) {
+                    const int32_t row = a.slots[at.token * a.ld_slots + j];
+                    uint32_t w[1];
+                    load_weights<1>(a, at.token, j, true, w);
+                    if (names(row, a.rows)) sum = fmaf(weight_of(a, w[0]), to_float(in[row * a.ld_in + i]), sum);
+                }
+                y[i] = from_float<T>(sum);
+            }
+            return;
+        }
+        if (cut.none()) return;
+        c = cut.window / kSize;
+    }
+    const Extent e = extent_of<T>(a.in, a.rows, a.ld_in, a.cols);
+    in += c;
+    float sum[P::N];
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) sum[i] = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += K) {
+        int32_t row[K];
+        uint4 p[K];
+        uint32_t w[K];
+        load_weights<K>(a, at.token, j0, true, w);
+        load_slots<K>(a.slots, a.ld_slots, at.token, j0, a.k, true, row);
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (names(row[j], a.rows)) {
+                const T* from = in + row[j] * a.ld_in;
+                if constexpr (ODD) p[j] = unaligned16(reinterpret_cast<const char*>(from), e, sizeof(T));
+                else p[j] = *reinterpret_cast<const uint4*>(from);
+            }
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (names(row[j], a.rows)) {       // a choice without a row adds nothing, whatever its weight is
+                const float f = weight_of(a, w[j]);
+                float v[P::N];
+                P::widen(p[j], v);
+#pragma unroll
+                for (int i = 0; i < P::N; ++i) sum[i] = fmaf(f, v[i], sum[i]);
+            }
+    }
+    if (!ODD || cut.whole()) {
+        P::store(y + c, sum);
+    } else {
+#pragma unroll
+        for (int i = 0; i < P::N; ++i)
+            if (cut.has(i * static_cast<int>(kSize))) y[c + i] = from_float<T>(sum[i]);
+    }
+}
+
+// The same over many pieces, 16 bytes each: the next S - 1 pieces' rows on their
+// way into shared memory while one is added up; what a thread copies only it
+// reads, so that nothing waits for other threads.  K: choices, at most eight.
+constexpr int kRingBlock = 512;
+
+template <typename T, int K, int S>
+__global__ void __launch_bounds__(kRingBlock) combine_ring_kernel(const CombineArgs a) {
+    using P = Piece<T>;
+    extern __shared__ uint4 ring_smem[];
+    uint4* const ring = ring_smem + threadIdx.x;               // [S][K][threads]
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    Place ahead(static_cast<int64_t>(blockIdx.x) * kRingBlock + threadIdx.x, a.pieces), at = ahead;
+    const T* in = static_cast<const T*>(a.in);
+    auto look = [&](const Place& p, int32_t (&row)[K]) {
+        load_slots<K>(a.slots, a.ld_slots, p.token, 0, a.k, p.token < a.tokens, row);
+    };
+    auto fetch = [&](int stage, const int32_t (&row)[K]) {      // the piece `ahead`
+        const T* from = in + static_cast<int64_t>(ahead.piece) * P::N;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            if (names(row[j], a.rows))
+                ptx::cp_async_16(ring + (stage * K + j) * kRingBlock, from + row[j] * a.ld_in);
+        ptx::cp_async_commit();
+        ahead.advance(a.step_tokens, a.step_pieces, a.pieces);
+    };
+    int32_t row[K], row_next[K];                               // of the piece added up now, and next
+    uint32_t w[K], w_next[K];
+    auto weigh = [&](const Place& p) {
+        look(p, row_next);
+        load_weights<K>(a, p.token, 0, p.token < a.tokens, w_next);
+    };
+    int32_t next[K];                                           // slots of `ahead`
+    {
+        int32_t first[S][K];
+        Place p = ahead;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            look(p, first[i]);
+            p.advance(a.step_tokens, a.step_pieces, a.pieces);
+        }
+        weigh(at);
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) fetch(i, first[i]);
+#pragma unroll
+        for (int j = 0; j < K; ++j) next[j] = first[S - 1][j];
+    }
+    int stage = 0;
+    while (at.token < a.tokens) {
+        fetch(stage == 0 ? S - 1 : stage - 1, next);
+        look(ahead, next);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            row[j] = row_next[j];
+            w[j] = w_next[j];
+        }
+        T* const y = static_cast<T*>(a.out) + at.token * a.ld_out + static_cast<int64_t>(at.piece) * P::N;
+        at.advance(a.step_tokens, a.step_pieces, a.pieces);
+        weigh(at);
+        ptx::cp_async_wait_groups<S - 1>();
         float sum[P::N];
 #pragma unroll
         for (int i = 0; i < P::N; ++i) sum[i] = 0.0f;
-        for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-            P p[kChoices];
-            float w[kChoices];
 #pragma unroll
-            for (int j = 0; j < kChoices; ++j) {
-                const int32_t row = j0 + j < a.k ? slots[j0 + j] : -1;
-                // A choice without an expert adds nothing, whatever its weight is.
-                p[j].clear();
-                w[j] = 0.0f;
-                if (row >= 0 && row < a.rows) {
-                    p[j].load(in + row * a.ld_in + c);
-                    w[j] = a.weights ? load_any(a.weights, a.weight_dtype, token * a.ld_weights + j0 + j)
-                                     : 1.0f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kChoices; ++j) {
+        for (int j = 0; j < K; ++j)
+            if (names(row[j], a.rows)) {
+                const float f = weight_of(a, w[j]);
                 float v[P::N];
-                p[j].get(v);
+                P::widen(ring[(stage * K + j) * kRingBlock], v);
 #pragma unroll
-                for (int i = 0; i < P::N; ++i) sum[i] = fmaf(w[j], v[i], sum[i]);
+                for (int i = 0; i < P::N; ++i) sum[i] = fmaf(f, v[i], sum[i]);
             }
-        }
-        P::store(y + c, sum);
+        P::store(y, sum);
+        stage = stage + 1 == S ? 0 : stage + 1;
     }
 }
 
 // drows[slots[t][j]] = w[t][j] dy[t] and dw[t][j] = dy[t] . rows[slots[t][j]]: dy's
 // row is read once for all choices, and every expert row as its gradient is
-// written.
-template <typename T, bool VEC>
+// written.  A token's threads are a power of two within a warp, or whole warps.
+// ODD: rows that start anywhere, in pieces of each choice's row of drows.
+template <typename T, bool ODD>
 __global__ void __launch_bounds__(512) combine_grad_kernel(const CombineArgs a) {
-    using P = Piece<T, VEC>;
-    __shared__ float part[kChoices][16];       // one warp a word, where a token has several
+    using P = Piece<T>;
+    constexpr int K = ODD ? 2 : 4;             // choices at a time
+    constexpr int64_t kSize = sizeof(T);
+    constexpr uint32_t kAll = (1u << P::N) - 1;
+    __shared__ float part[K][16];              // one warp a word, where a token has several
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int64_t token = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = token < a.tokens;        // (all threads take part in the sums)
-    const int32_t* slots = a.slots + token * a.ld_slots;
     const T* dy = static_cast<const T*>(a.dy) + token * a.ld_dy;
     const T* in = static_cast<const T*>(a.in);
     T* out = static_cast<T*>(a.out);
-    for (int j0 = 0; j0 < a.k; j0 += kChoices) {
-        int32_t row[kChoices];
-        float w[kChoices], dot[kChoices];
+    const Extent of_dy = extent_of<T>(a.dy, a.tokens, a.ld_dy, a.cols);
+    const Extent of_in = extent_of<T>(a.in, a.rows, a.ld_in, a.cols);
+    for (int j0 = 0; j0 < a.k; j0 += K) {
+        int32_t row[K];
+        uint32_t bits[K];
+        float w[K], dot[K];
+        load_weights<K>(a, token, j0, live, bits);
+        load_slots<K>(a.slots, a.ld_slots, token, j0, a.k, live, row);
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j) {
-            row[j] = live && j0 + j < a.k ? slots[j0 + j] : -1;
-            if (row[j] >= a.rows) row[j] = -1;
-            w[j] = row[j] >= 0 ? load_any(a.weights, a.weight_dtype, token * a.ld_weights + j0 + j) : 0.0f;
+        for (int j = 0; j < K; ++j) {
+            if (!names(row[j], a.rows)) row[j] = -1;
+            w[j] = weight_of(a, bits[j]);
             dot[j] = 0.0f;
         }
-        if (live)
-            for (int64_t c = threadIdx.x * P::N; c < a.cols; c += blockDim.x * P::N) {
-                P g, p[kChoices];
-                g.load(dy + c);
+        if (ODD && a.cols * kSize < 16) {      // a row of less than a piece: its first thread's
+            if (live && threadIdx.x == 0)
+                for (int64_t i = 0; i < a.cols; ++i)
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j)
-                    if (row[j] >= 0) p[j].load(in + row[j] * a.ld_in + c);
-                float d[P::N];
-                g.get(d);
+                    for (int j = 0; j < K; ++j)
+                        if (row[j] >= 0) {
+                            const float d = to_float(dy[i]);
+                            dot[j] = fmaf(d, to_float(in[row[j] * a.ld_in + i]), dot[j]);
+                            out[row[j] * a.ld_out + i] = from_float<T>(d * w[j]);
+                        }
+        } else if (live)
+            for (int32_t piece = threadIdx.x; piece < a.pieces; piece += blockDim.x) {
+                uint4 g[ODD ? K : 1], p[K];
+                int64_t c[K];
+                uint32_t has[K];               // the elements of a piece, by bits
+                if constexpr (!ODD) g[0] = *reinterpret_cast<const uint4*>(dy + static_cast<int64_t>(piece) * P::N);
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j)
-                    if (row[j] >= 0) {
-                        float v[P::N], o[P::N];
-                        p[j].get(v);
+                for (int j = 0; j < K; ++j) {
+                    has[j] = row[j] >= 0 ? kAll : 0u;
+                    c[j] = static_cast<int64_t>(piece) * P::N;
+                    if (row[j] < 0) continue;
+                    const T* from = in + row[j] * a.ld_in;
+                    if constexpr (ODD) {
+                        const Cut cut(out + row[j] * a.ld_out, static_cast<int32_t>(a.cols * kSize), piece);
+                        has[j] = 0;
+                        if (cut.none()) continue;
+                        c[j] = cut.window / kSize;
+#pragma unroll
+                        for (int i = 0; i < P::N; ++i)
+                            has[j] |= cut.has(i * static_cast<int>(kSize)) ? 1u << i : 0u;
+                        g[j] = unaligned16(reinterpret_cast<const char*>(dy + c[j]), of_dy, sizeof(T));
+                        p[j] = unaligned16(reinterpret_cast<const char*>(from + c[j]), of_in, sizeof(T));
+                    } else {
+                        p[j] = *reinterpret_cast<const uint4*>(from + c[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (has[j]) {
+                        float d[P::N], v[P::N], o[P::N];
+                        P::widen(g[ODD ? j : 0], d);
+                        P::widen(p[j], v);
+                        T* to = out + row[j] * a.ld_out + c[j];
 #pragma unroll
                         for (int i = 0; i < P::N; ++i) {
-                            dot[j] = fmaf(d[i], v[i], dot[j]);
+                            const float f = fmaf(d[i], v[i], dot[j]);
+                            dot[j] = !ODD || has[j] >> i & 1 ? f : dot[j];
                             o[i] = d[i] * w[j];
                         }
-                        P::store(out + row[j] * a.ld_out + c, o);
+                        if (!ODD || has[j] == kAll) {
+                            P::store(to, o);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < P::N; ++i)
+                                if (has[j] >> i & 1) to[i] = from_float<T>(o[i]);
+                        }
                     }
             }
         const int lanes = min(32, static_cast<int>(blockDim.x));
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j)
+        for (int j = 0; j < K; ++j)
             for (int d = lanes >> 1; d >= 1; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
         if (blockDim.x > 32) {                 // then blockDim.y == 1
             const int warps = blockDim.x >> 5;
             if ((threadIdx.x & 31) == 0)
 #pragma unroll
-                for (int j = 0; j < kChoices; ++j) part[j][threadIdx.x >> 5] = dot[j];
+                for (int j = 0; j < K; ++j) part[j][threadIdx.x >> 5] = dot[j];
             __syncthreads();
-            if (threadIdx.x < kChoices && j0 + static_cast<int>(threadIdx.x) < a.k) {
+            if (threadIdx.x < K && j0 + static_cast<int>(threadIdx.x) < a.k) {
                 float s = 0.0f;
                 for (int i = 0; i < warps; ++i) s += part[threadIdx.x][i];
                 a.dweights[token * a.ld_dweights + j0 + threadIdx.x] = s;
@@ -456,9 +784,110 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(const CombineArgs a) 
             __syncthreads();
         } else if (live && threadIdx.x == 0) {
 #pragma unroll
-            for (int j = 0; j < kChoices; ++j)
+            for (int j = 0; j < K; ++j)
                 if (j0 + j < a.k) a.dweights[token * a.ld_dweights + j0 + j] = dot[j];
         }
+    }
+}
+
+// The same over many tokens, in pieces of 16 bytes, one to a thread: blockDim.x
+// threads a token (whole warps), blockDim.y tokens at a time, the next S - 1
+// tokens' rows on their way into shared memory.
+template <typename T, int K, int S>
+__global__ void __launch_bounds__(kRingBlock) combine_grad_ring_kernel(const CombineArgs a) {
+    using P = Piece<T>;
+    constexpr int STAGE = (K + 1) * kRingBlock;
+    constexpr int KK = K <= 2 ? K : K <= 4 ? 4 : 8;            // the power of two from K on
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float parts[8][2][16 * KK];                     // of tokens of several warps: [turn][warp][KK]
+    uint4* const ring = ring_smem + threadIdx.y * blockDim.x + threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+    const int c = tid * P::N;
+    const bool mine = tid < a.pieces;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    int64_t token = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y, ahead = token;
+    const T* in = static_cast<const T*>(a.in) + c;
+    T* out = static_cast<T*>(a.out) + c;
+    auto look = [&](int64_t t, int32_t (&row)[K]) {
+        load_slots<K>(a.slots, a.ld_slots, t, 0, a.k, t < a.tokens, row);
+    };
+    auto fetch = [&](int stage, const int32_t (&row)[K]) {      // the token `ahead`
+        if (mine && ahead < a.tokens) {
+            uint4* to = ring + stage * STAGE;
+            ptx::cp_async_16(to, static_cast<const T*>(a.dy) + ahead * a.ld_dy + c);
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (names(row[j], a.rows))
+                    ptx::cp_async_16(to + (j + 1) * kRingBlock, in + row[j] * a.ld_in);
+        }
+        ptx::cp_async_commit();
+        ahead += stride;
+    };
+    int32_t row[K], row_next[K];                               // of the token worked on now, and next
+    uint32_t w[K], w_next[K];
+    auto weigh = [&](int64_t t) {
+        look(t, row_next);
+        load_weights<K>(a, t, 0, t < a.tokens, w_next);
+    };
+    int32_t next[K];                                           // slots of `ahead`
+    {
+        int32_t first[S][K];
+#pragma unroll
+        for (int i = 0; i < S; ++i) look(ahead + i * stride, first[i]);
+        weigh(token);
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) fetch(i, first[i]);
+#pragma unroll
+        for (int j = 0; j < K; ++j) next[j] = first[S - 1][j];
+    }
+    int stage = 0, turn = 0;
+    for (; token < a.tokens; token += stride, turn ^= 1) {
+        fetch(stage == 0 ? S - 1 : stage - 1, next);
+        look(ahead, next);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            row[j] = row_next[j];
+            w[j] = w_next[j];
+        }
+        weigh(token + stride);
+        ptx::cp_async_wait_groups<S - 1>();
+        float dot[KK];
+#pragma unroll
+        for (int j = 0; j < KK; ++j) dot[j] = 0.0f;
+        if (mine) {
+            const uint4* from = ring + stage * STAGE;
+            float d[P::N];
+            P::widen(from[0], d);
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (names(row[j], a.rows)) {
+                    const float f = weight_of(a, w[j]);
+                    float e[P::N], o[P::N];
+                    P::widen(from[(j + 1) * kRingBlock], e);
+#pragma unroll
+                    for (int i = 0; i < P::N; ++i) {
+                        dot[j] = fmaf(d[i], e[i], dot[j]);
+                        o[i] = d[i] * f;
+                    }
+                    P::store(out + row[j] * a.ld_out, o);
+                }
+        }
+        float x = fold<KK, K>(dot);            // lane l: the warp's sum of choice l % KK
+        if (warps > 1) {
+            float* at = parts[threadIdx.y][turn];
+            if (lane < KK) at[(tid >> 5) * KK + lane] = x;
+            ptx::named_barrier(1 + threadIdx.y, blockDim.x);
+            if (tid < 32) {
+                x = 0.0f;
+                for (int i = lane; i < warps * KK; i += 32) x += at[i];
+#pragma unroll
+                for (int i = 16; i >= KK; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+            }
+        }
+        if (tid < a.k) a.dweights[token * a.ld_dweights + tid] = x;
+        stage = stage + 1 == S ? 0 : stage + 1;
     }
 }
 
@@ -474,35 +903,124 @@ dim3 token_block(int64_t pieces) {
     return dim3(static_cast<unsigned>(((pieces + rounds - 1) / rounds + 31) / 32 * 32), 1);
 }
 
-dim3 token_grid(int64_t tokens, dim3 block) {
-    return dim3(static_cast<unsigned>((tokens + block.y - 1) / block.y));
+// Blocks that move scales, past those that move rows.
+unsigned scale_grid(const DispatchArgs& a, int sms) {
+    if (!a.scales) return 0;
+    return static_cast<unsigned>(std::min<int64_t>(
+        (a.tokens * a.blocks + kMoveThreads - 1) / kMoveThreads, 2 * static_cast<int64_t>(sms)));
 }
 
-template <typename V>
+template <int K, int U>
 int launch_dispatch(DispatchArgs a, int sms, cudaStream_t st) {
-    const dim3 block = token_block(a.pieces);
-    dim3 grid = token_grid(a.tokens, block);
-    a.row_grid = grid.x;
-    if (a.scales) {
-        const int64_t threads = static_cast<int64_t>(block.x) * block.y;
-        grid.x += static_cast<unsigned>(
-            std::min<int64_t>((a.tokens * a.blocks + threads - 1) / threads, 4 * static_cast<int64_t>(sms)));
+    // Every block one round (8192 x 4 rows of 4096 bf16 54 us, with 4 blocks an SM
+    // that go round 63), as far as a grid goes.
+    constexpr int64_t kShare = U * kMoveThreads;
+    const int64_t grid = std::min<int64_t>((a.tokens * a.pieces + kShare - 1) / kShare, 1 << 30);
+    a.near_tokens = kMoveThreads / a.pieces;
+    a.near_pieces = kMoveThreads % a.pieces;
+    a.step_tokens = (grid - 1) * kShare / a.pieces;
+    a.step_pieces = static_cast<int32_t>((grid - 1) * kShare % a.pieces);
+    a.row_grid = static_cast<uint32_t>(grid);
+    return launch(dispatch_kernel<K, U>, dim3(a.row_grid + scale_grid(a, sms)), dim3(kMoveThreads), 0, st, a);
+}
+
+int launch_dispatch(DispatchArgs a, bool odd, int sms, cudaStream_t st) {
+    if (odd) {
+        a.pieces = static_cast<int32_t>((a.row_bytes + 14) / 16 + 1);
+        const int64_t grid = (a.tokens * a.k * a.pieces + kMoveThreads - 1) / kMoveThreads;
+        if (grid > 1 << 30) return static_cast<int>(cudaErrorInvalidConfiguration);
+        a.row_grid = static_cast<uint32_t>(grid);
+        return launch(dispatch_odd_kernel, dim3(a.row_grid + scale_grid(a, sms)), dim3(kMoveThreads), 0, st, a);
     }
-    return launch(dispatch_kernel<V>, grid, block, 0, st, a);
+    a.pieces = static_cast<int32_t>(a.row_bytes / 16);
+    if (a.k == 1) return launch_dispatch<1, 4>(a, sms, st);
+    if (a.k <= 2) return launch_dispatch<2, 4>(a, sms, st);
+    if (a.k <= 4) return launch_dispatch<4, 2>(a, sms, st);
+    return launch_dispatch<kChoices, 2>(a, sms, st);
+}
+
+// PER: blocks an SM.
+template <typename T, int K, int S, int PER>
+int launch_combine_ring(CombineArgs a, int sms, cudaStream_t st) {
+    constexpr size_t kBytes = static_cast<size_t>(S) * K * kRingBlock * 16;
+    static_assert(kBytes <= kRingBytesMost && PER * (kBytes + 1024) <= 228 * 1024, "the blocks fit an SM");
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(combine_ring_kernel<T, K, S>, kRingBytesMost, &opted);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    const int64_t grid = std::min<int64_t>((a.tokens * a.pieces + kRingBlock - 1) / kRingBlock,
+                                           static_cast<int64_t>(PER) * sms);
+    a.step_tokens = grid * kRingBlock / a.pieces;
+    a.step_pieces = static_cast<int32_t>(grid * kRingBlock % a.pieces);
+    return launch(combine_ring_kernel<T, K, S>, dim3(static_cast<unsigned>(grid)), dim3(kRingBlock),
+                  std::max(kBytes, exact_smem(PER)), st, a);
+}
+
+template <typename T, int K, int S, int PER>
+int launch_combine_grad_ring(const CombineArgs& a, int sms, cudaStream_t st) {
+    constexpr size_t kBytes = static_cast<size_t>(S) * (K + 1) * kRingBlock * 16;
+    static_assert(kBytes <= kRingBytesMost && PER * (kBytes + 1024) <= 228 * 1024, "the blocks fit an SM");
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(combine_grad_ring_kernel<T, K, S>, kRingBytesMost, &opted);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    const unsigned threads = static_cast<unsigned>((a.pieces + 31) / 32 * 32);
+    const unsigned tokens = std::max(1u, kRingBlock / threads);
+    const unsigned grid = static_cast<unsigned>(
+        std::min<int64_t>((a.tokens + tokens - 1) / tokens, static_cast<int64_t>(PER) * sms));
+    return launch(combine_grad_ring_kernel<T, K, S>, dim3(grid), dim3(threads, tokens), kBytes, st, a);
 }
 
 template <typename T>
-int launch_combine(const CombineArgs& a, bool vec, bool grad, cudaStream_t st) {
-    const int n = vec ? 16 / static_cast<int>(sizeof(T)) : 1;
-    const dim3 block = token_block((a.cols + n - 1) / n), grid = token_grid(a.tokens, block);
-    if (grad)
-        return vec ? launch(combine_grad_kernel<T, true>, grid, block, 0, st, a)
-                   : launch(combine_grad_kernel<T, false>, grid, block, 0, st, a);
-    return vec ? launch(combine_kernel<T, true>, grid, block, 0, st, a)
-               : launch(combine_kernel<T, false>, grid, block, 0, st, a);
+int launch_combine_grad(CombineArgs a, bool odd, int sms, cudaStream_t st) {
+    constexpr int64_t N = Piece<T>::N;
+    // The ring takes tokens of some pieces, one to a thread, where every block has
+    // a few of them (500 x 4 rows of 2048 bf16: 6.4 us against 9.3 without it).
+    a.pieces = static_cast<int32_t>(odd ? (a.cols * static_cast<int64_t>(sizeof(T)) + 14) / 16 + 1 : a.cols / N);
+    if (!odd && a.k <= 8 && a.pieces > 16 && a.pieces <= kRingBlock && a.tokens >= 2 * sms) {
+        // With few choices a token is little work: two blocks an SM (32768 rows of
+        // 2048 bf16, k 1: 74 us against 97 with one of twice the stages, k 2
+        // 57.5 against 68; k 4 55.4 against 51.5).
+        if (a.k == 1) return launch_combine_grad_ring<T, 1, 6, 2>(a, sms, st);
+        if (a.k == 2) return launch_combine_grad_ring<T, 2, 4, 2>(a, sms, st);
+        if (a.k == 3) return launch_combine_grad_ring<T, 3, 4, 1>(a, sms, st);
+        if (a.k == 4) return launch_combine_grad_ring<T, 4, 4, 1>(a, sms, st);
+        if (a.k <= 6) return launch_combine_grad_ring<T, 6, 3, 1>(a, sms, st);
+        return launch_combine_grad_ring<T, 8, 2, 1>(a, sms, st);
+    }
+    const dim3 block = token_block(a.pieces);
+    const dim3 grid(static_cast<unsigned>((a.tokens + block.y - 1) / block.y));
+    return odd ? launch(combine_grad_kernel<T, true>, grid, block, 0, st, a)
+               : launch(combine_grad_kernel<T, false>, grid, block, 0, st, a);
+}
+
+template <typename T>
+int launch_combine(CombineArgs a, bool odd, int sms, cudaStream_t st) {
+    constexpr int64_t N = Piece<T>::N;
+    a.pieces = static_cast<int32_t>(odd ? (a.cols * static_cast<int64_t>(sizeof(T)) + 14) / 16 + 1 : a.cols / N);
+    const int64_t units = a.tokens * a.pieces;
+    if (!odd && a.k <= 8 && units >= 4 * static_cast<int64_t>(sms) * kRingBlock) {
+        // Threads an SM: as many as hold some 100 KB in flight (32768 rows of 2048
+        // bf16: k 1 50 us with three blocks, 82 with one; k 2 35 against 50; k 4
+        // 29.4 with two, 33.3 with one, 32.1 with three of fewer stages).
+        if (a.k == 1) return launch_combine_ring<T, 1, 8, 3>(a, sms, st);
+        if (a.k == 2) return launch_combine_ring<T, 2, 4, 3>(a, sms, st);
+        if (a.k == 3) return launch_combine_ring<T, 3, 4, 2>(a, sms, st);
+        if (a.k == 4) return launch_combine_ring<T, 4, 3, 2>(a, sms, st);
+        if (a.k <= 6) return launch_combine_ring<T, 6, 2, 2>(a, sms, st);
+        return launch_combine_ring<T, 8, 3, 1>(a, sms, st);
+    }
+    const int64_t grid = (units + kMoveThreads - 1) / kMoveThreads;
+    if (grid > INT32_MAX) return static_cast<int>(cudaErrorInvalidConfiguration);
+    const dim3 g(static_cast<unsigned>(grid)), b(kMoveThreads);
+    if (a.k <= 4)
+        return odd ? launch(combine_kernel<T, true, 4>, g, b, 0, st, a)
+                   : launch(combine_kernel<T, false, 4>, g, b, 0, st, a);
+    return odd ? launch(combine_kernel<T, true, 8>, g, b, 0, st, a)
+               : launch(combine_kernel<T, false, 8>, g, b, 0, st, a);
 }
 
 // ---- checks ---------------------------------------------------------------------
+
+constexpr int64_t kMaxCols = 1 << 28;          // the bytes of a row, and of its pieces, in 32 bits
 
 int check_route(int64_t tokens, int64_t k, const int32_t* slots, int64_t ld_slots) {
     if (tokens < 0 || k < 1)
@@ -524,7 +1042,8 @@ int check_combine(const tiles_combine_desc* d, bool grad) {
     if (d->rows < 0 || d->cols < 1)
         return fail(TILES_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1 (rows=%lld cols=%lld)",
                     (long long)d->rows, (long long)d->cols);
-    if (d->rows > INT32_MAX || d->cols > kMaxRows) return fail(TILES_ERR_TOO_LARGE, "a size is too large");
+    if (d->rows > INT32_MAX || d->cols > kMaxCols)
+        return fail(TILES_ERR_TOO_LARGE, "more than 2^31 - 1 rows or 2^28 columns");
     const int eb = dtype_bytes(d->dtype);
     if (!eb) return fail(TILES_ERR_UNSUPPORTED_DTYPE, "the rows must be f16, bf16 or f32");
     if (d->tokens == 0) return TILES_OK;
@@ -555,14 +1074,26 @@ int run_combine(const tiles_combine_desc* d, bool grad, void* stream) {
     const int eb = dtype_bytes(d->dtype);
     const CombineArgs a{d->tokens, d->cols, d->rows, d->ld_slots, static_cast<int32_t>(d->k),
                         d->weight_dtype, d->slots, d->weights, d->ld_weights, d->in, d->ld_in, d->dy,
-                        d->ld_dy, d->out, d->ld_out, d->dweights, d->ld_dweights};
-    const bool vec = d->cols * eb % 16 == 0 && whole16(d->in, d->ld_in, eb) &&
-                     whole16(d->out, d->ld_out, eb) && (!grad || whole16(d->dy, d->ld_dy, eb));
+                        d->ld_dy, d->out, d->ld_out, d->dweights, d->ld_dweights, 0, 0, 0};
+    // Whether every row starts and ends on 16 bytes.
+    const uint64_t all = reinterpret_cast<uintptr_t>(d->in) | reinterpret_cast<uintptr_t>(d->out) |
+                         static_cast<uint64_t>(d->cols * eb) |
+                         static_cast<uint64_t>(d->rows > 1 ? d->ld_in * eb : 0) |
+                         static_cast<uint64_t>((grad ? d->rows : d->tokens) > 1 ? d->ld_out * eb : 0) |
+                         (grad ? reinterpret_cast<uintptr_t>(d->dy) |
+                                     static_cast<uint64_t>(d->tokens > 1 ? d->ld_dy * eb : 0) : 0);
+    const bool odd = all % 16 != 0;
+    int sms = 0;
+    const int q = current_sm_count(&sms);
+    if (q != TILES_OK) return q;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int e;
-    if (d->dtype == TILES_BF16) e = launch_combine<__nv_bfloat16>(a, vec, grad, st);
-    else if (d->dtype == TILES_F16) e = launch_combine<__half>(a, vec, grad, st);
-    else e = launch_combine<float>(a, vec, grad, st);
+    auto go = [&](auto zero) {
+        using T = decltype(zero);
+        return grad ? launch_combine_grad<T>(a, odd, sms, st) : launch_combine<T>(a, odd, sms, st);
+    };
+    const int e = d->dtype == TILES_F32    ? go(float())
+                  : d->dtype == TILES_BF16 ? go(__nv_bfloat16())
+                                           : go(__half());
     return launch_status(e, grad ? "combine gradient" : "combine");
 }
 
@@ -635,7 +1166,8 @@ int tiles_expert_dispatch(const tiles_dispatch_desc* d, void* stream) {
     if (d->rows < 0 || d->cols < 1)
         return fail(TILES_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1 (rows=%lld cols=%lld)",
                     (long long)d->rows, (long long)d->cols);
-    if (d->rows > INT32_MAX || d->cols > kMaxRows) return fail(TILES_ERR_TOO_LARGE, "a size is too large");
+    if (d->rows > INT32_MAX || d->cols > kMaxCols)
+        return fail(TILES_ERR_TOO_LARGE, "more than 2^31 - 1 rows or 2^28 columns");
     const int eb = d->dtype == TILES_E4M3 ? 1 : dtype_bytes(d->dtype);
     if (!eb) return fail(TILES_ERR_UNSUPPORTED_DTYPE, "the rows must be f16, bf16, f32 or e4m3");
     if (d->tokens == 0 || d->rows == 0) return TILES_OK;
@@ -645,30 +1177,33 @@ int tiles_expert_dispatch(const tiles_dispatch_desc* d, void* stream) {
         return fail(TILES_ERR_INVALID_ARG, "scales go with out_scales");
     if (!element_aligned(d->scales, 4) || !element_aligned(d->out_scales, 4))
         return fail(TILES_ERR_MISALIGNED, "the scales are not aligned to their element");
-    const int64_t row_bytes = d->cols * eb;
-    DispatchArgs a{d->tokens, d->rows, d->ld_slots, static_cast<int32_t>(d->k), d->slots,
-                   static_cast<const char*>(d->x), static_cast<char*>(d->out), d->ldx * eb,
-                   d->ld_out * eb, 0, d->scales, d->out_scales, d->scale_row, d->scale_block,
-                   d->out_scale_row, d->out_scale_block,
-                   static_cast<int32_t>((d->cols + kBlock - 1) / kBlock), 0};
-    // The widest piece that every row is whole in.
+    DispatchArgs a{};
+    a.tokens = d->tokens;
+    a.rows = d->rows;
+    a.ld_slots = d->ld_slots;
+    a.k = static_cast<int32_t>(d->k);
+    a.row_bytes = static_cast<int32_t>(d->cols * eb);
+    a.elem_bytes = eb;
+    a.slots = d->slots;
+    a.x = static_cast<const char*>(d->x);
+    a.out = static_cast<char*>(d->out);
+    a.pitch_x = d->ldx * eb;
+    a.pitch_out = d->ld_out * eb;
+    a.scales = d->scales;
+    a.out_scales = d->out_scales;
+    a.scale_row = d->scale_row;
+    a.scale_block = d->scale_block;
+    a.out_scale_row = d->out_scale_row;
+    a.out_scale_block = d->out_scale_block;
+    a.blocks = static_cast<int32_t>((d->cols + kBlock - 1) / kBlock);
+    // Whether every row starts and ends on 16 bytes.
     const uint64_t all = reinterpret_cast<uintptr_t>(d->x) | reinterpret_cast<uintptr_t>(d->out) |
-                         static_cast<uint64_t>(row_bytes) |
+                         static_cast<uint64_t>(a.row_bytes) |
                          static_cast<uint64_t>(d->tokens > 1 ? a.pitch_x : 0) |
                          static_cast<uint64_t>(d->rows > 1 ? a.pitch_out : 0);
-    const int piece = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
-    a.pieces = row_bytes / piece;
     int sms = 0;
     if ((s = current_sm_count(&sms)) != TILES_OK) return s;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int e;
-    switch (piece) {
-        case 16: e = launch_dispatch<uint4>(a, sms, st); break;
-        case 8: e = launch_dispatch<uint2>(a, sms, st); break;
-        case 4: e = launch_dispatch<uint32_t>(a, sms, st); break;
-        case 2: e = launch_dispatch<uint16_t>(a, sms, st); break;
-        default: e = launch_dispatch<uint8_t>(a, sms, st); break;
-    }
+    const int e = launch_dispatch(a, all % 16 != 0, sms, static_cast<cudaStream_t>(stream));
     return launch_status(e, "dispatch");
 }
 
