@@ -819,7 +819,7 @@ typedef struct {
 
 /* Workspace bytes of the sort: the 256-byte header (left alone) and the counts
  * of its blocks (0 on invalid arguments).  16-byte aligned; its contents do not
- * matter.  Host only. */
+ * matter.  Where it is no more than the header NULL is taken too.  Host only. */
 size_t tiles_expert_sort_workspace_bytes(int64_t tokens, int64_t k, int64_t groups);
 
 int tiles_expert_sort(const tiles_expert_sort_desc* desc, void* workspace, size_t ws_bytes,

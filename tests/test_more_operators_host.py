@@ -161,7 +161,7 @@ SORT = dict(tokens=8, k=2, groups=4, experts=PTR, ld=2, slots=PTR, offsets=PTR, 
     (dict(offsets=PTR + 2), _abi.ERR_INVALID_ARG),
     (dict(order=PTR + 1), _abi.ERR_MISALIGNED),
     (dict(ld=1), _abi.ERR_INVALID_ARG),
-    (dict(), _abi.ERR_INVALID_ARG),                             # no workspace
+    (dict(tokens=10000), _abi.ERR_INVALID_ARG),                 # no workspace
 ])
 def test_sort_refusals(lib, kw, status):
     d = fill(_abi.ExpertSortDesc(), SORT, **kw)

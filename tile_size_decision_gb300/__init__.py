@@ -1048,7 +1048,7 @@ def _scratch(workspace, nbytes, where, device):
     holds."""
     if nbytes == 0:
         raise TilesError(_abi.ERR_INVALID_ARG, where)
-    if workspace is None:
+    if workspace is None and nbytes > workspace_bytes():       # more than the header, which is not used
         workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
     return (workspace, *_workspace_args(workspace))
 

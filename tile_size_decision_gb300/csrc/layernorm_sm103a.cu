@@ -137,7 +137,7 @@ __device__ __forceinline__ void emit(const LayerArgs& a, int64_t row, int c, int
         keep<VEC>(y, c, cols);
         float v[8];
         y.to(v);
-        const float s = block_scale(block_amax(amax8(v))), inv = reciprocal(s);
+        const float s = max_nan(__fdiv_rn(block_amax(amax8(v)), kE4m3Max), kTinyScale), inv = __frcp_rn(s);
         const uint64_t inv2 = ptx::pair(inv, inv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y.p[i] = ptx::mul2(y.p[i], inv2);

@@ -27,6 +27,8 @@ struct SortArgs {
     int32_t* offsets;
     int32_t* order;
     uint16_t* counts;                         // [blocks][groups], with more than one block
+    int32_t* below;                           // [blocks][groups]: pairs in the blocks before; NULL: not
+    int32_t* totals;                          // [groups], with below
 };
 
 // The expert of pair p, or `groups` where its id is none's.
@@ -72,12 +74,54 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(const SortArgs a) {
 // them among its own of the same expert; the warps' counts, those of the blocks
 // before and the experts' totals then give every pair its row.  Everything
 // is counted, nothing competes: the order is stable, and the same every time.
+// The blocks' counts of every expert to what lies before each block, and the
+// totals: 32 experts a block, whose 32 rows of threads share the column.
+__global__ void __launch_bounds__(1024) sort_scan_kernel(const SortArgs a, int blocks) {
+    __shared__ int sums[32][33];
+    const int g = blockIdx.x * 32 + threadIdx.x, share = (blocks + 31) / 32;
+    const int first = threadIdx.y * share, last = min(blocks, first + share);
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const bool live = g < a.groups;
+    int s = 0;
+    if (live)
+#pragma unroll 4
+        for (int b = first; b < last; ++b) s += a.counts[static_cast<int64_t>(b) * a.groups + g];
+    sums[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    // Warp y adds up column y: lane i has the sum of the rows' shares up to i.
+    int x = sums[threadIdx.x][threadIdx.y];
+    const int n = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (static_cast<int>(threadIdx.x) >= d) x += y;
+    }
+    sums[threadIdx.x][threadIdx.y] = x - n;
+    const int column = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 31 && column < a.groups) a.totals[column] = x;
+    __syncthreads();
+    if (!live) return;
+    int run = sums[threadIdx.y][threadIdx.x];
+    for (int b = first; b < last; ++b) {
+        const int64_t at = static_cast<int64_t>(b) * a.groups + g;
+        a.below[at] = run;
+        run += a.counts[at];
+    }
+}
+
+__host__ __device__ constexpr int rank_pitch(int groups) {
+    // Counts of 16 bits: whole words, an odd number of them, so that the warps'
+    // counts of one expert lie in different banks.
+    return (groups + 1) / 2 % 2 ? (groups + 1) / 2 * 2 : (groups + 1) / 2 * 2 + 2;
+}
+
 template <int I>
 __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a) {
     extern __shared__ int start[];             // [groups]: totals, then the first row of the block's pairs
     __shared__ int sums[32];
     const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    const int warps = threads >> 5, groups = a.groups, pitch = (groups + 1) & ~1;
+    const int warps = threads >> 5, groups = a.groups, pitch = rank_pitch(groups);
     int* below = start + groups;               // [groups]: pairs in the blocks before
     uint16_t* rank = reinterpret_cast<uint16_t*>(below + groups);   // [warps][pitch]
     for (int i = tid; i < warps * pitch / 2; i += threads) reinterpret_cast<uint32_t*>(rank)[i] = 0;
@@ -117,7 +161,13 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a) {
         }
         if (gridDim.x == 1) start[g] = run;
     }
-    if (gridDim.x > 1) {
+    if (gridDim.x > 1 && a.below) {
+        ptx::grid_dependency_wait();
+        for (int g = tid; g < groups; g += threads) {
+            start[g] = a.totals[g];
+            below[g] = a.below[static_cast<int64_t>(blockIdx.x) * groups + g];
+        }
+    } else if (gridDim.x > 1) {
         ptx::grid_dependency_wait();
         // `side` threads share an expert's column of counts.
         const int side = max(1, threads / groups);
@@ -176,47 +226,66 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a) {
             a.order[p] = -1;
 }
 
-struct SortGeometry { int threads, items, blocks; };
+struct SortGeometry { int threads, items, blocks; bool scan; };
 
 SortGeometry sort_geometry(int64_t pairs, int64_t groups) {
     SortGeometry g;
-    // A warp's counts of 4096 experts are 8 KB.
-    const int most = groups > 1024 ? 512 : 1024;
-    g.threads = static_cast<int>(std::min<int64_t>(most, (std::max(pairs, groups) + 31) / 32 * 32));
     g.items = 1;
-    // One block, one launch, for as long as a block has few pairs; then as many
-    // blocks as there are SMs, of more pairs a thread where there are more.
-    if (pairs <= 4 * static_cast<int64_t>(g.threads)) {
+    g.blocks = 1;
+    g.scan = false;
+    if (pairs <= 1024) {
+        // One block, one launch (512 pairs among 64 experts 2.4 us, 2.4 with two
+        // launches; 4096 pairs 7.8 against 4.2).  A warp's counts of 4096 experts
+        // are 8 KB.
+        const int most = groups > 1024 ? 512 : 1024;
+        g.threads = static_cast<int>(std::min<int64_t>(most, (std::max(pairs, groups) + 31) / 32 * 32));
         while (pairs > static_cast<int64_t>(g.threads) * g.items) g.items *= 2;
-    } else {
-        while (g.items < kMaxSortItems && pairs > 152 * static_cast<int64_t>(g.threads) * g.items)
-            g.items *= 2;
+        return g;
     }
+    // Blocks of 1024 pairs, of 512 where that leaves SMs without (131072 pairs
+    // among 64 experts: 6.1 us, 9.0 with 1024 threads of a pair, 7.0 with 2048
+    // pairs a block); more pairs a thread where there are more than two blocks
+    // an SM.
+    g.threads = pairs <= 65536 && groups <= 256 ? 256 : 512;
+    g.items = 2;
+    while (g.items < kMaxSortItems && pairs > 304 * static_cast<int64_t>(g.threads) * g.items) g.items *= 2;
     const int64_t share = static_cast<int64_t>(g.threads) * g.items;
-    g.blocks = static_cast<int>(std::max<int64_t>(1, (pairs + share - 1) / share));
+    g.blocks = static_cast<int>((pairs + share - 1) / share);
+    // Every block adds up the blocks' counts itself, or a launch of its own does:
+    // 24 loads a thread are about a launch (131072 pairs: 64 experts 6.1 us against
+    // 7.0, 256 experts 11.8 against 7.6, 4096 experts 103 against 17.5).
+    g.scan = g.blocks > 1 && g.blocks * groups > 24 * static_cast<int64_t>(g.threads);
     return g;
+}
+
+// The header, the blocks' counts (whole 16 bytes), and what lies below each block
+// with the totals.
+size_t sort_counts_bytes(const SortGeometry& g, int64_t groups) {
+    return (static_cast<size_t>(g.blocks) * static_cast<size_t>(groups) * 2 + 15) / 16 * 16;
 }
 
 size_t sort_bytes(int64_t pairs, int64_t groups) {
     const SortGeometry g = sort_geometry(pairs, groups);
-    return kConvMinWorkspaceBytes +
-           (g.blocks > 1 ? static_cast<size_t>(g.blocks) * static_cast<size_t>(groups) * 2 : 0);
+    if (g.blocks == 1) return kConvMinWorkspaceBytes;
+    return kConvMinWorkspaceBytes + sort_counts_bytes(g, groups) +
+           (g.scan ? (static_cast<size_t>(g.blocks) + 1) * static_cast<size_t>(groups) * 4 : 0);
 }
 
 template <int I>
 int launch_sort(const SortArgs& a, const SortGeometry& g, cudaStream_t st) {
-    const int pitch = (a.groups + 1) & ~1;
-    const size_t smem = static_cast<size_t>(a.groups) * 8 + static_cast<size_t>(g.threads / 32) * pitch * 2;
+    const size_t smem = static_cast<size_t>(a.groups) * 8 +
+                        static_cast<size_t>(g.threads / 32) * rank_pitch(a.groups) * 2;
     if (smem > 40 * 1024) {
         static std::atomic<uint64_t> opted{0};
         const cudaError_t e = opt_in_smem(sort_place_kernel<I>, kRingBytesMost, &opted);
         if (e != cudaSuccess) return static_cast<int>(e);
     }
-    if (g.blocks > 1) {
-        const int e = launch(sort_count_kernel<I>, dim3(g.blocks), dim3(g.threads),
-                             static_cast<size_t>(a.groups) * 4, st, a);
-        if (e != cudaSuccess) return e;
-    }
+    int e = cudaSuccess;
+    if (g.blocks > 1)
+        e = launch(sort_count_kernel<I>, dim3(g.blocks), dim3(g.threads), static_cast<size_t>(a.groups) * 4, st, a);
+    if (e == cudaSuccess && g.scan)
+        e = launch(sort_scan_kernel, dim3((a.groups + 31) / 32), dim3(32, 32), 0, st, a, g.blocks);
+    if (e != cudaSuccess) return e;
     return launch(sort_place_kernel<I>, dim3(g.blocks), dim3(g.threads), smem, st, a);
 }
 
@@ -270,55 +339,9 @@ __device__ __forceinline__ bool names(int32_t row, int64_t rows) {
     return static_cast<uint32_t>(row) < static_cast<uint32_t>(rows);   // rows are at most 2^31 - 1
 }
 
-// Rows that start anywhere.  What is written is cut into pieces that start on 16
+// Rows that start anywhere: what is written is cut into pieces that start on 16
 // bytes of its own row (the first and the last may be part of one); what is read
-// for a piece starts anywhere, and is put together from the two aligned pieces
-// that hold it.
-struct Extent {                               // of a matrix that is read
-    const char* from;
-    const char* to;                           // past its last byte
-};
-
-__device__ __forceinline__ uint4 unaligned16(const char* p, const Extent& e, int elem_bytes) {
-    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
-    const char* base = p - s;
-    if (s == 0) return *reinterpret_cast<const uint4*>(p);
-    uint32_t w[8];
-    if (base >= e.from && base + 32 <= e.to) {
-        const uint4 a = *reinterpret_cast<const uint4*>(base), b = *reinterpret_cast<const uint4*>(base + 16);
-        w[0] = a.x;
-        w[1] = a.y;
-        w[2] = a.z;
-        w[3] = a.w;
-        w[4] = b.x;
-        w[5] = b.y;
-        w[6] = b.z;
-        w[7] = b.w;
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
-        const int bits = (s & 3) * 8;
-        return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-    }
-    // At the matrix's ends the aligned pieces may reach out of it.
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (elem_bytes == 4) {
-            w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-        } else if (elem_bytes == 2) {
-            const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
-            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 16;
-        } else {
-            const uint8_t* q = reinterpret_cast<const uint8_t*>(p) + 4 * i;
-            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 8 | static_cast<uint32_t>(q[2]) << 16 |
-                   static_cast<uint32_t>(q[3]) << 24;
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
+// for a piece is unaligned16's.
 // Piece c of a row of `bytes` (16 at least) that is written at `row`: the bytes
 // [from, to) of the row, which may be none, and the 16 bytes of the row, from
 // `window` on, that hold them.
@@ -349,7 +372,7 @@ struct DispatchArgs {
     float* out_scales;
     int64_t scale_row, scale_block, out_scale_row, out_scale_block;
     int32_t blocks;                           // scales a row
-    uint32_t row_grid;                        // blocks of the launch that move rows; the rest move scales
+    uint32_t scale_grid;                      // blocks of the launch that move scales, before those for rows
     int32_t row_bytes, elem_bytes;
     int64_t near_tokens, step_tokens;         // what a thread advances by: to its next piece of
     int32_t near_pieces, step_pieces;         // the block's, and from past the last to the next round
@@ -357,14 +380,14 @@ struct DispatchArgs {
 
 constexpr int kMoveThreads = 256;
 
-// Scales of 8-bit rows, by the blocks of a launch past those that move rows:
-// neighbours along whichever of rows and blocks lies together in the output.
+// Scales of 8-bit rows, by the first blocks of a launch (behind those that move
+// rows they would end later: 8192 x 4 rows of 4096 e4m3 32.1 us against 28.2): neighbours
+// along whichever of rows and blocks lies together in the output.
 __device__ __forceinline__ void dispatch_scales(const DispatchArgs& a) {
     const int64_t n = a.tokens * a.blocks;
-    const int64_t step = static_cast<int64_t>(gridDim.x - a.row_grid) * kMoveThreads;
+    const int64_t step = static_cast<int64_t>(a.scale_grid) * kMoveThreads;
     const bool along = a.out_scale_block == 1;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x - a.row_grid) * kMoveThreads + threadIdx.x; i < n;
-         i += step) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; i < n; i += step) {
         const int64_t t = along ? i / a.blocks : i % a.tokens;
         const int64_t b = along ? i - t * a.blocks : i / a.tokens;
         const float s = a.scales[t * a.scale_row + b * a.scale_block];
@@ -381,10 +404,11 @@ template <int K, int U>
 __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const DispatchArgs a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    if (blockIdx.x >= a.row_grid) return dispatch_scales(a);
+    if (blockIdx.x < a.scale_grid) return dispatch_scales(a);
+    const int64_t block = blockIdx.x - a.scale_grid;
     // A block takes U kMoveThreads pieces that lie together, then the same
     // gridDim.x times as far.
-    Place at(static_cast<int64_t>(blockIdx.x) * (U * kMoveThreads) + threadIdx.x, a.pieces);
+    Place at(block * (U * kMoveThreads) + threadIdx.x, a.pieces);
     while (at.token < a.tokens) {
         uint4 v[U];
         int32_t row[U][K], piece[U];
@@ -419,8 +443,9 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const DispatchAr
 __global__ void __launch_bounds__(kMoveThreads) dispatch_odd_kernel(const DispatchArgs a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    if (blockIdx.x >= a.row_grid) return dispatch_scales(a);
-    const Place at(static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x, a.pieces);
+    if (blockIdx.x < a.scale_grid) return dispatch_scales(a);
+    const int64_t block = blockIdx.x - a.scale_grid;
+    const Place at(block * kMoveThreads + threadIdx.x, a.pieces);
     const int64_t pair = at.token, token = pair / a.k;
     if (token >= a.tokens) return;
     const int32_t row = a.slots[token * a.ld_slots + (pair - token * a.k)];
@@ -676,134 +701,115 @@ __global__ void __launch_bounds__(kRingBlock) combine_ring_kernel(const CombineA
     }
 }
 
-// drows[slots[t][j]] = w[t][j] dy[t] and dw[t][j] = dy[t] . rows[slots[t][j]]: dy's
-// row is read once for all choices, and every expert row as its gradient is
-// written.  A token's threads are a power of two within a warp, or whole warps.
-// ODD: rows that start anywhere, in pieces of each choice's row of drows.
+// drows[slots[t][j]] = w[t][j] dy[t] and dw[t][j] = dy[t] . rows[slots[t][j]], one
+// (token, choice) pair to blockDim.x threads: a power of two within a warp, or
+// whole warps.  A token's pairs are neighbours, so that dy comes from DRAM once.
+// ODD: rows that start anywhere, in pieces of drows' row.
 template <typename T, bool ODD>
 __global__ void __launch_bounds__(512) combine_grad_kernel(const CombineArgs a) {
     using P = Piece<T>;
-    constexpr int K = ODD ? 2 : 4;             // choices at a time
-    constexpr int64_t kSize = sizeof(T);
-    constexpr uint32_t kAll = (1u << P::N) - 1;
-    __shared__ float part[K][16];              // one warp a word, where a token has several
+    constexpr int kSize = sizeof(T);
+    constexpr int U = 2;                       // pieces a thread has in flight
+    __shared__ float part[16];                 // one warp a word, where a pair has several
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const bool live = token < a.tokens;        // (all threads take part in the sums)
-    const T* dy = static_cast<const T*>(a.dy) + token * a.ld_dy;
-    const T* in = static_cast<const T*>(a.in);
-    T* out = static_cast<T*>(a.out);
-    const Extent of_dy = extent_of<T>(a.dy, a.tokens, a.ld_dy, a.cols);
-    const Extent of_in = extent_of<T>(a.in, a.rows, a.ld_in, a.cols);
-    for (int j0 = 0; j0 < a.k; j0 += K) {
-        int32_t row[K];
-        uint32_t bits[K];
-        float w[K], dot[K];
-        load_weights<K>(a, token, j0, live, bits);
-        load_slots<K>(a.slots, a.ld_slots, token, j0, a.k, live, row);
+    const int64_t pair = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t token = pair / a.k;
+    const int j = static_cast<int>(pair - token * a.k);
+    const bool live = token < a.tokens;        // (all threads take part in the sum)
+    int32_t row[1];
+    uint32_t bits[1];
+    load_weights<1>(a, token, j, live, bits);
+    load_slots<1>(a.slots, a.ld_slots, token, j, a.k, live, row);
+    float dot = 0.0f;
+    if (names(row[0], a.rows)) {
+        const T* dy = static_cast<const T*>(a.dy) + token * a.ld_dy;
+        const T* from = static_cast<const T*>(a.in) + row[0] * a.ld_in;
+        T* to = static_cast<T*>(a.out) + row[0] * a.ld_out;
+        const float w = weight_of(a, bits[0]);
+        const int32_t bytes = static_cast<int32_t>(a.cols * kSize);
+        if (ODD && bytes < 16) {               // a row of less than a piece: its first thread's
+            for (int i = threadIdx.x == 0 ? 0 : 16; i < a.cols; ++i) {
+                const float d = to_float(dy[i]);
+                dot = fmaf(d, to_float(from[i]), dot);
+                to[i] = from_float<T>(d * w);
+            }
+        } else {
+            const Extent of_dy = extent_of<T>(a.dy, a.tokens, a.ld_dy, a.cols);
+            const Extent of_in = extent_of<T>(a.in, a.rows, a.ld_in, a.cols);
+            for (int32_t p0 = threadIdx.x; p0 < a.pieces; p0 += U * static_cast<int32_t>(blockDim.x)) {
+                uint4 g[U], q[U];
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            if (!names(row[j], a.rows)) row[j] = -1;
-            w[j] = weight_of(a, bits[j]);
-            dot[j] = 0.0f;
-        }
-        if (ODD && a.cols * kSize < 16) {      // a row of less than a piece: its first thread's
-            if (live && threadIdx.x == 0)
-                for (int64_t i = 0; i < a.cols; ++i)
-#pragma unroll
-                    for (int j = 0; j < K; ++j)
-                        if (row[j] >= 0) {
-                            const float d = to_float(dy[i]);
-                            dot[j] = fmaf(d, to_float(in[row[j] * a.ld_in + i]), dot[j]);
-                            out[row[j] * a.ld_out + i] = from_float<T>(d * w[j]);
-                        }
-        } else if (live)
-            for (int32_t piece = threadIdx.x; piece < a.pieces; piece += blockDim.x) {
-                uint4 g[ODD ? K : 1], p[K];
-                int64_t c[K];
-                uint32_t has[K];               // the elements of a piece, by bits
-                if constexpr (!ODD) g[0] = *reinterpret_cast<const uint4*>(dy + static_cast<int64_t>(piece) * P::N);
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    has[j] = row[j] >= 0 ? kAll : 0u;
-                    c[j] = static_cast<int64_t>(piece) * P::N;
-                    if (row[j] < 0) continue;
-                    const T* from = in + row[j] * a.ld_in;
+                for (int u = 0; u < U; ++u) {
+                    const int32_t piece = p0 + u * static_cast<int32_t>(blockDim.x);
+                    if (piece >= a.pieces) continue;
                     if constexpr (ODD) {
-                        const Cut cut(out + row[j] * a.ld_out, static_cast<int32_t>(a.cols * kSize), piece);
-                        has[j] = 0;
+                        const Cut cut(to, bytes, piece);
+                        const char* d = reinterpret_cast<const char*>(dy) + cut.window;
+                        const char* f = reinterpret_cast<const char*>(from) + cut.window;
                         if (cut.none()) continue;
-                        c[j] = cut.window / kSize;
-#pragma unroll
-                        for (int i = 0; i < P::N; ++i)
-                            has[j] |= cut.has(i * static_cast<int>(kSize)) ? 1u << i : 0u;
-                        g[j] = unaligned16(reinterpret_cast<const char*>(dy + c[j]), of_dy, sizeof(T));
-                        p[j] = unaligned16(reinterpret_cast<const char*>(from + c[j]), of_in, sizeof(T));
+                        g[u] = unaligned16(d, of_dy, kSize);
+                        q[u] = unaligned16(f, of_in, kSize);
                     } else {
-                        p[j] = *reinterpret_cast<const uint4*>(from + c[j]);
+                        g[u] = reinterpret_cast<const uint4*>(dy)[piece];
+                        q[u] = reinterpret_cast<const uint4*>(from)[piece];
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < K; ++j)
-                    if (has[j]) {
-                        float d[P::N], v[P::N], o[P::N];
-                        P::widen(g[ODD ? j : 0], d);
-                        P::widen(p[j], v);
-                        T* to = out + row[j] * a.ld_out + c[j];
+                for (int u = 0; u < U; ++u) {
+                    const int32_t piece = p0 + u * static_cast<int32_t>(blockDim.x);
+                    const Cut cut(to, bytes, piece);
+                    if (piece >= a.pieces || (ODD && cut.none())) continue;
+                    float d[P::N], v[P::N], o[P::N];
+                    P::widen(g[u], d);
+                    P::widen(q[u], v);
 #pragma unroll
-                        for (int i = 0; i < P::N; ++i) {
-                            const float f = fmaf(d[i], v[i], dot[j]);
-                            dot[j] = !ODD || has[j] >> i & 1 ? f : dot[j];
-                            o[i] = d[i] * w[j];
-                        }
-                        if (!ODD || has[j] == kAll) {
-                            P::store(to, o);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < P::N; ++i)
-                                if (has[j] >> i & 1) to[i] = from_float<T>(o[i]);
-                        }
+                    for (int i = 0; i < P::N; ++i) {
+                        const float f = fmaf(d[i], v[i], dot);
+                        dot = !ODD || cut.has(i * kSize) ? f : dot;
+                        o[i] = d[i] * w;
                     }
+                    if (!ODD) {
+                        P::store(to + static_cast<int64_t>(piece) * P::N, o);
+                    } else if (cut.whole()) {
+                        P::store(to + cut.window / kSize, o);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < P::N; ++i)
+                            if (cut.has(i * kSize)) to[cut.window / kSize + i] = from_float<T>(o[i]);
+                    }
+                }
             }
-        const int lanes = min(32, static_cast<int>(blockDim.x));
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-            for (int d = lanes >> 1; d >= 1; d >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d);
-        if (blockDim.x > 32) {                 // then blockDim.y == 1
-            const int warps = blockDim.x >> 5;
-            if ((threadIdx.x & 31) == 0)
-#pragma unroll
-                for (int j = 0; j < K; ++j) part[j][threadIdx.x >> 5] = dot[j];
-            __syncthreads();
-            if (threadIdx.x < K && j0 + static_cast<int>(threadIdx.x) < a.k) {
-                float s = 0.0f;
-                for (int i = 0; i < warps; ++i) s += part[threadIdx.x][i];
-                a.dweights[token * a.ld_dweights + j0 + threadIdx.x] = s;
-            }
-            __syncthreads();
-        } else if (live && threadIdx.x == 0) {
-#pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (j0 + j < a.k) a.dweights[token * a.ld_dweights + j0 + j] = dot[j];
         }
     }
+    const int lanes = min(32, static_cast<int>(blockDim.x));
+    for (int d = lanes >> 1; d >= 1; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (blockDim.x > 32) {                     // then blockDim.y == 1
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i) dot += part[i];
+    }
+    if (live && threadIdx.x == 0) a.dweights[token * a.ld_dweights + j] = dot;
 }
 
-// The same over many tokens, in pieces of 16 bytes, one to a thread: blockDim.x
+// The same over many tokens, in pieces of 16 bytes, V to a thread: blockDim.x
 // threads a token (whole warps), blockDim.y tokens at a time, the next S - 1
-// tokens' rows on their way into shared memory.
-template <typename T, int K, int S>
+// tokens' rows on their way into shared memory.  Each row of drows is written as
+// its row is read, dy is read once for all K choices.
+template <typename T, int K, int V, int S>
 __global__ void __launch_bounds__(kRingBlock) combine_grad_ring_kernel(const CombineArgs a) {
     using P = Piece<T>;
-    constexpr int STAGE = (K + 1) * kRingBlock;
+    constexpr int STAGE = (K + 1) * V * kRingBlock;
     constexpr int KK = K <= 2 ? K : K <= 4 ? 4 : 8;            // the power of two from K on
     extern __shared__ uint4 ring_smem[];
     __shared__ float parts[8][2][16 * KK];                     // of tokens of several warps: [turn][warp][KK]
     uint4* const ring = ring_smem + threadIdx.y * blockDim.x + threadIdx.x;
     const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
-    const int c = tid * P::N;
-    const bool mine = tid < a.pieces;
+    const int c = tid * P::N, step = static_cast<int>(blockDim.x) * P::N;
+    bool mine[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) mine[v] = v * static_cast<int>(blockDim.x) + tid < a.pieces;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
@@ -814,13 +820,18 @@ __global__ void __launch_bounds__(kRingBlock) combine_grad_ring_kernel(const Com
         load_slots<K>(a.slots, a.ld_slots, t, 0, a.k, t < a.tokens, row);
     };
     auto fetch = [&](int stage, const int32_t (&row)[K]) {      // the token `ahead`
-        if (mine && ahead < a.tokens) {
-            uint4* to = ring + stage * STAGE;
-            ptx::cp_async_16(to, static_cast<const T*>(a.dy) + ahead * a.ld_dy + c);
+        if (ahead < a.tokens) {
+            const T* dy = static_cast<const T*>(a.dy) + ahead * a.ld_dy + c;
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (names(row[j], a.rows))
-                    ptx::cp_async_16(to + (j + 1) * kRingBlock, in + row[j] * a.ld_in);
+            for (int v = 0; v < V; ++v) {
+                if (!mine[v]) continue;
+                uint4* to = ring + stage * STAGE + v * kRingBlock;
+                ptx::cp_async_16(to, dy + v * step);
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (names(row[j], a.rows))
+                        ptx::cp_async_16(to + (j + 1) * V * kRingBlock, in + row[j] * a.ld_in + v * step);
+            }
         }
         ptx::cp_async_commit();
         ahead += stride;
@@ -856,8 +867,10 @@ __global__ void __launch_bounds__(kRingBlock) combine_grad_ring_kernel(const Com
         float dot[KK];
 #pragma unroll
         for (int j = 0; j < KK; ++j) dot[j] = 0.0f;
-        if (mine) {
-            const uint4* from = ring + stage * STAGE;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (!mine[v]) continue;
+            const uint4* from = ring + stage * STAGE + v * kRingBlock;
             float d[P::N];
             P::widen(from[0], d);
 #pragma unroll
@@ -865,13 +878,13 @@ __global__ void __launch_bounds__(kRingBlock) combine_grad_ring_kernel(const Com
                 if (names(row[j], a.rows)) {
                     const float f = weight_of(a, w[j]);
                     float e[P::N], o[P::N];
-                    P::widen(from[(j + 1) * kRingBlock], e);
+                    P::widen(from[(j + 1) * V * kRingBlock], e);
 #pragma unroll
                     for (int i = 0; i < P::N; ++i) {
                         dot[j] = fmaf(d[i], e[i], dot[j]);
                         o[i] = d[i] * f;
                     }
-                    P::store(out + row[j] * a.ld_out, o);
+                    P::store(out + row[j] * a.ld_out + v * step, o);
                 }
         }
         float x = fold<KK, K>(dot);            // lane l: the warp's sum of choice l % KK
@@ -891,19 +904,20 @@ __global__ void __launch_bounds__(kRingBlock) combine_grad_ring_kernel(const Com
     }
 }
 
-// Threads a token and tokens a block: a power of two lanes for rows of a few
-// pieces, else whole warps.
-dim3 token_block(int64_t pieces) {
-    if (pieces <= 32) {
+// Threads a pair (two pieces or so each) and pairs a block: a power of two lanes
+// for rows of a few pieces, else whole warps.
+dim3 pair_block(int64_t pieces) {
+    const int64_t want = (pieces + 1) / 2;
+    if (want <= 32) {
         unsigned lanes = 1;
-        while (lanes < pieces) lanes *= 2;
+        while (lanes < want) lanes *= 2;
         return dim3(lanes, 256 / lanes);
     }
-    const int64_t rounds = (pieces + 511) / 512;
-    return dim3(static_cast<unsigned>(((pieces + rounds - 1) / rounds + 31) / 32 * 32), 1);
+    const int64_t rounds = (want + 511) / 512;
+    return dim3(static_cast<unsigned>(((want + rounds - 1) / rounds + 31) / 32 * 32), 1);
 }
 
-// Blocks that move scales, past those that move rows.
+// Blocks that move scales.
 unsigned scale_grid(const DispatchArgs& a, int sms) {
     if (!a.scales) return 0;
     return static_cast<unsigned>(std::min<int64_t>(
@@ -920,8 +934,9 @@ int launch_dispatch(DispatchArgs a, int sms, cudaStream_t st) {
     a.near_pieces = kMoveThreads % a.pieces;
     a.step_tokens = (grid - 1) * kShare / a.pieces;
     a.step_pieces = static_cast<int32_t>((grid - 1) * kShare % a.pieces);
-    a.row_grid = static_cast<uint32_t>(grid);
-    return launch(dispatch_kernel<K, U>, dim3(a.row_grid + scale_grid(a, sms)), dim3(kMoveThreads), 0, st, a);
+    a.scale_grid = scale_grid(a, sms);
+    return launch(dispatch_kernel<K, U>, dim3(static_cast<unsigned>(grid) + a.scale_grid), dim3(kMoveThreads), 0,
+                  st, a);
 }
 
 int launch_dispatch(DispatchArgs a, bool odd, int sms, cudaStream_t st) {
@@ -929,8 +944,9 @@ int launch_dispatch(DispatchArgs a, bool odd, int sms, cudaStream_t st) {
         a.pieces = static_cast<int32_t>((a.row_bytes + 14) / 16 + 1);
         const int64_t grid = (a.tokens * a.k * a.pieces + kMoveThreads - 1) / kMoveThreads;
         if (grid > 1 << 30) return static_cast<int>(cudaErrorInvalidConfiguration);
-        a.row_grid = static_cast<uint32_t>(grid);
-        return launch(dispatch_odd_kernel, dim3(a.row_grid + scale_grid(a, sms)), dim3(kMoveThreads), 0, st, a);
+        a.scale_grid = scale_grid(a, sms);
+        return launch(dispatch_odd_kernel, dim3(static_cast<unsigned>(grid) + a.scale_grid), dim3(kMoveThreads), 0,
+                      st, a);
     }
     a.pieces = static_cast<int32_t>(a.row_bytes / 16);
     if (a.k == 1) return launch_dispatch<1, 4>(a, sms, st);
@@ -955,39 +971,51 @@ int launch_combine_ring(CombineArgs a, int sms, cudaStream_t st) {
                   std::max(kBytes, exact_smem(PER)), st, a);
 }
 
-template <typename T, int K, int S, int PER>
+template <typename T, int K, int V, int S, int PER>
 int launch_combine_grad_ring(const CombineArgs& a, int sms, cudaStream_t st) {
-    constexpr size_t kBytes = static_cast<size_t>(S) * (K + 1) * kRingBlock * 16;
+    constexpr size_t kBytes = static_cast<size_t>(S) * (K + 1) * V * kRingBlock * 16;
     static_assert(kBytes <= kRingBytesMost && PER * (kBytes + 1024) <= 228 * 1024, "the blocks fit an SM");
     static std::atomic<uint64_t> opted{0};
-    const cudaError_t e = opt_in_smem(combine_grad_ring_kernel<T, K, S>, kRingBytesMost, &opted);
+    const cudaError_t e = opt_in_smem(combine_grad_ring_kernel<T, K, V, S>, kRingBytesMost, &opted);
     if (e != cudaSuccess) return static_cast<int>(e);
-    const unsigned threads = static_cast<unsigned>((a.pieces + 31) / 32 * 32);
+    const unsigned threads = static_cast<unsigned>((a.pieces + 32 * V - 1) / (32 * V) * 32);
     const unsigned tokens = std::max(1u, kRingBlock / threads);
     const unsigned grid = static_cast<unsigned>(
         std::min<int64_t>((a.tokens + tokens - 1) / tokens, static_cast<int64_t>(PER) * sms));
-    return launch(combine_grad_ring_kernel<T, K, S>, dim3(grid), dim3(threads, tokens), kBytes, st, a);
+    return launch(combine_grad_ring_kernel<T, K, V, S>, dim3(grid), dim3(threads, tokens), kBytes, st, a);
 }
 
 template <typename T>
 int launch_combine_grad(CombineArgs a, bool odd, int sms, cudaStream_t st) {
     constexpr int64_t N = Piece<T>::N;
-    // The ring takes tokens of some pieces, one to a thread, where every block has
-    // a few of them (500 x 4 rows of 2048 bf16: 6.4 us against 9.3 without it).
     a.pieces = static_cast<int32_t>(odd ? (a.cols * static_cast<int64_t>(sizeof(T)) + 14) / 16 + 1 : a.cols / N);
-    if (!odd && a.k <= 8 && a.pieces > 16 && a.pieces <= kRingBlock && a.tokens >= 2 * sms) {
-        // With few choices a token is little work: two blocks an SM (32768 rows of
-        // 2048 bf16, k 1: 74 us against 97 with one of twice the stages, k 2
-        // 57.5 against 68; k 4 55.4 against 51.5).
-        if (a.k == 1) return launch_combine_grad_ring<T, 1, 6, 2>(a, sms, st);
-        if (a.k == 2) return launch_combine_grad_ring<T, 2, 4, 2>(a, sms, st);
-        if (a.k == 3) return launch_combine_grad_ring<T, 3, 4, 1>(a, sms, st);
-        if (a.k == 4) return launch_combine_grad_ring<T, 4, 4, 1>(a, sms, st);
-        if (a.k <= 6) return launch_combine_grad_ring<T, 6, 3, 1>(a, sms, st);
-        return launch_combine_grad_ring<T, 8, 2, 1>(a, sms, st);
+    // The ring takes tokens of some pieces where every block has a few of them
+    // (500 x 4 rows of 2048 bf16: 6.4 us against 9.3 without it).  Two pieces a
+    // thread make more of a token's fixed work (16000 rows of 4096 bf16, k 1: 64.8 us
+    // against 75.3; 5333 x 3: 53.9 against 54.9) and take longer rows (4000 x 4 of
+    // 8192: 101 us against 150 without the ring); one leaves room for more stages,
+    // which k 4 is better off with (2048 columns: 51.2 us against 54.1) unless it
+    // leaves threads idle (3000 columns: 44.6 against 38.4), and k 2 does
+    // not care.  Beyond four choices two do not fit.
+    if (!odd && a.k <= 8 && a.pieces > 16 && a.tokens >= 2 * sms) {
+        const int threads = (a.pieces + 31) / 32 * 32;
+        const bool idle = threads <= kRingBlock && kRingBlock / threads * threads < kRingBlock * 7 / 8;
+        const bool two = a.pieces > kRingBlock || a.k == 1 || a.k == 3 || (a.k == 4 && idle);
+        if (two && a.k <= 4 && a.pieces <= 2 * kRingBlock) {
+            if (a.k == 1) return launch_combine_grad_ring<T, 1, 2, 3, 2>(a, sms, st);
+            if (a.k == 2) return launch_combine_grad_ring<T, 2, 2, 4, 1>(a, sms, st);
+            if (a.k == 3) return launch_combine_grad_ring<T, 3, 2, 3, 1>(a, sms, st);
+            return launch_combine_grad_ring<T, 4, 2, 2, 1>(a, sms, st);
+        }
+        if (a.pieces <= kRingBlock) {
+            if (a.k == 2) return launch_combine_grad_ring<T, 2, 1, 4, 2>(a, sms, st);
+            if (a.k == 4) return launch_combine_grad_ring<T, 4, 1, 4, 1>(a, sms, st);
+            if (a.k <= 6) return launch_combine_grad_ring<T, 6, 1, 3, 1>(a, sms, st);
+            return launch_combine_grad_ring<T, 8, 1, 2, 1>(a, sms, st);
+        }
     }
-    const dim3 block = token_block(a.pieces);
-    const dim3 grid(static_cast<unsigned>((a.tokens + block.y - 1) / block.y));
+    const dim3 block = pair_block(a.pieces);
+    const dim3 grid(static_cast<unsigned>((a.tokens * a.k + block.y - 1) / block.y));
     return odd ? launch(combine_grad_kernel<T, true>, grid, block, 0, st, a)
                : launch(combine_grad_kernel<T, false>, grid, block, 0, st, a);
 }
@@ -1138,15 +1166,18 @@ int tiles_expert_sort(const tiles_expert_sort_desc* d, void* ws, size_t ws_bytes
             return fail(TILES_ERR_INVALID_ARG, "experts: row pitch smaller than the row length");
     }
     const size_t need = sort_bytes(pairs, d->groups);
-    if (!ws || ws_bytes < need)
+    if (need > kConvMinWorkspaceBytes && (!ws || ws_bytes < need))
         return fail(TILES_ERR_INVALID_ARG, "the sort needs %zu workspace bytes", need);
     if (reinterpret_cast<uintptr_t>(ws) & 15u)
         return fail(TILES_ERR_MISALIGNED, "the workspace must be 16-byte aligned");
+    const SortGeometry g = sort_geometry(pairs, d->groups);
+    char* const room = g.blocks > 1 ? static_cast<char*>(ws) + kConvMinWorkspaceBytes : nullptr;
+    int32_t* const below = g.scan ? reinterpret_cast<int32_t*>(room + sort_counts_bytes(g, d->groups)) : nullptr;
     const SortArgs a{d->experts, d->tokens > 1 ? d->ld : d->k, static_cast<uint32_t>(pairs),
                      static_cast<uint32_t>(d->k), static_cast<int32_t>(d->groups),
                      d->index_bytes == 8, d->slots, d->offsets, d->order,
-                     reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes)};
-    const SortGeometry g = sort_geometry(pairs, d->groups);
+                     reinterpret_cast<uint16_t*>(room), below,
+                     below ? below + static_cast<int64_t>(g.blocks) * d->groups : nullptr};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int e;
     switch (g.items) {

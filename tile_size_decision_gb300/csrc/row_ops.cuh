@@ -236,6 +236,54 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* slot, int turn) {
     }
 }
 
+// The bytes of what is read.
+struct Extent {
+    const char* from;
+    const char* to;                           // past the last
+};
+
+// 16 bytes that start on any element, inside the extent: put together from the two
+// aligned pieces that hold them.
+__device__ __forceinline__ uint4 unaligned16(const char* p, const Extent& e, int elem_bytes) {
+    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+    const char* base = p - s;
+    if (s == 0) return *reinterpret_cast<const uint4*>(p);
+    uint32_t w[8];
+    if (base >= e.from && base + 32 <= e.to) {
+        const uint4 a = *reinterpret_cast<const uint4*>(base), b = *reinterpret_cast<const uint4*>(base + 16);
+        w[0] = a.x;
+        w[1] = a.y;
+        w[2] = a.z;
+        w[3] = a.w;
+        w[4] = b.x;
+        w[5] = b.y;
+        w[6] = b.z;
+        w[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+        const int bits = (s & 3) * 8;
+        return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+    }
+    // At the ends the aligned pieces may reach out of the extent.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (elem_bytes == 4) {
+            w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        } else if (elem_bytes == 2) {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 16;
+        } else {
+            const uint8_t* q = reinterpret_cast<const uint8_t*>(p) + 4 * i;
+            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 8 | static_cast<uint32_t>(q[2]) << 16 |
+                   static_cast<uint32_t>(q[3]) << 24;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Lane l's share of the warp's sums of s[0 .. N): that of s[l % N].  Each exchange
 // halves what a lane is responsible for; of the N values the last N - USED
 // are zeros.

@@ -487,12 +487,13 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // stream's pool (call under OnStream), which goes back there when the call is
 // made: whatever takes it next on the stream runs after the call's kernels.
 struct Scratch {
+    static constexpr size_t kHeader = 256;
     Workspace given;
     at::Tensor own;
 
     Scratch(PyObject* o, size_t bytes, const at::Tensor& like) : given(o) {
         require(bytes > 0);
-        if (given.at) return;
+        if (given.at || bytes <= kHeader) return;  // no more than the header: nothing is used
         own = empty(like, {static_cast<int64_t>(bytes)}, {1}, at::ScalarType::Byte);
         given.at = own.data_ptr();
         given.bytes = bytes;
