@@ -15,7 +15,7 @@ namespace {
 // Tensors a launch takes: their descriptions travel with it as arguments (4 KB),
 // so that nothing on the host has to outlive the call and a captured launch
 // carries them.
-constexpr int kTensors = 120;
+constexpr int kTensors = 120, kFewTensors = 16;
 constexpr int kClipThreads = 256;
 constexpr int kMostBlocksPerSm = 8;
 
@@ -25,6 +25,7 @@ struct Tensor {
     int64_t count;
 };
 
+template <int N>
 struct TensorBatch {
     int32_t tensors;
     uint32_t chunks;
@@ -33,11 +34,11 @@ struct TensorBatch {
     uint32_t once;                             // chunks before this one are not read again soon
     double* partials;                          // this launch's first, or (scaling) the very first
     float* norm;
-    uint32_t chunks_before[kTensors];          // of the launch's tensors before each
-    uint8_t dtype[kTensors];
-    Tensor at[kTensors];
+    uint32_t chunks_before[N];                 // of the launch's tensors before each
+    uint8_t dtype[N];
+    Tensor at[N];
 };
-static_assert(sizeof(TensorBatch) <= 4096, "arguments of one launch");
+static_assert(sizeof(TensorBatch<kTensors>) <= 4096, "arguments of one launch");
 
 // A tensor is seen as 16-byte pieces that start on 16 bytes, of which its first
 // and last may hold other memory too; U pieces a thread are a chunk, what a
@@ -62,7 +63,8 @@ __device__ __forceinline__ void widen_piece(const uint4& q, float (&v)[16 / size
 }
 
 // The tensor that chunk c is of: the last one that starts at c or before.
-__device__ __forceinline__ int tensor_of(const TensorBatch& a, uint32_t c) {
+template <int N>
+__device__ __forceinline__ int tensor_of(const TensorBatch<N>& a, uint32_t c) {
     int lo = 0, n = a.tensors;
     while (n > 1) {
         const int half = n / 2;
@@ -180,8 +182,9 @@ __device__ __forceinline__ double block_sum(double s) {
 
 // One partial sum a block, over the chunks blockIdx.x, + gridDim.x, ...  256
 // million bf16 elements 78 us with the norm: 98% of the measured copy bandwidth.
-template <int U>
-__global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8) squares_kernel(const __grid_constant__ TensorBatch a) {
+template <int U, int N>
+__global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
+    squares_kernel(const __grid_constant__ TensorBatch<N> a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     double s = 0.0;
@@ -197,12 +200,19 @@ __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8) squares_kernel(co
     if (threadIdx.x == 0) a.partials[blockIdx.x] = s;
 }
 
+// The square root of a sum of squares.  In fp32 (whose two roundings are a unit in
+// the last place together) where its range holds the sum: in fp64 it takes this
+// chip a microsecond.
+__device__ __forceinline__ float norm_from(double s) {
+    return s >= 0x1p-120 && s <= 0x1p120 ? sqrtf(static_cast<float>(s)) : static_cast<float>(sqrt(s));
+}
+
 // The norm from all partial sums, in a fixed order (every thread of a block
 // gets it).
 __device__ __forceinline__ float norm_of(const double* partials, int parts) {
     double s = 0.0;
     for (int i = threadIdx.x; i < parts; i += kClipThreads) s += partials[i];
-    return static_cast<float>(sqrt(block_sum(s)));
+    return norm_from(block_sum(s));
 }
 
 __global__ void __launch_bounds__(kClipThreads) norm_kernel(const double* partials, int parts,
@@ -211,6 +221,11 @@ __global__ void __launch_bounds__(kClipThreads) norm_kernel(const double* partia
     ptx::grid_launch_dependents();
     const float n = norm_of(partials, parts);
     if (threadIdx.x == 0) *norm = n;
+}
+
+__device__ __forceinline__ float factor_of(float norm, float max_norm, float eps) {
+    const float under = norm + eps;
+    return under <= max_norm ? 1.0f : max_norm / under;        // a NaN stays one
 }
 
 template <typename T>
@@ -269,19 +284,18 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t first, floa
     for (int64_t b = start, end = min(bytes, start + U * kStep); b < end; b += kStep) scale_piece<T>(t, b, scale);
 }
 
-// Finds the norm, from a few partial sums itself (a launch less; 300,000 elements
-// 6.1 us against 6.3) or where norm_kernel left it (parts < 0; 5 million elements
-// in 60 tensors 15.8 us against 26.6), then scales its chunks, the last ones
-// first: those the squares read last, which L2 still holds.  256 million bf16
+// Finds the norm, from a few partial sums itself (a launch less) or where
+// norm_kernel left it (parts < 0; 5 million elements in 60 tensors 15.8 us
+// against 26.6), then scales its chunks, the last ones first: those the squares read last, which L2 still holds.  256 million bf16
 // elements, norm and scaling: 228 us, 1.54 GB at the measured copy bandwidth.
-template <int U>
-__global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8) scale_kernel(const __grid_constant__ TensorBatch a) {
+template <int U, int N>
+__global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
+    scale_kernel(const __grid_constant__ TensorBatch<N> a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const float norm = a.parts < 0 ? *a.norm : norm_of(a.partials, a.parts);
     if (a.parts >= 0 && a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-    const float under = norm + a.eps;
-    const float scale = under <= a.max_norm ? 1.0f : a.max_norm / under;   // a NaN stays one
+    const float scale = factor_of(norm, a.max_norm, a.eps);
     for (uint32_t i = blockIdx.x; i < a.chunks; i += gridDim.x) {
         const uint32_t c = a.chunks - 1 - i;
         const int n = tensor_of(a, c);
@@ -294,12 +308,153 @@ __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8) scale_kernel(cons
     }
 }
 
+// Few gradients, at most kHeld pieces a thread of one cluster: they stay in its
+// registers between the norm and the scaling, and one launch does it all
+// (300,000 elements, as a program calls it, 6.8 us against 8.1 with two launches).
+// Neither fp64 nor its square root is done by more than a warp where fp32 holds the
+// sums (with fp64 for every thread 15.8 us).  max_norm < 0: the norm
+// alone.  Every tensor's output starts as far off 16 bytes as its gradient.
+constexpr int kClusterCtas = 8, kClusterThreads = 1024, kHeld = 8;
+
+template <typename T>
+__device__ __forceinline__ float piece_squares(const uint4& q) {
+    float v[16 / sizeof(T)], s = 0.0f;
+    widen_piece<T>(q, v);
+#pragma unroll
+    for (float e : v) s = fmaf(e, e, s);
+    return s;
+}
+
+template <typename T>
+__device__ __forceinline__ double piece_squares_in_double(const uint4& q) {
+    float v[16 / sizeof(T)];
+    widen_piece<T>(q, v);
+    double s = 0.0;
+    for (float e : v) s += static_cast<double>(e) * static_cast<double>(e);
+    return s;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kClusterThreads)
+    clip_cluster_kernel(const __grid_constant__ TensorBatch<N> a) {
+    // A chunk of the block: the tensor's memory, where the chunk starts in it, and
+    // the tensor's bytes (none: no chunk).
+    struct Chunk {
+        const char* from;
+        char* to;
+        int64_t start, bytes;
+        int dtype;
+    };
+    __shared__ Chunk chunks[kHeld];
+    __shared__ double warp_sums[kClusterThreads / 32], total;
+    __shared__ float factor;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid < kHeld) {
+        const uint32_t c = rank + tid * kClusterCtas;
+        Chunk k{nullptr, nullptr, 0, 0, 0};
+        if (c < a.chunks) {
+            const int n = tensor_of(a, c);
+            const Tensor& t = a.at[n];
+            k = {static_cast<const char*>(t.from), static_cast<char*>(t.to),
+                 static_cast<int64_t>(c - a.chunks_before[n]) * (kClusterThreads * 16) - misaligned(t.from),
+                 t.count * (a.dtype[n] == TILES_F32 ? 4 : 2), a.dtype[n]};
+        }
+        chunks[tid] = k;
+    }
+    __syncthreads();
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    uint4 q[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const Chunk& k = chunks[i];
+        const int64_t b = k.start + tid * 16;
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (b >= 0 && b + 16 <= k.bytes)
+            q[i] = *reinterpret_cast<const uint4*>(k.from + b);
+        else if (b < k.bytes)
+            q[i] = k.dtype == TILES_F32
+                       ? partial_piece(reinterpret_cast<const float*>(k.from), b, k.bytes / 4)
+                       : partial_piece(reinterpret_cast<const __half*>(k.from), b, k.bytes / 2);
+    }
+    // As in chunk_squares, with the warp's sum in fp32 too where it fits.
+    float s32 = 0.0f;
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int dtype = chunks[i].dtype;
+        any |= (q[i].x | q[i].y | q[i].z | q[i].w) & (dtype == TILES_F32 ? 0x7fffffffu : 0x7fff7fffu);
+        s32 += dtype == TILES_BF16  ? piece_squares<__nv_bfloat16>(q[i])
+               : dtype == TILES_F16 ? piece_squares<__half>(q[i])
+                                    : piece_squares<float>(q[i]);
+    }
+    const bool fits = any == 0 || (s32 >= kSmallSquares && s32 <= FLT_MAX / 64);
+    double s = 0.0;
+    if (__all_sync(0xffffffffu, fits)) {
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) s32 += __shfl_xor_sync(0xffffffffu, s32, d);
+        s = static_cast<double>(s32);
+    } else {
+        for (int i = 0; i < kHeld; ++i) {
+            const int dtype = chunks[i].dtype;
+            s += dtype == TILES_BF16  ? piece_squares_in_double<__nv_bfloat16>(q[i])
+                 : dtype == TILES_F16 ? piece_squares_in_double<__half>(q[i])
+                                      : piece_squares_in_double<float>(q[i]);
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    }
+    if (lane == 0) warp_sums[tid >> 5] = s;
+    __syncthreads();
+    if (tid < 32) {
+        s = warp_sums[lane];
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (lane == 0) total = s;
+    }
+    ptx::cluster_sync();
+    if (tid < 32) {
+        s = ptx::ld_shared_cluster_f64(ptx::map_to_cta(ptx::smem_addr(&total), lane % kClusterCtas));
+#pragma unroll
+        for (int d = kClusterCtas / 2; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        const float norm = norm_from(s);
+        if (tid == 0) {
+            if (rank == 0) *a.norm = norm;
+            factor = factor_of(norm, a.max_norm, a.eps);
+        }
+    }
+    ptx::cluster_arrive();                     // the others' totals are read; no block may leave before that
+    __syncthreads();
+    const float scale = factor;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const Chunk& k = chunks[i];
+        const int64_t b = k.start + tid * 16;
+        if (a.max_norm < 0.0f || b >= k.bytes || (scale == 1.0f && k.to == k.from)) continue;
+        const uint4 o = k.dtype == TILES_BF16  ? scaled<__nv_bfloat16>(q[i], scale)
+                        : k.dtype == TILES_F16 ? scaled<__half>(q[i], scale)
+                                               : scaled<float>(q[i], scale);
+        if (b >= 0 && b + 16 <= k.bytes) {
+            *reinterpret_cast<uint4*>(k.to + b) = o;
+            continue;
+        }
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)            // in 16 bits, of either type
+            if (b + 2 * e >= 0 && b + 2 * e < k.bytes)
+                *reinterpret_cast<uint16_t*>(k.to + b + 2 * e) = static_cast<uint16_t>(w[e / 2] >> 16 * (e & 1));
+    }
+    ptx::cluster_wait();
+}
+
 // A run of tensors that one launch takes: [first, last) of the caller's, those
 // without elements left out.
 struct Run { int64_t first, last; };
 
 // `written`: in pieces of what is written, not of what is read.
-void fill_batch(TensorBatch* b, const tiles_grad_tensor* t, Run r, int chunk_pieces, bool written) {
+template <int N>
+void fill_batch(TensorBatch<N>* b, const tiles_grad_tensor* t, Run r, int chunk_pieces, bool written) {
     b->tensors = 0;
     b->chunks = 0;
     const int64_t chunk = static_cast<int64_t>(chunk_pieces) * 16;
@@ -319,8 +474,8 @@ void fill_batch(TensorBatch* b, const tiles_grad_tensor* t, Run r, int chunk_pie
 
 template <int U> constexpr int kBlocksPerSm = U > 4 ? 4 : 8;
 
-template <int U>
-int run_blocks(const TensorBatch& b, int sms) {
+template <int U, int N>
+int run_blocks(const TensorBatch<N>& b, int sms) {
     return static_cast<int>(std::min<int64_t>(b.chunks, static_cast<int64_t>(sms) * kBlocksPerSm<U>));
 }
 
@@ -396,33 +551,33 @@ constexpr int64_t kKeptBytes = 100000000;
 
 // The launches of the squares; the number of partial sums they leave.  `again`:
 // the gradients are read again.
-template <int U>
+template <int U, int N>
 int launch_squares(const tiles_grad_tensor* t, int64_t n, bool again, double* partials, int sms, int* parts,
                    cudaStream_t st) {
-    TensorBatch b{};
+    TensorBatch<N> b{};
     *parts = 0;
     constexpr int64_t kChunk = kChunkPieces<U> * 16;
     int64_t left = again ? total_bytes(t, n) : 0;
-    for (int64_t i = 0; i < n; i += kTensors) {
-        fill_batch(&b, t, {i, std::min<int64_t>(n, i + kTensors)}, kChunkPieces<U>, false);
+    for (int64_t i = 0; i < n; i += N) {
+        fill_batch(&b, t, {i, std::min<int64_t>(n, i + N)}, kChunkPieces<U>, false);
         if (b.chunks == 0) continue;
         b.partials = partials + *parts;
         b.once = static_cast<uint32_t>(
             std::min<int64_t>(b.chunks, std::max<int64_t>(0, left - kKeptBytes) / kChunk));
         left -= b.chunks * kChunk;
         const int blocks = run_blocks<U>(b, sms);
-        const int e = launch(squares_kernel<U>, dim3(blocks), dim3(kClipThreads), 0, st, b);
+        const int e = launch(squares_kernel<U, N>, dim3(blocks), dim3(kClipThreads), 0, st, b);
         if (e != cudaSuccess) return e;
         *parts += blocks;
     }
     return cudaSuccess;
 }
 
-template <int U>
+template <int U, int N>
 int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
                 double* partials, int sms, cudaStream_t st) {
-    TensorBatch b{};
-    int e = launch_squares<U>(t, n, true, partials, sms, &b.parts, st);
+    TensorBatch<N> b{};
+    int e = launch_squares<U, N>(t, n, true, partials, sms, &b.parts, st);
     if (e != cudaSuccess) return e;
     b.partials = partials;
     b.max_norm = max_norm;
@@ -436,16 +591,48 @@ int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps
         if (e != cudaSuccess) return e;
         b.parts = -1;
     }
-    for (int64_t i = (n - 1) / kTensors * kTensors; i >= 0; i -= kTensors) {
-        fill_batch(&b, t, {i, std::min<int64_t>(n, i + kTensors)}, kChunkPieces<U>, true);
+    for (int64_t i = (n - 1) / N * N; i >= 0; i -= N) {
+        fill_batch(&b, t, {i, std::min<int64_t>(n, i + N)}, kChunkPieces<U>, true);
         if (b.chunks == 0) continue;
-        e = launch(scale_kernel<U>, dim3(std::min<uint32_t>(b.chunks, 1u << 30)), dim3(kClipThreads), 0, st, b);
+        e = launch(scale_kernel<U, N>, dim3(std::min<uint32_t>(b.chunks, 1u << 30)), dim3(kClipThreads), 0, st, b);
         if (e != cudaSuccess) return e;
         if (b.parts >= 0) b.norm = nullptr;               // written once
     }
     if (b.parts == 0)                                     // no elements at all
         e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const double*>(partials), 0, norm);
     return e;
+}
+
+// Whether one cluster holds the gradients (and their outputs, if any, start where
+// they do).
+bool cluster_takes(const tiles_grad_tensor* t, int64_t n, bool out) {
+    if (n > kTensors) return false;
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (t[i].count == 0) continue;
+        if (out && t[i].out && misaligned(t[i].out) != misaligned(t[i].grad)) return false;
+        if (t[i].count > kHeld * kClusterCtas * kClusterThreads * 8) return false;
+        const int64_t bytes = t[i].count * dtype_bytes(t[i].dtype) + misaligned(t[i].grad);
+        chunks += (bytes + kClusterThreads * 16 - 1) / (kClusterThreads * 16);
+    }
+    return chunks <= kHeld * kClusterCtas;
+}
+
+template <int N>
+int launch_cluster_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
+                        cudaStream_t st) {
+    TensorBatch<N> b{};
+    fill_batch(&b, t, {0, n}, kClusterThreads, false);
+    b.max_norm = max_norm;
+    b.eps = eps;
+    b.norm = norm;
+    return launch_cluster(clip_cluster_kernel<N>, kClusterCtas, dim3(kClusterCtas), dim3(kClusterThreads), 0, st, b);
+}
+
+int launch_cluster_clip_any(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
+                            cudaStream_t st) {
+    return n <= kFewTensors ? launch_cluster_clip<kFewTensors>(t, n, max_norm, eps, norm, st)
+                            : launch_cluster_clip<kTensors>(t, n, max_norm, eps, norm, st);
 }
 
 // Pieces a thread: small gradients are spread over more blocks.
@@ -479,8 +666,10 @@ int tiles_grad_norm(const tiles_grad_tensor* t, int64_t n, float* norm, void* ws
     double* partials = reinterpret_cast<double*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int parts = 0;
-    int e = few_bytes(t, n, sms) ? launch_squares<2>(t, n, false, partials, sms, &parts, st)
-                                 : launch_squares<8>(t, n, false, partials, sms, &parts, st);
+    if (cluster_takes(t, n, false))
+        return launch_status(launch_cluster_clip_any(t, n, -1.0f, 0.0f, norm, st), "gradient norm");
+    int e = few_bytes(t, n, sms) ? launch_squares<2, kTensors>(t, n, false, partials, sms, &parts, st)
+                                 : launch_squares<8, kTensors>(t, n, false, partials, sms, &parts, st);
     if (e == cudaSuccess)
         e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const double*>(partials), parts, norm);
     return launch_status(e, "gradient norm");
@@ -497,8 +686,9 @@ int tiles_clip_grads(const tiles_grad_tensor* t, int64_t n, float max_norm, floa
     if ((s = check_clip_workspace(ws, ws_bytes, n, sms)) != TILES_OK) return s;
     double* partials = reinterpret_cast<double*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int e = few_bytes(t, n, sms) ? launch_clip<2>(t, n, max_norm, eps, norm, partials, sms, st)
-                                       : launch_clip<8>(t, n, max_norm, eps, norm, partials, sms, st);
+    const int e = cluster_takes(t, n, true) ? launch_cluster_clip_any(t, n, max_norm, eps, norm, st)
+                  : few_bytes(t, n, sms)    ? launch_clip<2, kTensors>(t, n, max_norm, eps, norm, partials, sms, st)
+                                            : launch_clip<8, kTensors>(t, n, max_norm, eps, norm, partials, sms, st);
     return launch_status(e, "gradient clipping");
 }
 
