@@ -14,7 +14,7 @@ namespace {
 
 // Tensors a launch takes: their descriptions travel with it as arguments (4 KB),
 // so that nothing on the host has to outlive the call and a captured launch
-// carries them.
+// carries them.  (Fewer where there is but one launch, and a short one.)
 constexpr int kTensors = 120, kFewTensors = 16;
 constexpr int kClipThreads = 256;
 constexpr int kMostBlocksPerSm = 8;
@@ -38,7 +38,8 @@ struct TensorBatch {
     uint8_t dtype[N];
     Tensor at[N];
 };
-static_assert(sizeof(TensorBatch<kTensors>) <= 4096, "arguments of one launch");
+using Batch = TensorBatch<kTensors>;
+static_assert(sizeof(Batch) <= 4096, "arguments of one launch");
 
 // A tensor is seen as 16-byte pieces that start on 16 bytes, of which its first
 // and last may hold other memory too; U pieces a thread are a chunk, what a
@@ -182,9 +183,9 @@ __device__ __forceinline__ double block_sum(double s) {
 
 // One partial sum a block, over the chunks blockIdx.x, + gridDim.x, ...  256
 // million bf16 elements 78 us with the norm: 98% of the measured copy bandwidth.
-template <int U, int N>
+template <int U>
 __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
-    squares_kernel(const __grid_constant__ TensorBatch<N> a) {
+    squares_kernel(const __grid_constant__ Batch a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     double s = 0.0;
@@ -286,11 +287,12 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t first, floa
 
 // Finds the norm, from a few partial sums itself (a launch less) or where
 // norm_kernel left it (parts < 0; 5 million elements in 60 tensors 15.8 us
-// against 26.6), then scales its chunks, the last ones first: those the squares read last, which L2 still holds.  256 million bf16
-// elements, norm and scaling: 228 us, 1.54 GB at the measured copy bandwidth.
-template <int U, int N>
+// against 26.6), then scales its chunks, the last ones first: those the squares
+// read last, which L2 still holds.  256 million bf16 elements, norm and scaling:
+// 228 us, 1.54 GB at the measured copy bandwidth.
+template <int U>
 __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
-    scale_kernel(const __grid_constant__ TensorBatch<N> a) {
+    scale_kernel(const __grid_constant__ Batch a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const float norm = a.parts < 0 ? *a.norm : norm_of(a.partials, a.parts);
@@ -309,11 +311,13 @@ __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
 }
 
 // Few gradients, at most kHeld pieces a thread of one cluster: they stay in its
-// registers between the norm and the scaling, and one launch does it all
-// (300,000 elements, as a program calls it, 6.8 us against 8.1 with two launches).
-// Neither fp64 nor its square root is done by more than a warp where fp32 holds the
-// sums (with fp64 for every thread 15.8 us).  max_norm < 0: the norm
-// alone.  Every tensor's output starts as far off 16 bytes as its gradient.
+// registers between the norm and the scaling, and one launch does it all.  As a
+// program calls it 12 tensors of 25,000 elements take 6.8 us against 8.1 with two
+// launches; in a captured graph, where two launches overlap, 12,288 elements 4.7
+// against 5.1, but 524,288, which only eight SMs move, 6.7 against 4.9.  Neither fp64 nor
+// its square root is done by more than a warp where fp32 holds the sums (with fp64
+// for every thread 15.8 us).  max_norm < 0: the norm alone.  Every tensor's output
+// starts as far off 16 bytes as its gradient.
 constexpr int kClusterCtas = 8, kClusterThreads = 1024, kHeld = 8;
 
 template <typename T>
@@ -474,8 +478,8 @@ void fill_batch(TensorBatch<N>* b, const tiles_grad_tensor* t, Run r, int chunk_
 
 template <int U> constexpr int kBlocksPerSm = U > 4 ? 4 : 8;
 
-template <int U, int N>
-int run_blocks(const TensorBatch<N>& b, int sms) {
+template <int U>
+int run_blocks(const Batch& b, int sms) {
     return static_cast<int>(std::min<int64_t>(b.chunks, static_cast<int64_t>(sms) * kBlocksPerSm<U>));
 }
 
@@ -551,33 +555,33 @@ constexpr int64_t kKeptBytes = 100000000;
 
 // The launches of the squares; the number of partial sums they leave.  `again`:
 // the gradients are read again.
-template <int U, int N>
+template <int U>
 int launch_squares(const tiles_grad_tensor* t, int64_t n, bool again, double* partials, int sms, int* parts,
                    cudaStream_t st) {
-    TensorBatch<N> b{};
+    Batch b{};
     *parts = 0;
     constexpr int64_t kChunk = kChunkPieces<U> * 16;
     int64_t left = again ? total_bytes(t, n) : 0;
-    for (int64_t i = 0; i < n; i += N) {
-        fill_batch(&b, t, {i, std::min<int64_t>(n, i + N)}, kChunkPieces<U>, false);
+    for (int64_t i = 0; i < n; i += kTensors) {
+        fill_batch(&b, t, {i, std::min<int64_t>(n, i + kTensors)}, kChunkPieces<U>, false);
         if (b.chunks == 0) continue;
         b.partials = partials + *parts;
         b.once = static_cast<uint32_t>(
             std::min<int64_t>(b.chunks, std::max<int64_t>(0, left - kKeptBytes) / kChunk));
         left -= b.chunks * kChunk;
         const int blocks = run_blocks<U>(b, sms);
-        const int e = launch(squares_kernel<U, N>, dim3(blocks), dim3(kClipThreads), 0, st, b);
+        const int e = launch(squares_kernel<U>, dim3(blocks), dim3(kClipThreads), 0, st, b);
         if (e != cudaSuccess) return e;
         *parts += blocks;
     }
     return cudaSuccess;
 }
 
-template <int U, int N>
+template <int U>
 int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
                 double* partials, int sms, cudaStream_t st) {
-    TensorBatch<N> b{};
-    int e = launch_squares<U, N>(t, n, true, partials, sms, &b.parts, st);
+    Batch b{};
+    int e = launch_squares<U>(t, n, true, partials, sms, &b.parts, st);
     if (e != cudaSuccess) return e;
     b.partials = partials;
     b.max_norm = max_norm;
@@ -591,10 +595,10 @@ int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps
         if (e != cudaSuccess) return e;
         b.parts = -1;
     }
-    for (int64_t i = (n - 1) / N * N; i >= 0; i -= N) {
-        fill_batch(&b, t, {i, std::min<int64_t>(n, i + N)}, kChunkPieces<U>, true);
+    for (int64_t i = (n - 1) / kTensors * kTensors; i >= 0; i -= kTensors) {
+        fill_batch(&b, t, {i, std::min<int64_t>(n, i + kTensors)}, kChunkPieces<U>, true);
         if (b.chunks == 0) continue;
-        e = launch(scale_kernel<U, N>, dim3(std::min<uint32_t>(b.chunks, 1u << 30)), dim3(kClipThreads), 0, st, b);
+        e = launch(scale_kernel<U>, dim3(std::min<uint32_t>(b.chunks, 1u << 30)), dim3(kClipThreads), 0, st, b);
         if (e != cudaSuccess) return e;
         if (b.parts >= 0) b.norm = nullptr;               // written once
     }
@@ -668,8 +672,8 @@ int tiles_grad_norm(const tiles_grad_tensor* t, int64_t n, float* norm, void* ws
     int parts = 0;
     if (cluster_takes(t, n, false))
         return launch_status(launch_cluster_clip_any(t, n, -1.0f, 0.0f, norm, st), "gradient norm");
-    int e = few_bytes(t, n, sms) ? launch_squares<2, kTensors>(t, n, false, partials, sms, &parts, st)
-                                 : launch_squares<8, kTensors>(t, n, false, partials, sms, &parts, st);
+    int e = few_bytes(t, n, sms) ? launch_squares<2>(t, n, false, partials, sms, &parts, st)
+                                 : launch_squares<8>(t, n, false, partials, sms, &parts, st);
     if (e == cudaSuccess)
         e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const double*>(partials), parts, norm);
     return launch_status(e, "gradient norm");
@@ -687,8 +691,8 @@ int tiles_clip_grads(const tiles_grad_tensor* t, int64_t n, float max_norm, floa
     double* partials = reinterpret_cast<double*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int e = cluster_takes(t, n, true) ? launch_cluster_clip_any(t, n, max_norm, eps, norm, st)
-                  : few_bytes(t, n, sms)    ? launch_clip<2, kTensors>(t, n, max_norm, eps, norm, partials, sms, st)
-                                            : launch_clip<8, kTensors>(t, n, max_norm, eps, norm, partials, sms, st);
+                  : few_bytes(t, n, sms)    ? launch_clip<2>(t, n, max_norm, eps, norm, partials, sms, st)
+                                            : launch_clip<8>(t, n, max_norm, eps, norm, partials, sms, st);
     return launch_status(e, "gradient clipping");
 }
 

@@ -325,9 +325,8 @@ struct Ring {
 // The same with the rows' pieces 16-byte aligned: one block an SM, blockDim.y
 // rows at a time (their threads meet at barriers of their own), the next two on
 // their way in.  The sums of one row go together with the mean of the next, so
-// that a row costs one barrier.  16384 x 4096 bf16 rows with residual 86.2 us,
-// 93% of the measured copy bandwidth (to e4m3 80.2); one row at a time without
-// the ring 110.
+// that a row costs one barrier.  16384 x 4096 bf16 rows with residual 83.3 us,
+// 96% of the measured copy bandwidth; one row at a time without the ring 110.
 template <typename T, int VPT, bool FP8, bool RES>
 __global__ void __launch_bounds__(kRows)
     layernorm_ring_kernel(const LayerArgs a) {
@@ -623,7 +622,7 @@ __global__ void __launch_bounds__(512, 2)
 // time (their threads meet at barriers of their own, and add their parts of the
 // gradients in the end), the next two on their way in.  The sums of one row go
 // together with the mean of the next, so that a row costs one barrier.
-// 8192 x 4096 bf16 rows with dh 57 us, the reduction's launch included: 70% of
+// 8192 x 4096 bf16 rows with dh 53.5 us, the reduction's launch included: 75% of
 // the measured copy bandwidth.  The instructions bound it (a vector a thread and
 // twice the threads: 77.6 us; single fp32 additions instead of pairs: 60.6).
 template <typename T, int VPT>

@@ -70,10 +70,6 @@ __global__ void __launch_bounds__(1024) sort_count_kernel(const SortArgs a) {
         a.counts[static_cast<int64_t>(blockIdx.x) * a.groups + g] = static_cast<uint16_t>(count[g]);
 }
 
-// The places of a block's pairs.  A warp takes 32 I consecutive pairs and ranks
-// them among its own of the same expert; the warps' counts, those of the blocks
-// before and the experts' totals then give every pair its row.  Everything
-// is counted, nothing competes: the order is stable, and the same every time.
 // The blocks' counts of every expert to what lies before each block, and the
 // totals: 32 experts a block, whose 32 rows of threads share the column.
 __global__ void __launch_bounds__(1024) sort_scan_kernel(const SortArgs a, int blocks) {
@@ -116,6 +112,10 @@ __host__ __device__ constexpr int rank_pitch(int groups) {
     return (groups + 1) / 2 % 2 ? (groups + 1) / 2 * 2 : (groups + 1) / 2 * 2 + 2;
 }
 
+// The places of a block's pairs.  A warp takes 32 I consecutive pairs and ranks
+// them among its own of the same expert; the warps' counts, those of the blocks
+// before and the experts' totals then give every pair its row.  Everything
+// is counted, nothing competes: the order is stable, and the same every time.
 template <int I>
 __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a) {
     extern __shared__ int start[];             // [groups]: totals, then the first row of the block's pairs
