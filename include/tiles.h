@@ -891,9 +891,10 @@ typedef struct {
 size_t tiles_grad_norm_workspace_bytes(int64_t tensors);
 
 /* *norm = the square root of the sum of all elements' squares (0 without any).
- * The array of tensors is the host's and may go when the call returns.  Squares
- * are fp32 where its range holds them, the sums above a thread's few elements
- * fp64, in a fixed order for given sizes and device. */
+ * At most 2^20 tensors, of 2^40 elements each and 2^46 bytes together.  The array
+ * of tensors is the host's and may go when the call returns.  Squares and their
+ * sums are fp32 (a thread's many with what the additions round off), fp64 where they
+ * leave its range, in a fixed order for given sizes and device. */
 int tiles_grad_norm(const tiles_grad_tensor* tensors, int64_t n, float* norm, void* workspace,
                     size_t ws_bytes, void* stream);
 

@@ -1,9 +1,11 @@
 """GPU parity of the gradients' norm and clipping with the float64 definitions.
 
-The squares of a thread's at most 64 elements are added in fp32 (65 roundings
-of 2^-24), everything above that in fp64, and the norm is rounded once: it is
-within 34 * 2^-24 of itself.  The factor adds its own two roundings, a scaled
-element one fp32 product and half a spacing of its type."""
+The squares of a thread's at most 64 elements are added in fp32, in at most 17
+roundings of 2^-24; its sums of those lose nothing that counts; then come 5 levels
+of lanes, 8 warps, a thread's share of the blocks' sums, 5 levels and 8 warps: under
+60 roundings together, half of which reach the root, whose own argument and result
+are rounded once more.  The norm is within 34 * 2^-24 of itself.  The factor adds its
+own two roundings, a scaled element one fp32 product and half a spacing of its type."""
 
 import numpy as np
 import pytest

@@ -227,7 +227,8 @@ def test_dispatch(k, dtype):
 
 # One launch holds 64 chunks of 16 KB, each of one tensor: on both sides of that.
 CLIPS = [[524288], [524289], [524280, 8], [8192] * 64, [8192] * 65, [8193] * 32, [8193] * 33, [1] * 64,
-         [1] * 65, [1] * 121, [0, 3, 0], [262144, 262144], [262144, 262145]]
+         [1] * 65, [1] * 121, [0, 3, 0], [262144, 262144], [262144, 262145],
+         [700] * 1000, [700] * 1001, [3001] * 2003]
 
 
 @pytest.mark.parametrize("sizes", CLIPS, ids=lambda s: f"{len(s)}x{s[0]}")
@@ -255,3 +256,26 @@ def test_clip(sizes, shift, shift_out):
             assert torch.equal(grads[i], g)
             rest = torch.cat([full[i][:shift_out], full[i][shift_out + g.numel():]])
             assert bool((rest == 7.0).all())
+
+
+@pytest.mark.parametrize("count", [1, 150])
+def test_clip_of_much_with_elements_whose_squares_leave_the_range(count):
+    n = 3000000 // count
+    for scale, odd in ((1.0, 1e25), (1e-25, 1e-3), (1e-25, 1e-25), (1.0, 1e-30), (1e13, 1.0)):
+        grads = [draw(1, n, "f32", i)[0] * scale for i in range(count)]
+        grads[count // 2][5::1009] = odd
+        norm64 = sum((g.double() ** 2).sum() for g in grads).sqrt()
+        norm = T.grad_norm(grads)
+        assert abs(float(norm) - float(norm64)) <= 34 * 2.0 ** -24 * float(norm64), (scale, odd)
+        before = [g.double() for g in grads]
+        bound = 0.5 * float(norm64)
+        assert torch.equal(T.clip_grads(grads, bound), norm)
+        factor = bound / (float(norm64) + 1e-6)
+        for g, b in zip(grads, before):
+            within(g, b * factor, 38 * 2.0 ** -24 * (b * factor).abs() + 2.0 ** -149)
+    for odd in (float("inf"), float("nan")):
+        grads = [draw(1, n, "f32", i)[0] for i in range(count)]
+        grads[-1][-1] = odd
+        got = float(T.clip_grads(grads, 1.0))
+        assert got == odd or (odd != odd and got != got)
+        assert bool(grads[0][:-1].isnan().all() if odd != odd else (grads[0][:-1] == 0).all())

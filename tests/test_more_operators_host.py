@@ -261,6 +261,7 @@ def tensors(*specs):
     ([(PTR + 2, None, 4, _abi.F32)], 1.0, 0.0, _abi.ERR_MISALIGNED),
     ([(PTR, PTR + 0x101, 4, _abi.BF16)], 1.0, 0.0, _abi.ERR_MISALIGNED),
     ([(PTR, None, 1 << 41, _abi.F32)], 1.0, 0.0, _abi.ERR_TOO_LARGE),
+    ([(PTR, None, 1 << 40, _abi.F32)] * 17, 1.0, 0.0, _abi.ERR_TOO_LARGE),
     # The same tensor twice; one that starts inside another; an output over
     # another gradient, over its own a little shifted, and over another output.
     ([(PTR, None, 4, _abi.F32)] * 2, 1.0, 0.0, _abi.ERR_INVALID_ARG),

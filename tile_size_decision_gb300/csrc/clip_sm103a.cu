@@ -12,10 +12,11 @@
 namespace tiles {
 namespace {
 
-// Tensors a launch takes: their descriptions travel with it as arguments (4 KB),
-// so that nothing on the host has to outlive the call and a captured launch
-// carries them.  (Fewer where there is but one launch, and a short one.)
-constexpr int kTensors = 120, kFewTensors = 16;
+// Tensors a launch takes: their descriptions travel with it as arguments (at most
+// 32,764 bytes), so that nothing on the host has to outlive the call and a captured
+// launch carries them.  Three sizes, as the host copies all of it: 600 tensors of
+// 20,000 bf16 in one launch 20 us, in five 51.
+constexpr int kTensors = 1000, kSomeTensors = 120, kFewTensors = 16;
 constexpr int kClipThreads = 256;
 constexpr int kMostBlocksPerSm = 8;
 
@@ -25,6 +26,15 @@ struct Tensor {
     int64_t count;
 };
 
+// A sum of squares: that of the elements whose squares fp32 holds, and of others.
+struct alignas(16) Partial {
+    float near;
+    double far;
+
+    // (Without an fp64 comparison.)
+    __device__ __forceinline__ bool has_far() const { return __double_as_longlong(far) != 0; }
+};
+
 template <int N>
 struct TensorBatch {
     int32_t tensors;
@@ -32,14 +42,13 @@ struct TensorBatch {
     int32_t parts;                             // partial sums of all launches; -1: norm is there
     float max_norm, eps;
     uint32_t once;                             // chunks before this one are not read again soon
-    double* partials;                          // this launch's first, or (scaling) the very first
+    Partial* partials;                         // this launch's first, or (scaling) the very first
     float* norm;
     uint32_t chunks_before[N];                 // of the launch's tensors before each
     uint8_t dtype[N];
     Tensor at[N];
 };
-using Batch = TensorBatch<kTensors>;
-static_assert(sizeof(Batch) <= 4096, "arguments of one launch");
+static_assert(sizeof(TensorBatch<kTensors>) <= 32764, "arguments of one launch");
 
 // A tensor is seen as 16-byte pieces that start on 16 bytes, of which its first
 // and last may hold other memory too; U pieces a thread are a chunk, what a
@@ -93,11 +102,30 @@ __device__ __forceinline__ uint4 partial_piece(const T* from, int64_t at, int64_
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Squares and sums in fp32 within a thread's pieces of a chunk, in fp64 from
-// there on.  Where that leaves fp32's range (a square over 2^127, or squares
-// that together are under 2^-90 and are not of zeros) the thread takes its
-// elements once more in fp64.
-constexpr float kSmallSquares = 0x1p-90f;
+// Squares and their sums are fp32: a thread adds its pieces of a chunk in four
+// chains, its chunks' sums with what their additions round off, and the threads'
+// sums in a tree.  (fp64 takes this chip 64 times as long: with sums in fp64
+// from a chunk's on 5 million bf16 elements took 13.8 us to clip, not 10.6.)  A chunk's
+// share that leaves fp32's range (over 2^80, so that no sum of such leaves it
+// either, or under 2^-90 and not of zeros alone) the thread takes once more, in fp64,
+// and that sum stays apart.
+constexpr float kSmallSquares = 0x1p-90f, kBigSquares = 0x1p80f;
+
+struct Sum {
+    float s = 0.0f, lost = 0.0f;               // lost: what the additions rounded off
+    double far = 0.0;
+    bool has_far = false;
+
+    __device__ __forceinline__ void add(float x) {
+        const float t = s + x, b = t - s;
+        lost += (s - (t - b)) + (x - b);
+        s = t;
+    }
+    __device__ __forceinline__ void add_far(double x) {
+        far += x;
+        has_far = true;
+    }
+};
 
 template <typename T> __device__ __forceinline__ constexpr uint32_t magnitude_bits() {
     return sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
@@ -127,9 +155,9 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
     return v;
 }
 
-// The squares of a thread's share of the chunk that starts at piece `first`.
+// The squares of a thread's share of the chunk that starts at piece `first`, to its sum.
 template <typename T, int U>
-__device__ __forceinline__ double chunk_squares(const Tensor& t, int64_t first, bool once) {
+__device__ __forceinline__ void chunk_squares(const Tensor& t, int64_t first, bool once, Sum& sum) {
     constexpr int N = 16 / static_cast<int>(sizeof(T));
     const T* from = static_cast<const T*>(t.from);
     const int64_t bytes = t.count * static_cast<int64_t>(sizeof(T));
@@ -153,7 +181,7 @@ __device__ __forceinline__ double chunk_squares(const Tensor& t, int64_t first, 
                 q[u] = partial_piece(from, b, t.count);
         }
     }
-    float s = 0.0f;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t any = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -161,62 +189,79 @@ __device__ __forceinline__ double chunk_squares(const Tensor& t, int64_t first, 
         float v[N];
         widen_piece<T>(q[u], v);
 #pragma unroll
-        for (int i = 0; i < N; ++i) s = fmaf(v[i], v[i], s);
+        for (int i = 0; i < N; ++i) s[i & 3] = fmaf(v[i], v[i], s[i & 3]);
     }
-    if (!(s >= kSmallSquares && s <= FLT_MAX) && (any & magnitude_bits<T>()))
-        return squares_in_double<T, U>(t, first);
-    return static_cast<double>(s);
+    const float all = (s[0] + s[1]) + (s[2] + s[3]);
+    if (!(all >= kSmallSquares && all <= kBigSquares) && (any & magnitude_bits<T>()))
+        sum.add_far(squares_in_double<T, U>(t, first));
+    else
+        sum.add(all);
 }
 
-// The sum over a block; every thread gets it.
-__device__ __forceinline__ double block_sum(double s) {
-    __shared__ double warp_sums[kClipThreads / 32];
+// The sum over a block; every thread gets it.  Both parts, the far one where any
+// thread has one.
+__device__ __forceinline__ Partial block_sum(const Sum& sum) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    __shared__ float near[kClipThreads / 32];
+    __shared__ double far[kClipThreads / 32];
+    const int warp = threadIdx.x >> 5;
+    float s = sum.s + sum.lost;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = s;
-    __syncthreads();
-    s = 0.0;
+    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(kAll, s, d);
+    if ((threadIdx.x & 31) == 0) near[warp] = s;
+    Partial p{0.0f, 0.0};
+    if (__syncthreads_or(sum.has_far)) {
+        double f = sum.far;
 #pragma unroll
-    for (int i = 0; i < kClipThreads / 32; ++i) s += warp_sums[i];
-    return s;
+        for (int d = 16; d >= 1; d >>= 1) f += __shfl_xor_sync(kAll, f, d);
+        if ((threadIdx.x & 31) == 0) far[warp] = f;
+        __syncthreads();
+        for (double w : far) p.far += w;
+    }
+#pragma unroll
+    for (float w : near) p.near += w;
+    return p;
 }
 
 // One partial sum a block, over the chunks blockIdx.x, + gridDim.x, ...  256
 // million bf16 elements 78 us with the norm: 98% of the measured copy bandwidth.
-template <int U>
+template <int U, int N>
 __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
-    squares_kernel(const __grid_constant__ Batch a) {
+    squares_kernel(const __grid_constant__ TensorBatch<N> a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    double s = 0.0;
+    Sum s;
     for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
         const int n = tensor_of(a, c);
         const Tensor& t = a.at[n];
         const int64_t first = static_cast<int64_t>(c - a.chunks_before[n]) * kChunkPieces<U>;
-        if (a.dtype[n] == TILES_BF16) s += chunk_squares<__nv_bfloat16, U>(t, first, c < a.once);
-        else if (a.dtype[n] == TILES_F16) s += chunk_squares<__half, U>(t, first, c < a.once);
-        else s += chunk_squares<float, U>(t, first, c < a.once);
+        if (a.dtype[n] == TILES_BF16) chunk_squares<__nv_bfloat16, U>(t, first, c < a.once, s);
+        else if (a.dtype[n] == TILES_F16) chunk_squares<__half, U>(t, first, c < a.once, s);
+        else chunk_squares<float, U>(t, first, c < a.once, s);
     }
-    s = block_sum(s);
-    if (threadIdx.x == 0) a.partials[blockIdx.x] = s;
+    const Partial p = block_sum(s);
+    if (threadIdx.x == 0) a.partials[blockIdx.x] = p;
 }
 
-// The square root of a sum of squares.  In fp32 (whose two roundings are a unit in
-// the last place together) where its range holds the sum: in fp64 it takes this
-// chip a microsecond.
-__device__ __forceinline__ float norm_from(double s) {
-    return s >= 0x1p-120 && s <= 0x1p120 ? sqrtf(static_cast<float>(s)) : static_cast<float>(sqrt(s));
+// The square root of a sum of squares.  fp64's takes this chip a microsecond.
+__device__ __forceinline__ float root_of(const Partial& p) {
+    return !p.has_far() ? sqrtf(p.near) : static_cast<float>(sqrt(static_cast<double>(p.near) + p.far));
 }
 
 // The norm from all partial sums, in a fixed order (every thread of a block
 // gets it).
-__device__ __forceinline__ float norm_of(const double* partials, int parts) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kClipThreads) s += partials[i];
-    return norm_from(block_sum(s));
+__device__ __forceinline__ float norm_of(const Partial* partials, int parts) {
+    Sum s;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < parts; i += kClipThreads) {
+        const Partial p = partials[i];
+        s.add(p.near);
+        if (p.has_far()) s.add_far(p.far);
+    }
+    return root_of(block_sum(s));
 }
 
-__global__ void __launch_bounds__(kClipThreads) norm_kernel(const double* partials, int parts,
+__global__ void __launch_bounds__(kClipThreads) norm_kernel(const Partial* partials, int parts,
                                                             float* norm) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
@@ -264,49 +309,54 @@ __device__ __forceinline__ void scale_piece(const Tensor& t, int64_t b, float sc
             static_cast<T*>(t.to)[first + i] = from_float<T>(v[i] * scale);
 }
 
-// The chunk that starts at piece `first`, pieces being those of what is written.
-template <typename T, int U>
-__device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t first, float scale) {
-    const int64_t bytes = t.count * static_cast<int64_t>(sizeof(T));
-    const int64_t start = first * 16 - misaligned(t.to) + static_cast<int64_t>(threadIdx.x) * 16;
-    const char* from = static_cast<const char*>(t.from) + start;
-    char* to = static_cast<char*>(t.to) + start;
-    constexpr int kStep = kClipThreads * 16;
-    const bool same = misaligned(t.from) == misaligned(t.to);
-    if (same && first * 16 >= misaligned(t.to) && (first + kChunkPieces<U>) * 16 - misaligned(t.to) <= bytes) {
-        uint4 q[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = *reinterpret_cast<const uint4*>(from + u * kStep);
-#pragma unroll
-        for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(to + u * kStep) = scaled<T>(q[u], scale);
-        return;
-    }
-#pragma unroll 1
-    for (int64_t b = start, end = min(bytes, start + U * kStep); b < end; b += kStep) scale_piece<T>(t, b, scale);
-}
-
-// Finds the norm, from a few partial sums itself (a launch less) or where
-// norm_kernel left it (parts < 0; 5 million elements in 60 tensors 15.8 us
-// against 26.6), then scales its chunks, the last ones first: those the squares
-// read last, which L2 still holds.  256 million bf16 elements, norm and scaling:
+// Finds the norm, from the partial sums itself (a launch less) or where
+// norm_kernel left it (parts < 0), then scales its chunks, the last ones first:
+// those the squares read last, which L2 still holds.  256 million bf16 elements, norm and scaling:
 // 228 us, 1.54 GB at the measured copy bandwidth.
-template <int U>
+template <int U, int N>
 __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
-    scale_kernel(const __grid_constant__ Batch a) {
+    scale_kernel(const __grid_constant__ TensorBatch<N> a) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const float norm = a.parts < 0 ? *a.norm : norm_of(a.partials, a.parts);
-    if (a.parts >= 0 && a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = norm;
-    const float scale = factor_of(norm, a.max_norm, a.eps);
+    float scale = 0.0f;
+    bool known = false;
     for (uint32_t i = blockIdx.x; i < a.chunks; i += gridDim.x) {
         const uint32_t c = a.chunks - 1 - i;
         const int n = tensor_of(a, c);
         const Tensor& t = a.at[n];
+        // In pieces of what is written.
+        constexpr int kStep = kClipThreads * 16;
+        const int64_t bytes = t.count * (a.dtype[n] == TILES_F32 ? 4 : 2);
+        const int64_t at = static_cast<int64_t>(c - a.chunks_before[n]) * (U * kStep) - misaligned(t.to);
+        const int64_t mine = at + static_cast<int>(threadIdx.x) * 16;
+        const bool whole = misaligned(t.from) == misaligned(t.to) && at >= 0 && at + U * kStep <= bytes;
+        uint4 q[U];
+        if (whole)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                q[u] = *reinterpret_cast<const uint4*>(static_cast<const char*>(t.from) + mine + u * kStep);
+        if (!known) {                                     // (with the first chunk on its way)
+            const float norm = a.parts < 0 ? *a.norm : norm_of(a.partials, a.parts);
+            if (a.parts >= 0 && a.norm && i == 0 && threadIdx.x == 0) *a.norm = norm;
+            scale = factor_of(norm, a.max_norm, a.eps);
+            known = true;
+        }
         if (scale == 1.0f && t.to == t.from) continue;    // as it is
-        const int64_t first = static_cast<int64_t>(c - a.chunks_before[n]) * kChunkPieces<U>;
-        if (a.dtype[n] == TILES_BF16) scale_chunk<__nv_bfloat16, U>(t, first, scale);
-        else if (a.dtype[n] == TILES_F16) scale_chunk<__half, U>(t, first, scale);
-        else scale_chunk<float, U>(t, first, scale);
+        auto write = [&](auto zero) {
+            using T = decltype(zero);
+            if (whole) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    *reinterpret_cast<uint4*>(static_cast<char*>(t.to) + mine + u * kStep) = scaled<T>(q[u], scale);
+            } else {
+#pragma unroll 1
+                for (int64_t b = mine, end = min(bytes, mine + U * kStep); b < end; b += kStep)
+                    scale_piece<T>(t, b, scale);
+            }
+        };
+        if (a.dtype[n] == TILES_BF16) write(__nv_bfloat16());
+        else if (a.dtype[n] == TILES_F16) write(__half());
+        else write(float());
     }
 }
 
@@ -319,6 +369,10 @@ __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
 // for every thread 15.8 us).  max_norm < 0: the norm alone.  Every tensor's output
 // starts as far off 16 bytes as its gradient.
 constexpr int kClusterCtas = 8, kClusterThreads = 1024, kHeld = 8;
+
+__device__ __forceinline__ float norm_from(double s) {
+    return s >= 0x1p-120 && s <= 0x1p120 ? sqrtf(static_cast<float>(s)) : static_cast<float>(sqrt(s));
+}
 
 template <typename T>
 __device__ __forceinline__ float piece_squares(const uint4& q) {
@@ -478,14 +532,14 @@ void fill_batch(TensorBatch<N>* b, const tiles_grad_tensor* t, Run r, int chunk_
 
 template <int U> constexpr int kBlocksPerSm = U > 4 ? 4 : 8;
 
-template <int U>
-int run_blocks(const Batch& b, int sms) {
+template <int U, int N>
+int run_blocks(const TensorBatch<N>& b, int sms) {
     return static_cast<int>(std::min<int64_t>(b.chunks, static_cast<int64_t>(sms) * kBlocksPerSm<U>));
 }
 
 size_t clip_bytes(int64_t tensors, int sms) {
     const int64_t launches = (tensors + kTensors - 1) / kTensors;
-    return kConvMinWorkspaceBytes + static_cast<size_t>(launches) * sms * kMostBlocksPerSm * 8;
+    return kConvMinWorkspaceBytes + static_cast<size_t>(launches) * sms * kMostBlocksPerSm * sizeof(Partial);
 }
 
 // No output may lie over another tensor's output or gradient.
@@ -521,12 +575,15 @@ int check_tensors(const tiles_grad_tensor* t, int64_t n, const float* norm, bool
     if (n > (1 << 20)) return fail(TILES_ERR_TOO_LARGE, "more than 2^20 tensors");
     if (!norm || !element_aligned(norm, 4))
         return fail(TILES_ERR_INVALID_ARG, "norm is null or not aligned to its element");
+    int64_t bytes = 0;
     for (int64_t i = 0; i < n; ++i) {
         const int eb = dtype_bytes(t[i].dtype);
         if (!eb) return fail(TILES_ERR_UNSUPPORTED_DTYPE, "tensor %lld must be f16, bf16 or f32", (long long)i);
         if (t[i].count < 0) return fail(TILES_ERR_INVALID_ARG, "tensor %lld has a negative size", (long long)i);
         if (t[i].count > (int64_t(1) << 40)) return fail(TILES_ERR_TOO_LARGE, "tensor %lld exceeds 2^40", (long long)i);
         if (t[i].count == 0) continue;
+        bytes += t[i].count * eb;
+        if (bytes > (int64_t(1) << 46)) return fail(TILES_ERR_TOO_LARGE, "the gradients exceed 2^46 bytes");
         if (!t[i].grad) return fail(TILES_ERR_INVALID_ARG, "tensor %lld is null", (long long)i);
         if (!element_aligned(t[i].grad, eb) || (out && !element_aligned(t[i].out, eb)))
             return fail(TILES_ERR_MISALIGNED, "tensor %lld is not aligned to its element", (long long)i);
@@ -555,62 +612,63 @@ constexpr int64_t kKeptBytes = 100000000;
 
 // The launches of the squares; the number of partial sums they leave.  `again`:
 // the gradients are read again.
-template <int U>
-int launch_squares(const tiles_grad_tensor* t, int64_t n, bool again, double* partials, int sms, int* parts,
+template <int U, int N>
+int launch_squares(const tiles_grad_tensor* t, int64_t n, bool again, Partial* partials, int sms, int* parts,
                    cudaStream_t st) {
-    Batch b{};
+    TensorBatch<N> b{};
     *parts = 0;
     constexpr int64_t kChunk = kChunkPieces<U> * 16;
     int64_t left = again ? total_bytes(t, n) : 0;
-    for (int64_t i = 0; i < n; i += kTensors) {
-        fill_batch(&b, t, {i, std::min<int64_t>(n, i + kTensors)}, kChunkPieces<U>, false);
+    for (int64_t i = 0; i < n; i += N) {
+        fill_batch(&b, t, {i, std::min<int64_t>(n, i + N)}, kChunkPieces<U>, false);
         if (b.chunks == 0) continue;
         b.partials = partials + *parts;
         b.once = static_cast<uint32_t>(
             std::min<int64_t>(b.chunks, std::max<int64_t>(0, left - kKeptBytes) / kChunk));
         left -= b.chunks * kChunk;
         const int blocks = run_blocks<U>(b, sms);
-        const int e = launch(squares_kernel<U>, dim3(blocks), dim3(kClipThreads), 0, st, b);
+        const int e = launch(squares_kernel<U, N>, dim3(blocks), dim3(kClipThreads), 0, st, b);
         if (e != cudaSuccess) return e;
         *parts += blocks;
     }
     return cudaSuccess;
 }
 
-template <int U>
+template <int U, int N>
 int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
-                double* partials, int sms, cudaStream_t st) {
-    Batch b{};
-    int e = launch_squares<U>(t, n, true, partials, sms, &b.parts, st);
+                Partial* partials, int sms, cudaStream_t st) {
+    TensorBatch<N> b{};
+    int e = launch_squares<U, N>(t, n, true, partials, sms, &b.parts, st);
     if (e != cudaSuccess) return e;
     b.partials = partials;
     b.max_norm = max_norm;
     b.eps = eps;
     b.norm = norm;
-    // Few partial sums every block adds up itself; of many one block makes the
-    // norm first, and the scaling's blocks can be as many as there are chunks.
-    if (b.parts > kClipThreads) {
-        e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const double*>(partials), b.parts,
+    // One launch's partial sums every block of the scaling adds up itself; where there
+    // are more one block makes the norm first (of 17 launches
+    // 131 us against 163).
+    if (b.parts > kMostBlocksPerSm * sms) {
+        e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const Partial*>(partials), b.parts,
                    norm);
         if (e != cudaSuccess) return e;
         b.parts = -1;
     }
-    for (int64_t i = (n - 1) / kTensors * kTensors; i >= 0; i -= kTensors) {
-        fill_batch(&b, t, {i, std::min<int64_t>(n, i + kTensors)}, kChunkPieces<U>, true);
+    for (int64_t i = (n - 1) / N * N; i >= 0; i -= N) {
+        fill_batch(&b, t, {i, std::min<int64_t>(n, i + N)}, kChunkPieces<U>, true);
         if (b.chunks == 0) continue;
-        e = launch(scale_kernel<U>, dim3(std::min<uint32_t>(b.chunks, 1u << 30)), dim3(kClipThreads), 0, st, b);
+        e = launch(scale_kernel<U, N>, dim3(std::min<uint32_t>(b.chunks, 1u << 30)), dim3(kClipThreads), 0, st, b);
         if (e != cudaSuccess) return e;
         if (b.parts >= 0) b.norm = nullptr;               // written once
     }
     if (b.parts == 0)                                     // no elements at all
-        e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const double*>(partials), 0, norm);
+        e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const Partial*>(partials), 0, norm);
     return e;
 }
 
 // Whether one cluster holds the gradients (and their outputs, if any, start where
 // they do).
 bool cluster_takes(const tiles_grad_tensor* t, int64_t n, bool out) {
-    if (n > kTensors) return false;
+    if (n > kSomeTensors) return false;
     int64_t chunks = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (t[i].count == 0) continue;
@@ -636,12 +694,18 @@ int launch_cluster_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, f
 int launch_cluster_clip_any(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
                             cudaStream_t st) {
     return n <= kFewTensors ? launch_cluster_clip<kFewTensors>(t, n, max_norm, eps, norm, st)
-                            : launch_cluster_clip<kTensors>(t, n, max_norm, eps, norm, st);
+                            : launch_cluster_clip<kSomeTensors>(t, n, max_norm, eps, norm, st);
 }
 
 // Pieces a thread: small gradients are spread over more blocks.
 bool few_bytes(const tiles_grad_tensor* t, int64_t n, int sms) {
     return total_bytes(t, n) < static_cast<int64_t>(sms) * 4 * kChunkPieces<8> * 16;
+}
+
+// By the bytes and the number of tensors.
+template <typename F>
+F pick(bool few, int64_t n, F few_some, F few_many, F some, F many) {
+    return n <= kSomeTensors ? (few ? few_some : some) : (few ? few_many : many);
 }
 
 }  // namespace
@@ -667,15 +731,16 @@ int tiles_grad_norm(const tiles_grad_tensor* t, int64_t n, float* norm, void* ws
     if (s != TILES_OK) return s;
     if ((s = current_sm_count(&sms)) != TILES_OK) return s;
     if ((s = check_clip_workspace(ws, ws_bytes, n, sms)) != TILES_OK) return s;
-    double* partials = reinterpret_cast<double*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
+    Partial* partials = reinterpret_cast<Partial*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int parts = 0;
     if (cluster_takes(t, n, false))
         return launch_status(launch_cluster_clip_any(t, n, -1.0f, 0.0f, norm, st), "gradient norm");
-    int e = few_bytes(t, n, sms) ? launch_squares<2>(t, n, false, partials, sms, &parts, st)
-                                 : launch_squares<8>(t, n, false, partials, sms, &parts, st);
+    const auto squares = pick(few_bytes(t, n, sms), n, launch_squares<2, kSomeTensors>, launch_squares<2, kTensors>,
+                              launch_squares<8, kSomeTensors>, launch_squares<8, kTensors>);
+    int e = squares(t, n, false, partials, sms, &parts, st);
     if (e == cudaSuccess)
-        e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const double*>(partials), parts, norm);
+        e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const Partial*>(partials), parts, norm);
     return launch_status(e, "gradient norm");
 }
 
@@ -688,11 +753,12 @@ int tiles_clip_grads(const tiles_grad_tensor* t, int64_t n, float max_norm, floa
     if ((s = check_apart(t, n)) != TILES_OK) return s;
     if ((s = current_sm_count(&sms)) != TILES_OK) return s;
     if ((s = check_clip_workspace(ws, ws_bytes, n, sms)) != TILES_OK) return s;
-    double* partials = reinterpret_cast<double*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
+    Partial* partials = reinterpret_cast<Partial*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const auto clip = pick(few_bytes(t, n, sms), n, launch_clip<2, kSomeTensors>, launch_clip<2, kTensors>,
+                           launch_clip<8, kSomeTensors>, launch_clip<8, kTensors>);
     const int e = cluster_takes(t, n, true) ? launch_cluster_clip_any(t, n, max_norm, eps, norm, st)
-                  : few_bytes(t, n, sms)    ? launch_clip<2>(t, n, max_norm, eps, norm, partials, sms, st)
-                                            : launch_clip<8>(t, n, max_norm, eps, norm, partials, sms, st);
+                                            : clip(t, n, max_norm, eps, norm, partials, sms, st);
     return launch_status(e, "gradient clipping");
 }
 
