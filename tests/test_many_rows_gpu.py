@@ -1,6 +1,6 @@
 """GPU parity of the layer norm, the routing calls and the clipping where there
 are many rows or many bytes: the kernels that keep the next rows on their way in
-(from some hundred rows on), and the clip on both sides of what one launch holds.
+(from some hundred rows on), and the clip on both sides of what a chunk and a launch hold.
 The plain forms are computed in float64 on the GPU.
 
 Tolerances, from the kernels' arithmetic (fp32, one rounding to the output's
@@ -225,8 +225,8 @@ def test_dispatch(k, dtype):
 
 # ---- clipping -------------------------------------------------------------------------------
 
-# One launch holds 64 chunks of 16 KB, each of one tensor: on both sides of that.
-CLIPS = [[524288], [524289], [524280, 8], [8192] * 64, [8192] * 65, [8193] * 32, [8193] * 33, [1] * 64,
+# Chunks are 8 KB, tensors 16, 120 and 1000 a launch: on both sides of those.
+CLIPS = [[4096], [4097], [524288], [524280, 8], [8192] * 16, [8193] * 17, [8193] * 33, [1] * 64,
          [1] * 65, [1] * 121, [0, 3, 0], [262144, 262144], [262144, 262145],
          [700] * 1000, [700] * 1001, [3001] * 2003]
 

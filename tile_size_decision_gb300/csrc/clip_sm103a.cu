@@ -360,152 +360,6 @@ __global__ void __launch_bounds__(kClipThreads, U > 4 ? 4 : 8)
     }
 }
 
-// Few gradients, at most kHeld pieces a thread of one cluster: they stay in its
-// registers between the norm and the scaling, and one launch does it all.  As a
-// program calls it 12 tensors of 25,000 elements take 6.8 us against 8.1 with two
-// launches; in a captured graph, where two launches overlap, 12,288 elements 4.7
-// against 5.1, but 524,288, which only eight SMs move, 6.7 against 4.9.  Neither fp64 nor
-// its square root is done by more than a warp where fp32 holds the sums (with fp64
-// for every thread 15.8 us).  max_norm < 0: the norm alone.  Every tensor's output
-// starts as far off 16 bytes as its gradient.
-constexpr int kClusterCtas = 8, kClusterThreads = 1024, kHeld = 8;
-
-__device__ __forceinline__ float norm_from(double s) {
-    return s >= 0x1p-120 && s <= 0x1p120 ? sqrtf(static_cast<float>(s)) : static_cast<float>(sqrt(s));
-}
-
-template <typename T>
-__device__ __forceinline__ float piece_squares(const uint4& q) {
-    float v[16 / sizeof(T)], s = 0.0f;
-    widen_piece<T>(q, v);
-#pragma unroll
-    for (float e : v) s = fmaf(e, e, s);
-    return s;
-}
-
-template <typename T>
-__device__ __forceinline__ double piece_squares_in_double(const uint4& q) {
-    float v[16 / sizeof(T)];
-    widen_piece<T>(q, v);
-    double s = 0.0;
-    for (float e : v) s += static_cast<double>(e) * static_cast<double>(e);
-    return s;
-}
-
-template <int N>
-__global__ void __launch_bounds__(kClusterThreads)
-    clip_cluster_kernel(const __grid_constant__ TensorBatch<N> a) {
-    // A chunk of the block: the tensor's memory, where the chunk starts in it, and
-    // the tensor's bytes (none: no chunk).
-    struct Chunk {
-        const char* from;
-        char* to;
-        int64_t start, bytes;
-        int dtype;
-    };
-    __shared__ Chunk chunks[kHeld];
-    __shared__ double warp_sums[kClusterThreads / 32], total;
-    __shared__ float factor;
-    const uint32_t rank = ptx::cluster_ctarank();
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid < kHeld) {
-        const uint32_t c = rank + tid * kClusterCtas;
-        Chunk k{nullptr, nullptr, 0, 0, 0};
-        if (c < a.chunks) {
-            const int n = tensor_of(a, c);
-            const Tensor& t = a.at[n];
-            k = {static_cast<const char*>(t.from), static_cast<char*>(t.to),
-                 static_cast<int64_t>(c - a.chunks_before[n]) * (kClusterThreads * 16) - misaligned(t.from),
-                 t.count * (a.dtype[n] == TILES_F32 ? 4 : 2), a.dtype[n]};
-        }
-        chunks[tid] = k;
-    }
-    __syncthreads();
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
-    uint4 q[kHeld];
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const Chunk& k = chunks[i];
-        const int64_t b = k.start + tid * 16;
-        q[i] = make_uint4(0, 0, 0, 0);
-        if (b >= 0 && b + 16 <= k.bytes)
-            q[i] = *reinterpret_cast<const uint4*>(k.from + b);
-        else if (b < k.bytes)
-            q[i] = k.dtype == TILES_F32
-                       ? partial_piece(reinterpret_cast<const float*>(k.from), b, k.bytes / 4)
-                       : partial_piece(reinterpret_cast<const __half*>(k.from), b, k.bytes / 2);
-    }
-    // As in chunk_squares, with the warp's sum in fp32 too where it fits.
-    float s32 = 0.0f;
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int dtype = chunks[i].dtype;
-        any |= (q[i].x | q[i].y | q[i].z | q[i].w) & (dtype == TILES_F32 ? 0x7fffffffu : 0x7fff7fffu);
-        s32 += dtype == TILES_BF16  ? piece_squares<__nv_bfloat16>(q[i])
-               : dtype == TILES_F16 ? piece_squares<__half>(q[i])
-                                    : piece_squares<float>(q[i]);
-    }
-    const bool fits = any == 0 || (s32 >= kSmallSquares && s32 <= FLT_MAX / 64);
-    double s = 0.0;
-    if (__all_sync(0xffffffffu, fits)) {
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) s32 += __shfl_xor_sync(0xffffffffu, s32, d);
-        s = static_cast<double>(s32);
-    } else {
-        for (int i = 0; i < kHeld; ++i) {
-            const int dtype = chunks[i].dtype;
-            s += dtype == TILES_BF16  ? piece_squares_in_double<__nv_bfloat16>(q[i])
-                 : dtype == TILES_F16 ? piece_squares_in_double<__half>(q[i])
-                                      : piece_squares_in_double<float>(q[i]);
-        }
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    }
-    if (lane == 0) warp_sums[tid >> 5] = s;
-    __syncthreads();
-    if (tid < 32) {
-        s = warp_sums[lane];
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (lane == 0) total = s;
-    }
-    ptx::cluster_sync();
-    if (tid < 32) {
-        s = ptx::ld_shared_cluster_f64(ptx::map_to_cta(ptx::smem_addr(&total), lane % kClusterCtas));
-#pragma unroll
-        for (int d = kClusterCtas / 2; d >= 1; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        const float norm = norm_from(s);
-        if (tid == 0) {
-            if (rank == 0) *a.norm = norm;
-            factor = factor_of(norm, a.max_norm, a.eps);
-        }
-    }
-    ptx::cluster_arrive();                     // the others' totals are read; no block may leave before that
-    __syncthreads();
-    const float scale = factor;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const Chunk& k = chunks[i];
-        const int64_t b = k.start + tid * 16;
-        if (a.max_norm < 0.0f || b >= k.bytes || (scale == 1.0f && k.to == k.from)) continue;
-        const uint4 o = k.dtype == TILES_BF16  ? scaled<__nv_bfloat16>(q[i], scale)
-                        : k.dtype == TILES_F16 ? scaled<__half>(q[i], scale)
-                                               : scaled<float>(q[i], scale);
-        if (b >= 0 && b + 16 <= k.bytes) {
-            *reinterpret_cast<uint4*>(k.to + b) = o;
-            continue;
-        }
-        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)            // in 16 bits, of either type
-            if (b + 2 * e >= 0 && b + 2 * e < k.bytes)
-                *reinterpret_cast<uint16_t*>(k.to + b + 2 * e) = static_cast<uint16_t>(w[e / 2] >> 16 * (e & 1));
-    }
-    ptx::cluster_wait();
-}
-
 // A run of tensors that one launch takes: [first, last) of the caller's, those
 // without elements left out.
 struct Run { int64_t first, last; };
@@ -615,7 +469,7 @@ constexpr int64_t kKeptBytes = 100000000;
 template <int U, int N>
 int launch_squares(const tiles_grad_tensor* t, int64_t n, bool again, Partial* partials, int sms, int* parts,
                    cudaStream_t st) {
-    TensorBatch<N> b{};
+    TensorBatch<N> b;                                     // (its arrays need no zeros)
     *parts = 0;
     constexpr int64_t kChunk = kChunkPieces<U> * 16;
     int64_t left = again ? total_bytes(t, n) : 0;
@@ -637,7 +491,7 @@ int launch_squares(const tiles_grad_tensor* t, int64_t n, bool again, Partial* p
 template <int U, int N>
 int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
                 Partial* partials, int sms, cudaStream_t st) {
-    TensorBatch<N> b{};
+    TensorBatch<N> b;
     int e = launch_squares<U, N>(t, n, true, partials, sms, &b.parts, st);
     if (e != cudaSuccess) return e;
     b.partials = partials;
@@ -645,8 +499,7 @@ int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps
     b.eps = eps;
     b.norm = norm;
     // One launch's partial sums every block of the scaling adds up itself; where there
-    // are more one block makes the norm first (of 17 launches
-    // 131 us against 163).
+    // are more one block makes the norm first (of 17 launches 131 us against 163).
     if (b.parts > kMostBlocksPerSm * sms) {
         e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const Partial*>(partials), b.parts,
                    norm);
@@ -665,47 +518,16 @@ int launch_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps
     return e;
 }
 
-// Whether one cluster holds the gradients (and their outputs, if any, start where
-// they do).
-bool cluster_takes(const tiles_grad_tensor* t, int64_t n, bool out) {
-    if (n > kSomeTensors) return false;
-    int64_t chunks = 0;
-    for (int64_t i = 0; i < n; ++i) {
-        if (t[i].count == 0) continue;
-        if (out && t[i].out && misaligned(t[i].out) != misaligned(t[i].grad)) return false;
-        if (t[i].count > kHeld * kClusterCtas * kClusterThreads * 8) return false;
-        const int64_t bytes = t[i].count * dtype_bytes(t[i].dtype) + misaligned(t[i].grad);
-        chunks += (bytes + kClusterThreads * 16 - 1) / (kClusterThreads * 16);
-    }
-    return chunks <= kHeld * kClusterCtas;
-}
-
-template <int N>
-int launch_cluster_clip(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
-                        cudaStream_t st) {
-    TensorBatch<N> b{};
-    fill_batch(&b, t, {0, n}, kClusterThreads, false);
-    b.max_norm = max_norm;
-    b.eps = eps;
-    b.norm = norm;
-    return launch_cluster(clip_cluster_kernel<N>, kClusterCtas, dim3(kClusterCtas), dim3(kClusterThreads), 0, st, b);
-}
-
-int launch_cluster_clip_any(const tiles_grad_tensor* t, int64_t n, float max_norm, float eps, float* norm,
-                            cudaStream_t st) {
-    return n <= kFewTensors ? launch_cluster_clip<kFewTensors>(t, n, max_norm, eps, norm, st)
-                            : launch_cluster_clip<kSomeTensors>(t, n, max_norm, eps, norm, st);
-}
-
 // Pieces a thread: small gradients are spread over more blocks.
 bool few_bytes(const tiles_grad_tensor* t, int64_t n, int sms) {
     return total_bytes(t, n) < static_cast<int64_t>(sms) * 4 * kChunkPieces<8> * 16;
 }
 
-// By the bytes and the number of tensors.
+// The instance for few or many bytes, and for so many tensors.
 template <typename F>
-F pick(bool few, int64_t n, F few_some, F few_many, F some, F many) {
-    return n <= kSomeTensors ? (few ? few_some : some) : (few ? few_many : many);
+F pick(bool few, int64_t n, const F (&some)[3], const F (&much)[3]) {
+    const int i = n <= kFewTensors ? 0 : n <= kSomeTensors ? 1 : 2;
+    return few ? some[i] : much[i];
 }
 
 }  // namespace
@@ -734,10 +556,11 @@ int tiles_grad_norm(const tiles_grad_tensor* t, int64_t n, float* norm, void* ws
     Partial* partials = reinterpret_cast<Partial*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int parts = 0;
-    if (cluster_takes(t, n, false))
-        return launch_status(launch_cluster_clip_any(t, n, -1.0f, 0.0f, norm, st), "gradient norm");
-    const auto squares = pick(few_bytes(t, n, sms), n, launch_squares<2, kSomeTensors>, launch_squares<2, kTensors>,
-                              launch_squares<8, kSomeTensors>, launch_squares<8, kTensors>);
+    const auto squares =
+        pick<decltype(&launch_squares<2, kTensors>)>(
+            few_bytes(t, n, sms), n,
+            {launch_squares<2, kFewTensors>, launch_squares<2, kSomeTensors>, launch_squares<2, kTensors>},
+            {launch_squares<8, kFewTensors>, launch_squares<8, kSomeTensors>, launch_squares<8, kTensors>});
     int e = squares(t, n, false, partials, sms, &parts, st);
     if (e == cudaSuccess)
         e = launch(norm_kernel, dim3(1), dim3(kClipThreads), 0, st, static_cast<const Partial*>(partials), parts, norm);
@@ -755,10 +578,12 @@ int tiles_clip_grads(const tiles_grad_tensor* t, int64_t n, float max_norm, floa
     if ((s = check_clip_workspace(ws, ws_bytes, n, sms)) != TILES_OK) return s;
     Partial* partials = reinterpret_cast<Partial*>(static_cast<char*>(ws) + kConvMinWorkspaceBytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const auto clip = pick(few_bytes(t, n, sms), n, launch_clip<2, kSomeTensors>, launch_clip<2, kTensors>,
-                           launch_clip<8, kSomeTensors>, launch_clip<8, kTensors>);
-    const int e = cluster_takes(t, n, true) ? launch_cluster_clip_any(t, n, max_norm, eps, norm, st)
-                                            : clip(t, n, max_norm, eps, norm, partials, sms, st);
+    const auto clip =
+        pick<decltype(&launch_clip<2, kTensors>)>(
+            few_bytes(t, n, sms), n,
+            {launch_clip<2, kFewTensors>, launch_clip<2, kSomeTensors>, launch_clip<2, kTensors>},
+            {launch_clip<8, kFewTensors>, launch_clip<8, kSomeTensors>, launch_clip<8, kTensors>});
+    const int e = clip(t, n, max_norm, eps, norm, partials, sms, st);
     return launch_status(e, "gradient clipping");
 }
 

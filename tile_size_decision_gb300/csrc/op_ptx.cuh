@@ -16,21 +16,6 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t cluster_addr) {
     return v;
 }
 
-// The two halves of cluster_sync, for work in between.
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-__device__ __forceinline__ double ld_shared_cluster_f64(uint32_t cluster_addr) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
-    return v;
-}
-
 // Barrier `id` (1 .. 15) among `threads` threads of the block.
 __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -220,12 +205,6 @@ __device__ __forceinline__ void cp_async_wait_groups() {
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t p;
     asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
-
-__device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(lo), "r"(hi));
     return p;
 }
 
