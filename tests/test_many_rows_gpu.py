@@ -102,8 +102,48 @@ def test_norm(rows, cols, dtype, residual, bias):
         assert h3 is copy and torch.equal(copy, x) and torch.equal(y2, y)
 
 
-def test_norm_of_rows_with_nans_infinities_and_constants_between_others():
-    rows, cols = 1000, 4096
+# Rows that start anywhere, four times 152 blocks' worth and more: rows at a time of a
+# block 2, 16, 1, 5 and 2.  Pitches and offsets by which x, the residual and y start
+# differently from one another, and even ones.
+ODD = [(1300, 4001), (9800, 301), (620, 8191), (3100, 1501), (1250, 2760)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows,cols", ODD)
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("more,shift", [((0, 0, 0), (0, 0, 0)), ((0, 0, 0), (1, 1, 1)), ((1, 2, 5), (3, 0, 6)),
+                                        ((8, 3, 1), (7, 5, 2))], ids=str)
+def test_norm_of_rows_that_start_anywhere(rows, cols, dtype, residual, more, shift):
+    def view(i, seed, mean):
+        full = draw(1, rows * (cols + more[i]) + shift[i] + 9, dtype, seed, mean)[0]
+        return full, full[shift[i]:shift[i] + rows * (cols + more[i])].view(rows, -1)[:, :cols]
+    x, r = view(0, 1, 0.5)[1], view(1, 2, -0.25)[1] if residual else None
+    full, out = view(2, 3, 0.0)
+    full.fill_(7.0)
+    w, b = draw(1, cols, dtype, 4)[0], draw(1, cols + 1, dtype, 5)[0][1:]
+    y64, h64, slack = plain_norm(x, w, b, r, 1e-5)
+    y, h = T.layernorm(x, w, b, residual=r, out=out)
+    within(y, y64, slack)
+    keep = torch.ones_like(full, dtype=torch.bool)
+    keep[shift[2]:shift[2] + rows * (cols + more[2])].view(rows, -1)[:, :cols] = False
+    assert bool((full[keep] == 7.0).all())
+    if residual:
+        within(h, h64, 2.0 ** -24 * h64.abs())
+        y2, h2 = T.layernorm(x, w, b, residual=r, h_out=r)
+        assert h2 is r and torch.equal(r, h) and torch.equal(y2, y)
+    q, s, _ = T.layernorm_fp8(x, w, b, residual=None)
+    y64, _, slack = plain_norm(x, w, b, None, 1e-5)
+    spread = s.double().repeat_interleave(128, 1)[:, :cols]
+    err = (q.double() * spread - y64).abs()
+    assert bool((err <= y64.abs() * 2.0 ** -4 + spread * 2.0 ** -10 + slack * 1.1 + y64.abs() * 2.0 ** -21).all())
+    odd = torch.zeros(rows * (cols + 1) + 1, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    odd = odd[1:].view(rows, cols + 1)[:, :cols]
+    q2, s2, _ = T.layernorm_fp8(x, w, b, out=odd)
+    assert torch.equal(q2.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s2, s)
+
+
+@pytest.mark.parametrize("rows,cols", [(1000, 4096), (1300, 4097)])
+def test_norm_of_rows_with_nans_infinities_and_constants_between_others(rows, cols):
     x = draw(rows, cols, "bf16", 5)
     w, b = draw(1, cols, "bf16", 6)[0], draw(1, cols, "bf16", 7)[0]
     clean = T.layernorm(x, w, b)[0].clone()

@@ -421,6 +421,311 @@ __global__ void __launch_bounds__(kRows)
     }
 }
 
+// ---- rows that start anywhere, on their way in ------------------------------------
+//
+// Such a row (of 16-bit elements) comes in as the 16-byte pieces of memory that hold
+// it, and its threads read their columns out of what all of them have copied.  So a thread waits for a row's copies before the barrier
+// that the row before it has anyway, and what was read before a barrier makes
+// room after it.
+
+// A thread's vector c of such a row: four pairs of neighbouring columns, those of a
+// warp side by side (64 columns), 256 columns a warp.
+__device__ __forceinline__ int pair_column(int c, int k) { return (c & ~255) + ((c >> 3) & 31) * 2 + 64 * k; }
+
+// Out of shared memory, where 4 more bytes may be read behind a row; columns past its
+// end read as zero.
+__device__ __forceinline__ void load_words(const char* row, int c, int cols, uint32_t (&w)[4]) {
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(row - (reinterpret_cast<uintptr_t>(row) & 2u)) +
+                         pair_column(c, 0) / 2;
+    const uint32_t shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 2u) * 8;
+    if ((c | 255) < cols) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(at[32 * k], at[32 * k + 1], shift);
+    } else {
+        const int left = cols - pair_column(c, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = left > 64 * k
+                       ? __funnelshift_r(at[32 * k], at[32 * k + 1], shift) & (left > 64 * k + 1 ? ~0u : 0xffffu)
+                       : 0u;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void widen_words(const uint32_t (&w)[4], Eight& v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 t = unpack2<T>(w[k]);
+        v.p[k] = ptx::pair(t.x, t.y);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* row, int c, int cols, const Eight& v) {
+    uint16_t* at = reinterpret_cast<uint16_t*>(row) + pair_column(c, 0);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 t = ptx::unpair(v.p[k]);
+        w[k] = pack2<T>(t.x, t.y);
+    }
+    if ((c | 255) < cols) {
+        if ((reinterpret_cast<uintptr_t>(row) & 3u) == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(at + 64 * k) = w[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                at[64 * k] = static_cast<uint16_t>(w[k]);
+                at[64 * k + 1] = static_cast<uint16_t>(w[k] >> 16);
+            }
+        }
+    } else {
+        const int left = cols - pair_column(c, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (left > 64 * k) at[64 * k] = static_cast<uint16_t>(w[k]);
+            if (left > 64 * k + 1) at[64 * k + 1] = static_cast<uint16_t>(w[k] >> 16);
+        }
+    }
+}
+
+// Zeros for the columns past the row's end.
+__device__ __forceinline__ void keep_pairs(Eight& v, int c, int cols) {
+    if ((c | 255) < cols) return;
+    const int left = cols - pair_column(c, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 t = ptx::unpair(v.p[k]);
+        v.p[k] = ptx::pair(left > 64 * k ? t.x : 0.0f, left > 64 * k + 1 ? t.y : 0.0f);
+    }
+}
+
+__device__ __forceinline__ void load_pairs_any(const void* p, int dtype, int c, int cols, Eight& v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float t[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = pair_column(c, k) + i;
+            t[i] = at >= cols            ? 0.0f
+                   : dtype == TILES_BF16 ? to_float(static_cast<const __nv_bfloat16*>(p)[at])
+                   : dtype == TILES_F16  ? to_float(static_cast<const __half*>(p)[at])
+                                         : static_cast<const float*>(p)[at];
+        }
+        v.p[k] = ptx::pair(t[0], t[1]);
+    }
+}
+
+// As emit: the 128 columns that share a scale are two pairs of every lane.
+template <typename T, bool FP8>
+__device__ __forceinline__ void emit_pairs(const LayerArgs& a, int64_t row, int c, int cols, const Eight& d,
+                                           uint64_t rstd, uint64_t shift, const Eight& w, const Eight& b) {
+    Eight y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y.p[i] = ptx::fma2(ptx::fma2(d.p[i], rstd, shift), w.p[i], b.p[i]);
+    if constexpr (FP8) {
+        keep_pairs(y, c, cols);
+        uint8_t* const to = static_cast<uint8_t*>(a.y) + row * a.ldy;
+        const bool even = (reinterpret_cast<uintptr_t>(to) & 1u) == 0 && (c | 255) < cols;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float2 t[2] = {ptx::unpair(y.p[2 * half]), ptx::unpair(y.p[2 * half + 1])};
+            float m = max3_abs_nan(max3_abs_nan(t[0].x, t[0].y, t[1].x), t[1].y, 0.0f);
+            m = block_amax(m);
+            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float s = max_nan(__fdiv_rn(m, kE4m3Max), kTinyScale), inv = __frcp_rn(s);
+#pragma unroll
+            for (int k = 2 * half; k < 2 * half + 2; ++k) {
+                const float2 q = t[k & 1];
+                const uint32_t bytes =
+                    __nv_cvt_float2_to_fp8x2(make_float2(q.x * inv, q.y * inv), __NV_SATFINITE, __NV_E4M3);
+                const int at = pair_column(c, k);
+                if (even) {
+                    *reinterpret_cast<uint16_t*>(to + at) = static_cast<uint16_t>(bytes);
+                } else {
+                    if (at < cols) to[at] = static_cast<uint8_t>(bytes);
+                    if (at + 1 < cols) to[at + 1] = static_cast<uint8_t>(bytes >> 8);
+                }
+            }
+            const int block = (c & ~255) / kBlock + half;
+            if ((threadIdx.x & 31) == 0 && block * kBlock < cols)
+                a.scales[row * a.scale_row + block * a.scale_block] = s;
+        }
+    } else {
+        store_pairs<T>(static_cast<T*>(a.y) + row * a.ldy, c, cols, y);
+    }
+}
+
+template <typename T, int N, int VPT>
+struct OddRing {
+    static constexpr int PIECES = static_cast<int>(sizeof(T)) / 2;
+
+    char* at;                                  // the row's of the first stage
+    int pitch, stage_bytes;                    // from one matrix to the next, from one stage to the next
+
+    static constexpr size_t bytes(int threads, int per_block) {
+        return static_cast<size_t>(kStages) * N * per_block * (threads * VPT * PIECES + 2) * 16;
+    }
+    __device__ __forceinline__ explicit OddRing(uint4* smem) {
+        const int row = (static_cast<int>(blockDim.x) * VPT * PIECES + 2) * 16;
+        at = reinterpret_cast<char*>(smem) + threadIdx.y * row;
+        pitch = blockDim.y * row;
+        stage_bytes = N * pitch;
+    }
+    // Start the copies of a row.
+    __device__ __forceinline__ void copy(int stage, int n, const T* row, int cols, const Extent& e) const {
+        const int s = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);
+        const int pieces = (s + cols * static_cast<int>(sizeof(T)) + 15) / 16;
+        const char* from = reinterpret_cast<const char*>(row) - s;
+        char* to = at + stage * stage_bytes + n * pitch;
+        // What lies outside the matrix, of its first and its last row's pieces, is not read.
+        const int first = from < e.from, last = pieces - (from + pieces * 16 > e.to);
+#pragma unroll
+        for (int j = 0; j <= VPT * PIECES; ++j) {
+            const int i = j * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+            if (i >= first && i < last) ptx::cp_async_16(to + i * 16, from + i * 16);
+        }
+        if (first || last < pieces) copy_ends(to, from, pieces, e);
+    }
+    static __device__ __noinline__ void copy_ends(char* to, const char* from, int pieces, const Extent& e) {
+        const int i = threadIdx.x * static_cast<int>(sizeof(T));
+        if (i >= 16) return;
+        for (int piece : {0, pieces - 1}) {
+            const char* f = from + piece * 16 + i;
+            if (f >= e.from && f < e.to) *reinterpret_cast<T*>(to + piece * 16 + i) = *reinterpret_cast<const T*>(f);
+        }
+    }
+    // Vector j of a row whose first byte is the s-th of its first piece.
+    __device__ __forceinline__ void read(int stage, int n, int j, int s, int cols, uint32_t (&w)[4]) const {
+        load_words(at + stage * stage_bytes + n * pitch + s,
+                   (j * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8, cols, w);
+    }
+    __device__ __forceinline__ void read(int stage, int n, int j, int s, int cols, Eight& v) const {
+        uint32_t w[4];
+        read(stage, n, j, s, cols, w);
+        widen_words<T>(w, v);
+    }
+};
+
+// Rows of a matrix, one after the other, `by` rows apart: where the one lies that is
+// copied next, and where the one that is read starts in its first piece.
+template <typename T>
+struct Walk {
+    const T* ahead;
+    int64_t by;
+    int at;
+
+    __device__ __forceinline__ Walk(const void* p, int64_t row, int64_t rows_apart, int64_t ld)
+        : ahead(static_cast<const T*>(p) + row * ld), by(rows_apart * ld),
+          at(static_cast<int>(reinterpret_cast<uintptr_t>(ahead) & 15u)) {}
+    __device__ __forceinline__ int next() const { return (at + static_cast<int>(by * sizeof(T))) & 15; }
+};
+
+// A row's threads have all copied (and waited for) what they have.
+__device__ __forceinline__ void meet() {
+    if (blockDim.x > 32) ptx::named_barrier(1 + threadIdx.y, blockDim.x);
+    else __syncwarp();
+}
+
+template <typename T, int VPT, bool FP8, bool RES>
+__global__ void __launch_bounds__(kRows)
+    layernorm_odd_ring_kernel(const LayerArgs a) {
+    extern __shared__ uint4 ring_smem[];
+    __shared__ float slots[8][2][16 * 4];
+    float(*const mine)[16 * 4] = slots[blockDim.x > 32 ? threadIdx.y : 0];
+    clear_slots(&slots[0][0][0], sizeof(slots) / 4);
+    const int step = blockDim.x * 8, tid = threadIdx.x, cols = static_cast<int>(a.cols);
+    const OddRing<T, RES ? 2 : 1, VPT> ring(ring_smem);
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y, ahead = row;
+    const Extent of_x = extent_of<T>(a.x, a.rows, a.ldx, cols), of_r = extent_of<T>(a.residual, a.rows, a.ldr, cols);
+    Walk<T> x(a.x, row, stride, a.ldx), r(a.residual, row, stride, RES ? a.ldr : 0);
+    T* h = a.h ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
+    auto fetch = [&](int stage) {
+        if (ahead < a.rows) {
+            ring.copy(stage, 0, x.ahead, cols, of_x);
+            if constexpr (RES) ring.copy(stage, 1, r.ahead, cols, of_r);
+        }
+        ptx::cp_async_commit();
+        ahead += stride;
+        x.ahead += x.by;
+        if constexpr (RES) r.ahead += r.by;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(i);
+    Eight w[VPT], b[VPT], v[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        load_pairs_any(a.weight, a.weight_dtype, j * step + tid * 8, cols, w[j]);
+        b[j].fill(0.0f);
+        if (a.bias) load_pairs_any(a.bias, a.weight_dtype, j * step + tid * 8, cols, b[j]);
+    }
+    const float inv_n = 1.0f / static_cast<float>(cols);
+    auto take = [&](int stage) {
+        Eight all;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            ring.read(stage, 0, j, x.at, cols, v[j]);
+            if constexpr (RES) {
+                Eight q;
+                ring.read(stage, 1, j, r.at, cols, q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j].p[i] = ptx::add2(v[j].p[i], q.p[i]);
+            }
+            if (h) store_pairs<T>(h, j * step + tid * 8, cols, v[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) all.p[i] = j ? ptx::add2(all.p[i], v[j].p[i]) : v[j].p[i];
+        }
+        x.at = x.next();
+        if constexpr (RES) r.at = r.next();
+        if (h) h += stride * a.ldh;
+        return all.sum();
+    };
+    ptx::cp_async_wait_groups<kStages - 2>();                  // the first two rows
+    meet();
+    float s[4];
+    s[0] = row < a.rows ? take(0) : 0.0f;
+    row_sums<4, 1, 16, true>(s, mine[1]);
+    __syncwarp();
+    fetch(0);
+    float total = s[0];
+    int stage = 0, turn = 0;
+    for (; row < a.rows; row += stride, turn ^= 1) {
+        Eight d[VPT], d1, d2;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const uint64_t less = ptx::pair(-total * inv_n, -total * inv_n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[j].p[i] = ptx::add2(v[j].p[i], less);
+            keep_pairs(d[j], j * step + tid * 8, cols);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                d1.p[i] = j ? ptx::add2(d1.p[i], d[j].p[i]) : d[j].p[i];
+                d2.p[i] = j ? ptx::fma2(d[j].p[i], d[j].p[i], d2.p[i]) : ptx::mul2(d[j].p[i], d[j].p[i]);
+            }
+        }
+        s[0] = d1.sum();
+        s[1] = d2.sum();
+        s[2] = 0.0f;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if (row + stride < a.rows) s[2] = take(stage);
+        ptx::cp_async_wait_groups<kStages - 2>();              // the row after the next, for all after the barrier
+        row_sums<4, 3, 16, true>(s, mine[turn]);
+        __syncwarp();
+        fetch(stage);
+        total = s[2];
+        const float off = s[0] * inv_n, rstd = inverse_root(s[1] * inv_n, off, a.eps);
+        const uint64_t rstd2 = ptx::pair(rstd, rstd), shift = ptx::pair(-off * rstd, -off * rstd);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            emit_pairs<T, FP8>(a, row, j * step + tid * 8, cols, d[j], rstd2, shift, w[j], b[j]);
+    }
+}
+
 struct LayerGradArgs {
     int64_t rows, cols;
     const void* dy;
@@ -609,12 +914,8 @@ __global__ void __launch_bounds__(512, 2)
             }
     }
     float* out = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (column<VEC>(c, i) < cols) {
-            out[column<VEC>(c, i)] = tw[i];
-            out[a.cols + column<VEC>(c, i)] = tb[i];
-        }
+    store8<float, VEC>(out, c, cols, tw);
+    store8<float, VEC>(out + a.cols, c, cols, tb);
 }
 
 // The same with the rows' pieces 16-byte aligned and the whole row among
@@ -818,6 +1119,17 @@ int launch_layer_ring(const LayerArgs& a, const RingGeometry& g, cudaStream_t st
                   dim3(g.threads, g.per_block), smem, st, a);
 }
 
+template <typename T, bool FP8, bool RES>
+int launch_layer_odd_ring(const LayerArgs& a, const RingGeometry& g, cudaStream_t st) {
+    using R = OddRing<T, RES ? 2 : 1, kLayerVpt>;
+    static std::atomic<uint64_t> opted{0};
+    const cudaError_t e = opt_in_smem(layernorm_odd_ring_kernel<T, kLayerVpt, FP8, RES>, kRingBytesMost, &opted);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    const size_t smem = std::max(R::bytes(g.threads, g.per_block), exact_smem(1));
+    return launch(layernorm_odd_ring_kernel<T, kLayerVpt, FP8, RES>, dim3(g.blocks), dim3(g.threads, g.per_block),
+                  smem, st, a);
+}
+
 template <typename T>
 int launch_layer_any(const LayerArgs& a, bool vec, bool fp8, int sms, cudaStream_t st) {
     if constexpr (sizeof(T) == 2) {
@@ -826,8 +1138,18 @@ int launch_layer_any(const LayerArgs& a, bool vec, bool fp8, int sms, cudaStream
         // with residual 14.6 us against 18.9 without it, 16384 x 256 9.1
         // against 8.5), 16-bit (fp32: below), and where every row of a block
         // has a successor (2000 x 600: 5.8 against 4.8; 600 x 4096 6.9 against 7.8).
-        if (vec && a.cols > 256 && g.threads <= kRows &&
-            a.rows >= 2 * static_cast<int64_t>(g.per_block) * sms) {
+        const int64_t round = static_cast<int64_t>(g.per_block) * sms;
+        const bool fits = a.cols > 256 && g.threads <= kRows;
+        // Rows that start anywhere want some more rounds (2590 x 580 9.5 us, 7.6 without the
+        // ring; 12000 x 301 13.0 against 15.1).
+        if (!vec && fits && a.rows >= 4 * round) {
+            if (a.residual)
+                return fp8 ? launch_layer_odd_ring<T, true, true>(a, g, st)
+                           : launch_layer_odd_ring<T, false, true>(a, g, st);
+            return fp8 ? launch_layer_odd_ring<T, true, false>(a, g, st)
+                       : launch_layer_odd_ring<T, false, false>(a, g, st);
+        }
+        if (vec && fits && a.rows >= 2 * round) {
             if (a.residual)
                 return fp8 ? launch_layer_ring<T, true, true>(a, g, st)
                            : launch_layer_ring<T, false, true>(a, g, st);

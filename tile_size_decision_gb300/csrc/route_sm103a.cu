@@ -547,13 +547,6 @@ struct Piece {
     }
 };
 
-// The bytes of a matrix's rows that are read.
-template <typename T>
-__device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t ld, int64_t cols) {
-    const char* at = static_cast<const char*>(p);
-    return {at, at + ((rows - 1) * ld + cols) * static_cast<int64_t>(sizeof(T))};
-}
-
 // y[t] = the sum over the token's choices, in their order, in fp32.  One piece a
 // thread, its choices' loads in flight together.  K: choices at
 // a time.  ODD: rows that start anywhere.

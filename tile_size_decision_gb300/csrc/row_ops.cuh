@@ -242,6 +242,13 @@ struct Extent {
     const char* to;                           // past the last
 };
 
+// The bytes of a matrix's rows.
+template <typename T>
+__device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t ld, int64_t cols) {
+    const char* at = static_cast<const char*>(p);
+    return {at, at + ((rows - 1) * ld + cols) * static_cast<int64_t>(sizeof(T))};
+}
+
 // 16 bytes that start on any element, inside the extent: put together from the two
 // aligned pieces that hold them.
 __device__ __forceinline__ uint4 unaligned16(const char* p, const Extent& e, int elem_bytes) {
@@ -349,20 +356,17 @@ struct RowRing {
     }
 };
 
-// out[c] = the sum of the partials of column c: 16 columns a block, 64
-// threads a column, each over every 64th partial, then a tree: a fixed order.
+// out[c] = the sum of the partials of column c: COLUMNS columns a block, R threads
+// a column, each over every R-th partial, then a tree: a fixed order, which is the
+// same for every R that is no less than the partials are.
 // Partials of two gradients lie side by side ([parts][2][cols], gridDim.y 2).
-// (With 32 columns a block, 1024 columns kept only 32 SMs busy: 28.2 us for the
-// gradient of 16384 x 1024 rows against 26.8; with 8, 41.5 us against 39.0 for
-// 3000 x 8192.)
-constexpr int kReduceColumns = 16;
-__global__ void __launch_bounds__(1024) reduce_partials_kernel(const float* partials, int64_t cols,
-                                                               int parts, float* out, float* out2) {
-    constexpr int R = 1024 / kReduceColumns;
-    __shared__ float s[R][kReduceColumns + 1];
+template <int COLUMNS, int R>
+__global__ void __launch_bounds__(COLUMNS * R) reduce_partials_kernel(const float* partials, int64_t cols,
+                                                                      int parts, float* out, float* out2) {
+    __shared__ float s[R][COLUMNS + 1];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kReduceColumns + threadIdx.x;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * COLUMNS + threadIdx.x;
     const int64_t pitch = cols * gridDim.y, at = c + cols * blockIdx.y;
     float t = 0.0f;
     if (c < cols)
@@ -381,11 +385,23 @@ __global__ void __launch_bounds__(1024) reduce_partials_kernel(const float* part
 
 // ---- the host's side -----------------------------------------------------------
 
+template <int COLUMNS, int R>
+int launch_reduce_partials_of(const float* partials, int64_t cols, int parts, float* out, float* out2,
+                              cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((cols + COLUMNS - 1) / COLUMNS), out2 ? 2 : 1);
+    return launch(reduce_partials_kernel<COLUMNS, R>, grid, dim3(COLUMNS, R), 0, st, partials, cols, parts, out,
+                  out2);
+}
+
+// 64 threads a column (with 32 columns a block, 1024 columns kept only 32 SMs busy:
+// 28.2 us for the root-mean-square norm's gradient of 16384 x 1024 rows against 26.8; with
+// 8, 41.5 us against 39.0 for 3000 x 8192); few partials want no more threads than
+// they are (1 row of 8192 columns 7.0 us against 11.1, 16 of 3200 5.8 against 7.5).
 inline int launch_reduce_partials(const float* partials, int64_t cols, int parts, float* out,
                                   float* out2, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((cols + kReduceColumns - 1) / kReduceColumns), out2 ? 2 : 1);
-    return launch(reduce_partials_kernel, grid, dim3(kReduceColumns, 1024 / kReduceColumns), 0, st,
-                  partials, cols, parts, out, out2);
+    if (parts <= 8) return launch_reduce_partials_of<32, 8>(partials, cols, parts, out, out2, st);
+    if (parts <= 32) return launch_reduce_partials_of<16, 32>(partials, cols, parts, out, out2, st);
+    return launch_reduce_partials_of<16, 64>(partials, cols, parts, out, out2, st);
 }
 
 inline bool whole16(const void* p, int64_t pitch_elems, int elem_bytes) {
