@@ -769,7 +769,8 @@ int tiles_layernorm(const tiles_layernorm_desc* desc, void* stream);
  *   dweight_j = sum over rows of dy_j d_j u^(-1/2),  dbias_j = sum over rows of dy_j
  * dx is the gradient of x and of the residual alike; dh, the gradient that
  * reaches h past the norm, may be NULL.  dweight and dbias are fp32; the sums
- * over rows run in a fixed order for given sizes and device. */
+ * over rows run in a fixed order for given sizes and device.  At most 2^28
+ * columns. */
 typedef struct {
     int64_t rows, cols;
     const void* dy;

@@ -160,7 +160,8 @@ def test_norm_of_rows_with_nans_infinities_and_constants_between_others(rows, co
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("rows,cols", [(1600, 1304), (608, 4096), (5000, 264), (304, 8192), (700, 3200)])
+@pytest.mark.parametrize("rows,cols", [(1600, 1304), (608, 4096), (5000, 264), (304, 8192), (700, 3200),
+                                       (1700, 1301), (330, 5001), (200, 8191), (170, 12291), (170, 12296)])
 def test_norm_gradients(rows, cols, dtype):
     h, dy = draw(rows, cols, dtype, 8, 0.5, cols + 8), draw(rows, cols, dtype, 9)
     dh, w = draw(rows, cols, dtype, 10), draw(1, cols, dtype, 11)[0]

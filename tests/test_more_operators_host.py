@@ -125,6 +125,7 @@ def test_layernorm_refusals(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(cols=0), _abi.ERR_INVALID_ARG),
+    (dict(cols=(1 << 28) + 1), _abi.ERR_TOO_LARGE),
     (dict(dtype=_abi.E4M3), _abi.ERR_UNSUPPORTED_DTYPE),
     (dict(dweight=None), _abi.ERR_INVALID_ARG),
     (dict(dbias=None), _abi.ERR_INVALID_ARG),
