@@ -942,7 +942,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 // time (their threads meet at barriers of their own, and add their parts of the
 // gradients in the end), the next two on their way in.  The sums of one row go
 // together with the mean of the next, so that a row costs one barrier.
-// 8192 x 4096 bf16 rows with dh 53.5 us, the reduction's launch included: 75% of
+// 8192 x 4096 bf16 rows with dh 51.3 us, the reduction's launch included: 78% of
 // the measured copy bandwidth.  The instructions bound it (a vector a thread and
 // twice the threads: 77.6 us; single fp32 additions instead of pairs: 60.6).
 template <typename T, int VPT>

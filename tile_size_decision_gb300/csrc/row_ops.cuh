@@ -396,11 +396,14 @@ int launch_reduce_partials_of(const float* partials, int64_t cols, int parts, fl
 // 64 threads a column (with 32 columns a block, 1024 columns kept only 32 SMs busy:
 // 28.2 us for the root-mean-square norm's gradient of 16384 x 1024 rows against 26.8; with
 // 8, 41.5 us against 39.0 for 3000 x 8192); few partials want no more threads than
-// they are (1 row of 8192 columns 7.0 us against 11.1, 16 of 3200 5.8 against 7.5).
+// they are (1 row of 8192 columns 7.0 us against 11.1, 16 of 3200 5.8 against 7.5).  Of
+// two gradients, whose blocks are twice as many, 32 threads a column until the partials
+// are many (layer norm's gradient, 3000 x 8192 46.4 us against 51.8, 8192 x 4096 53.8
+// against 56.5; 1718 x 637, where they are 1520, 17.1 against 15.1).
 inline int launch_reduce_partials(const float* partials, int64_t cols, int parts, float* out,
                                   float* out2, cudaStream_t st) {
     if (parts <= 8) return launch_reduce_partials_of<32, 8>(partials, cols, parts, out, out2, st);
-    if (parts <= 32) return launch_reduce_partials_of<16, 32>(partials, cols, parts, out, out2, st);
+    if (parts <= 32 || (out2 && parts <= 512)) return launch_reduce_partials_of<16, 32>(partials, cols, parts, out, out2, st);
     return launch_reduce_partials_of<16, 64>(partials, cols, parts, out, out2, st);
 }
 
