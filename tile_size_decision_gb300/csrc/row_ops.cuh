@@ -249,46 +249,60 @@ __device__ __forceinline__ Extent extent_of(const void* p, int64_t rows, int64_t
     return {at, at + ((rows - 1) * ld + cols) * static_cast<int64_t>(sizeof(T))};
 }
 
-// 16 bytes that start on any element, inside the extent: put together from the two
-// aligned pieces that hold them.
-__device__ __forceinline__ uint4 unaligned16(const char* p, const Extent& e, int elem_bytes) {
-    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
-    const char* base = p - s;
-    if (s == 0) return *reinterpret_cast<const uint4*>(p);
-    uint32_t w[8];
-    if (base >= e.from && base + 32 <= e.to) {
-        const uint4 a = *reinterpret_cast<const uint4*>(base), b = *reinterpret_cast<const uint4*>(base + 16);
-        w[0] = a.x;
-        w[1] = a.y;
-        w[2] = a.z;
-        w[3] = a.w;
-        w[4] = b.x;
-        w[5] = b.y;
-        w[6] = b.z;
-        w[7] = b.w;
+// 16 bytes that start on any element, inside the extent: the two aligned pieces that
+// hold them as they lie in memory, so that many can be asked for before the first one is
+// looked at, and then what starts `shift` bytes into them.
+struct Window {
+    uint4 lo, hi;
+    int shift;
+
+    __device__ __forceinline__ void load(const char* p, const Extent& e, int elem_bytes) {
+        shift = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+        const char* base = p - shift;
+        if (base >= e.from && base + 32 <= e.to) {
+            lo = *reinterpret_cast<const uint4*>(base);
+            hi = *reinterpret_cast<const uint4*>(base + 16);
+        } else {
+            // At the ends the aligned pieces may reach out of the extent.
+            lo = hi = by_element(p, elem_bytes);
+            shift = 0;
+        }
+    }
+    static __device__ __forceinline__ uint4 by_element(const char* p, int elem_bytes) {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+        for (int i = 0; i < 4; ++i) {
+            if (elem_bytes == 4) {
+                w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+            } else if (elem_bytes == 2) {
+                const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+                w[i] = q[0] | static_cast<uint32_t>(q[1]) << 16;
+            } else {
+                const uint8_t* q = reinterpret_cast<const uint8_t*>(p) + 4 * i;
+                w[i] = q[0] | static_cast<uint32_t>(q[1]) << 8 | static_cast<uint32_t>(q[2]) << 16 |
+                       static_cast<uint32_t>(q[3]) << 24;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ uint4 get() const {
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
-        const int bits = (s & 3) * 8;
+        for (int i = 0; i < 6; ++i) w[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = shift & 4 ? w[i + 1] : w[i];
+        const int bits = (shift & 3) * 8;
         return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
                           __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
     }
-    // At the ends the aligned pieces may reach out of the extent.
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (elem_bytes == 4) {
-            w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-        } else if (elem_bytes == 2) {
-            const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
-            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 16;
-        } else {
-            const uint8_t* q = reinterpret_cast<const uint8_t*>(p) + 4 * i;
-            w[i] = q[0] | static_cast<uint32_t>(q[1]) << 8 | static_cast<uint32_t>(q[2]) << 16 |
-                   static_cast<uint32_t>(q[3]) << 24;
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+};
+
+// The same at once.
+__device__ __forceinline__ uint4 unaligned16(const char* p, const Extent& e, int elem_bytes) {
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) return *reinterpret_cast<const uint4*>(p);
+    Window w;
+    w.load(p, e, elem_bytes);
+    return w.get();
 }
 
 // Lane l's share of the warp's sums of s[0 .. N): that of s[l % N].  Each exchange
