@@ -67,6 +67,10 @@ def cases(**kw):
     bt, brows, bp = draw(5000, 520, seed=14), draw(20000, 520, seed=15), draw(5000, 4, seed=16)
     grads = [draw(1000), draw(33, dtype=f32), draw(7, 9, dtype=torch.float16)]
     large = [draw(3000000, seed=17), draw(100001, dtype=f32, seed=18)]
+    several = [draw(700 + i, seed=i) for i in range(300)]
+    ring, odd = draw(1300, 4096, seed=19), draw(1300, 4001, seed=20)
+    wr, wo = draw(4096, seed=21), draw(4001, seed=22)
+    ot, orows = draw(5000, 133, seed=23), draw(20000, 133, seed=24)
 
     def for_call(t):
         """t, made on the current stream, for a call on the given one."""
@@ -97,6 +101,9 @@ def cases(**kw):
                                           h_out=outs(5, 310)[:, :300], **kw),
         "norm parameter": lambda: T.layernorm(x, torch.nn.Parameter(w), **kw),
         "norm large": lambda: T.layernorm(big, wb, wb, residual=bigger, **kw),
+        "norm many rows": lambda: T.layernorm(ring, wr, wr, residual=ring, **kw),
+        "norm many odd rows": lambda: T.layernorm(odd, wo, wo, residual=odd, **kw),
+        "norm fp8 many odd rows": lambda: T.layernorm_fp8(odd, wo, **kw),
         "norm fp8": lambda: T.layernorm_fp8(x, w, b, **kw),
         "norm fp8 large": lambda: T.layernorm_fp8(big, wb, residual=bigger, **kw),
         "norm fp8 given": lambda: T.layernorm_fp8(
@@ -105,6 +112,7 @@ def cases(**kw):
         "norm of no rows": lambda: T.layernorm_fp8(x[:0], w, **kw),
         "norm grad": lambda: T.layernorm_grad(r, x, w, **kw),
         "norm grad large": lambda: T.layernorm_grad(big, bigger, wb, dh=big, **kw),
+        "norm grad many odd rows": lambda: T.layernorm_grad(odd, odd, wo, dh=odd, **kw),
         "norm grad given": lambda: T.layernorm_grad(
             r, x, w, dh=x, dx_out=outs(5, 300), dweight_out=outs(300, dtype=f32),
             dbias_out=outs(300, dtype=f32), workspace=for_call(T.layernorm_grad_workspace(x)), **kw),
@@ -114,6 +122,7 @@ def cases(**kw):
         "sort of no rows": lambda: T.expert_sort(ids[:0], 6, **kw),
         "dispatch": lambda: T.expert_dispatch(t, slots, **kw),
         "dispatch large": lambda: T.expert_dispatch(bt, mslots, out=outs(20000, 520), **kw),
+        "dispatch odd": lambda: T.expert_dispatch(ot, mslots, out=outs(20000, 133), **kw),
         "dispatch fp8": lambda: T.expert_dispatch(q, slots, scales=s, **kw),
         "dispatch fp8 given": lambda: T.expert_dispatch(
             q, slots, scales=s, out=outs(130, 200, dtype=torch.float8_e4m3fn),
@@ -121,6 +130,8 @@ def cases(**kw):
         "combine": lambda: T.expert_combine(rows, slots, p, **kw),
         "combine plain": lambda: T.expert_combine(rows, slots, **kw),
         "combine large": lambda: T.expert_combine(brows, mslots, bp, **kw),
+        "combine odd": lambda: T.expert_combine(orows, mslots, bp, **kw),
+        "combine grad odd": lambda: T.expert_combine_grad(ot, orows, mslots, bp, drows_out=outs(20000, 133), **kw),
         "combine given": lambda: T.expert_combine(rows, slots, p.half(), out=outs(40, 210)[:, 3:203], **kw),
         "combine grad": lambda: T.expert_combine_grad(dy, rows, slots, p, **kw),
         "combine grad large": lambda: T.expert_combine_grad(
@@ -129,6 +140,8 @@ def cases(**kw):
         "grad norm large": lambda: T.grad_norm(large, **kw),
         "clip": lambda: clipped(grads, 0.5),
         "clip large": lambda: clipped(large, 2, 0.0),
+        "clip of 300": lambda: clipped(several, 0.5),
+        "clip of 300 in place": lambda: in_place(several, 0.5),
         "clip in place": lambda: in_place(grads, 0.5),
         "clip large in place": lambda: in_place(large, 0.5),
     }
