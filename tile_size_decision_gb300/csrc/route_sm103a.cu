@@ -127,10 +127,9 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a) {
     for (int i = tid; i < warps * pitch / 2; i += threads) reinterpret_cast<uint32_t*>(rank)[i] = 0;
     for (int g = tid; g < groups; g += threads) start[g] = below[g] = 0;
     __syncthreads();
-    // With several blocks the counting kernel went before.  It let this one start
-    // after its own wait, so what came before it (the ids) is there: only the
-    // counts have to be waited for, below.
-    if (gridDim.x == 1) ptx::grid_dependency_wait();
+    // The ids too are there only after this wait: that the counting kernel has waited for
+    // them promises this one nothing.
+    ptx::grid_dependency_wait();
     uint16_t* mine = rank + warp * pitch;
     const uint32_t first = blockIdx.x * threads * I + warp * 32 * I + lane;
     uint32_t key[I];
@@ -162,13 +161,11 @@ __global__ void __launch_bounds__(1024) sort_place_kernel(const SortArgs a) {
         if (gridDim.x == 1) start[g] = run;
     }
     if (gridDim.x > 1 && a.below) {
-        ptx::grid_dependency_wait();
         for (int g = tid; g < groups; g += threads) {
             start[g] = a.totals[g];
             below[g] = a.below[static_cast<int64_t>(blockIdx.x) * groups + g];
         }
     } else if (gridDim.x > 1) {
-        ptx::grid_dependency_wait();
         // `side` threads share an expert's column of counts.
         const int side = max(1, threads / groups);
         for (int i = tid; i < side * groups; i += threads) {
@@ -234,16 +231,15 @@ SortGeometry sort_geometry(int64_t pairs, int64_t groups) {
     g.blocks = 1;
     g.scan = false;
     if (pairs <= 1024) {
-        // One block, one launch (512 pairs among 64 experts 2.4 us, 2.4 with two
-        // launches; 4096 pairs 7.8 against 4.2).  A warp's counts of 4096 experts
-        // are 8 KB.
+        // One block, one launch (512 pairs among 64 experts 2.3 us; 4096 pairs 7.7, two
+        // launches 4.8).  A warp's counts of 4096 experts are 8 KB.
         const int most = groups > 1024 ? 512 : 1024;
         g.threads = static_cast<int>(std::min<int64_t>(most, (std::max(pairs, groups) + 31) / 32 * 32));
         while (pairs > static_cast<int64_t>(g.threads) * g.items) g.items *= 2;
         return g;
     }
     // Blocks of 1024 pairs, of 512 where that leaves SMs without (131072 pairs
-    // among 64 experts: 6.1 us, 9.0 with 1024 threads of a pair, 7.0 with 2048
+    // among 64 experts: 7.5 us, 10.4 with 1024 threads of a pair, 9.4 with 2048
     // pairs a block); more pairs a thread where there are more than two blocks
     // an SM.
     g.threads = pairs <= 65536 && groups <= 256 ? 256 : 512;
@@ -252,8 +248,8 @@ SortGeometry sort_geometry(int64_t pairs, int64_t groups) {
     const int64_t share = static_cast<int64_t>(g.threads) * g.items;
     g.blocks = static_cast<int>((pairs + share - 1) / share);
     // Every block adds up the blocks' counts itself, or a launch of its own does:
-    // 24 loads a thread are about a launch (131072 pairs: 64 experts 6.1 us against
-    // 7.0, 256 experts 11.8 against 7.6, 4096 experts 103 against 17.5).
+    // 24 loads a thread are about a launch (131072 pairs: 64 experts 7.5 us against
+    // 8.6, 256 experts 13.4 against 9.3, 4096 experts 106 against 18.4).
     g.scan = g.blocks > 1 && g.blocks * groups > 24 * static_cast<int64_t>(g.threads);
     return g;
 }
