@@ -741,7 +741,8 @@ int tiles_grouped_wgrad(const tiles_wgrad_desc* desc, void* workspace, size_t ws
  * the mean is corrected by the mean of what is left after it, so that rows
  * far from zero keep their spread.  out_dtype is dtype or E4M3, with the
  * scales of tiles_rmsnorm.  A NaN or an infinity in a row makes the row's y (or
- * its scales) NaN. */
+ * its scales) NaN, and so does a row whose sum of h or of d^2 leaves fp32's
+ * range (deviations of some 1.8e19 / sqrt(cols)). */
 typedef struct {
     int64_t rows, cols;               /* rows >= 0, cols >= 1 */
     const void* x;                    /* device, rows x cols */
@@ -769,8 +770,8 @@ int tiles_layernorm(const tiles_layernorm_desc* desc, void* stream);
  *   dweight_j = sum over rows of dy_j d_j u^(-1/2),  dbias_j = sum over rows of dy_j
  * dx is the gradient of x and of the residual alike; dh, the gradient that
  * reaches h past the norm, may be NULL.  dweight and dbias are fp32; the sums
- * over rows run in a fixed order for given sizes and device.  At most 2^28
- * columns. */
+ * over rows run in a fixed order for given sizes and device.  A row whose y is
+ * NaN has NaN for dx and makes dweight NaN.  At most 2^28 columns. */
 typedef struct {
     int64_t rows, cols;
     const void* dy;

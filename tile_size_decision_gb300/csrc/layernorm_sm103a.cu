@@ -102,9 +102,10 @@ __device__ __forceinline__ void clear_slots(float* slots, int n) {
 }
 
 // (var + eps)^(-1/2) from the mean of d^2 and of d.  The variance is no less
-// than 0, whatever the two roundings leave; a NaN stays one.
+// than 0, whatever the two roundings leave; a NaN stays one, and squares whose sum
+// leaves fp32's range make one: the root of an infinity would be 0 and y the bias.
 __device__ __forceinline__ float inverse_root(float square, float off, float eps) {
-    const float var = square - off * off;
+    const float var = fmaf(square, 0.0f, square - off * off);
     return rsqrtf((var < 0.0f ? 0.0f : var) + eps);
 }
 
