@@ -573,7 +573,9 @@ def selftest_drop_stage(stage: int, limit_ns: int) -> None:
 # that stream, as after any PyTorch operation on it: used on another one, they
 # are the caller's to order (wait_stream, record_stream).  Outputs that the
 # caller gives may not overlap an input, but for a norm's h_out and the gradients
-# that clip_grads scales in place.
+# that clip_grads scales in place.  Of what layernorm, the routing calls and
+# clip_grads write into the caller's tensors autograd learns, as of any operation in
+# place.
 
 
 class _NoCalls:
@@ -1054,6 +1056,13 @@ def _scratch(workspace, nbytes, where, device):
     return (workspace, *_workspace_args(workspace))
 
 
+def _wrote(*tensors):
+    """Raises the versions of the caller's tensors that a call has written."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            _torch().autograd.graph.increment_version(t)
+
+
 def _matrices(*named):
     for name, t in named:
         if t is not None and t.dim() != 2:
@@ -1069,7 +1078,7 @@ def _layernorm(x, weight, bias, residual, eps, out, scales, h_out, stream, fp8):
     torch, codes = _torch(), _codes()
     _matrices(("x", x), ("residual", residual), ("out", out), ("h_out", h_out))
     rows, cols = x.shape
-    y_type = torch.float8_e4m3fn if fp8 else x.dtype
+    y_type, given = torch.float8_e4m3fn if fp8 else x.dtype, (out, scales, h_out)
     _demand(("x", x, None, set(codes)), ("weight", weight, (cols,), set(codes)),
             ("bias", bias, (cols,), weight.dtype), ("residual", residual, x.shape, x.dtype),
             ("h_out", h_out, x.shape, x.dtype), ("out", out, x.shape, y_type))
@@ -1093,6 +1102,7 @@ def _layernorm(x, weight, bias, residual, eps, out, scales, h_out, stream, fp8):
                         0 if h_out is None else _pitch(h_out), _pitch(out), sr, sb, eps,
                         codes[x.dtype], codes[weight.dtype], _abi.E4M3 if fp8 else codes[x.dtype])
     _check(load().tiles_layernorm(d, _raw_stream(stream)), "tiles_layernorm")
+    _wrote(*given)
     return out, scales, x if h_out is None else h_out
 
 
@@ -1160,6 +1170,7 @@ def layernorm_grad(dy, h, weight, eps=1e-5, dh=None, dx_out=None, dweight_out=No
                              0 if dh is None else _pitch(dh), _pitch(dx), eps, codes[h.dtype],
                              codes[weight.dtype], 0)
     _check(load().tiles_layernorm_grad(d, ws, wsb, _raw_stream(stream)), "tiles_layernorm_grad")
+    _wrote(dx_out, dweight_out, dbias_out)
     return dx, dw, db
 
 
@@ -1210,7 +1221,7 @@ def expert_dispatch(x, slots, scales=None, out=None, scales_out=None, stream=Non
     if scales is None and scales_out is not None:
         raise ValueError("scales_out goes with scales")
     k, nb = slots.shape[1], _blocks(cols)
-    rows = tokens * k if out is None else out.shape[0]
+    rows, given = tokens * k if out is None else out.shape[0], (out, scales_out)
     with _on(stream):
         if out is None:
             pitch = (cols + 15) // 16 * 16 if x.dtype == fp8 else cols
@@ -1228,6 +1239,7 @@ def expert_dispatch(x, slots, scales=None, out=None, scales_out=None, stream=Non
                        _at(scales), _at(scales_out), _pitch(slots), _pitch(x), _pitch(out),
                        *strides, _abi.E4M3 if x.dtype == fp8 else codes[x.dtype], 0)
     _check(load().tiles_expert_dispatch(d, _raw_stream(stream)), "tiles_expert_dispatch")
+    _wrote(*given)
     return out if scales is None else (out, scales_out)
 
 
@@ -1244,6 +1256,7 @@ def expert_combine(rows, slots, weights=None, out=None, stream=None):
     (n, cols), (tokens, k) = rows.shape, slots.shape
     _demand(("rows", rows, None, set(codes)), ("slots", slots, None, torch.int32),
             ("weights", weights, (tokens, k), set(codes)), ("out", out, (tokens, cols), rows.dtype))
+    given = out
     if out is None:
         with _on(stream):
             out = torch.empty((tokens, cols), dtype=rows.dtype, device=rows.device)
@@ -1253,6 +1266,7 @@ def expert_combine(rows, slots, weights=None, out=None, stream=None):
                       _pitch(rows), 0, _pitch(out), 0, codes[rows.dtype],
                       0 if weights is None else codes[weights.dtype])
     _check(load().tiles_expert_combine(d, _raw_stream(stream)), "tiles_expert_combine")
+    _wrote(given)
     return out
 
 
@@ -1283,6 +1297,7 @@ def expert_combine_grad(dy, rows, slots, weights, drows_out=None, dweights_out=N
                       _pitch(weights), _pitch(rows), _pitch(dy), _pitch(drows), _pitch(dw),
                       codes[rows.dtype], codes[weights.dtype])
     _check(load().tiles_expert_combine_grad(d, _raw_stream(stream)), "tiles_expert_combine_grad")
+    _wrote(drows_out, dweights_out)
     return drows, dw
 
 
@@ -1336,6 +1351,8 @@ def _clip(grads, max_norm, eps, out, workspace, stream):
         s = load().tiles_clip_grads(bytes(packed), len(grads), max_norm, eps, norm.data_ptr(), ws,
                                     wsb, _raw_stream(stream))
     _check(s, where)
+    if max_norm is not None:
+        _wrote(*(grads if out is None else out))
     return norm
 
 

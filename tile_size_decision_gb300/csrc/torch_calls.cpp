@@ -500,9 +500,20 @@ struct Scratch {
     }
 };
 
+// Autograd learns what a call has written into the caller's tensor, as of any
+// operation in place.  (It never throws: the call has been made.)
+void wrote(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+PyObject* written(PyObject* arg) {
+    if (arg != Py_None) wrote(THPVariable_Unpack(arg));
+    return given(arg);
+}
+
 // A new output, or the caller's argument.
 PyObject* made_or(at::Tensor& made, PyObject* arg) {
-    return made.defined() ? THPVariable_Wrap(std::move(made)) : given(arg);
+    return made.defined() ? THPVariable_Wrap(std::move(made)) : written(arg);
 }
 
 // x, weight, bias, residual, eps, out, scales, h_out, stream, fp8 -> (y, scales, h)
@@ -573,7 +584,7 @@ PyObject* layernorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
         d.y = out->data_ptr();
         run([&] { return calls.layernorm(&d, stream.at); });
         PyObject* h = new_h.defined() ? THPVariable_Wrap(std::move(new_h))
-                                      : given(h_out ? args[7] : args[0]);
+                                      : h_out ? written(args[7]) : given(args[0]);
         PyObject* r = PyTuple_New(3);
         PyTuple_SET_ITEM(r, 0, made_or(new_out, args[5]));
         PyTuple_SET_ITEM(r, 1, made_or(new_scales, args[6]));
@@ -870,6 +881,8 @@ PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t n) {
                 return calls.clip_grads(tensors.data(), count, max_norm, eps, at, ws.given.at,
                                         ws.given.bytes, stream.at);
             });
+            PyObject* const to = apart ? args[3] : args[0];
+            for (Py_ssize_t i = 0; i < count; ++i) wrote(THPVariable_Unpack(PyList_GET_ITEM(to, i)));
         }
         return THPVariable_Wrap(std::move(norm));
     });
