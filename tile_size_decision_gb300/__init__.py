@@ -649,6 +649,13 @@ def _blocks(n):
     return (n + SCALE_BLOCK - 1) // SCALE_BLOCK
 
 
+def _tensors(*named):
+    """Raises for the first that is no tensor."""
+    for name, t in named:
+        if not hasattr(t, "data_ptr"):
+            raise TypeError(f"{name} must be a tensor, not {type(t).__name__}")
+
+
 def _demand(*rules):
     """Raises for the first (name, tensor, shape, dtype) that is not a CUDA tensor
     of that shape and type with unit stride in its last dimension (shape:
@@ -656,6 +663,7 @@ def _demand(*rules):
     for name, t, shape, dtype in rules:
         if t is None:
             continue
+        _tensors((name, t))
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if shape is not None and tuple(t.shape) != tuple(shape):
@@ -1065,17 +1073,22 @@ def _wrote(*tensors):
 
 def _matrices(*named):
     for name, t in named:
-        if t is not None and t.dim() != 2:
+        if t is None:
+            continue
+        _tensors((name, t))
+        if t.dim() != 2:
             raise ValueError(f"{name} must be a matrix")
 
 
 def _fp8_scales(name, t, rows, nb):
+    _tensors((name, t))
     if t.shape != (rows, nb) or t.dtype != _torch().float32 or not t.is_cuda:
         raise ValueError(f"{name} must be a float32 CUDA tensor of shape {(rows, nb)}")
 
 
 def _layernorm(x, weight, bias, residual, eps, out, scales, h_out, stream, fp8):
     torch, codes = _torch(), _codes()
+    _tensors(("x", x), ("weight", weight))
     _matrices(("x", x), ("residual", residual), ("out", out), ("h_out", h_out))
     rows, cols = x.shape
     y_type, given = torch.float8_e4m3fn if fp8 else x.dtype, (out, scales, h_out)
@@ -1133,6 +1146,7 @@ def layernorm_fp8(x, weight, bias=None, residual=None, eps=1e-5, out=None, scale
 
 def layernorm_grad_workspace(x):
     """A workspace for layernorm_grad on matrices of x's shape."""
+    _tensors(("x", x))
     rows, cols = x.shape
     n = int(load().tiles_layernorm_grad_workspace_bytes(rows, cols))
     if n == 0:
@@ -1151,6 +1165,7 @@ def layernorm_grad(dy, h, weight, eps=1e-5, dh=None, dx_out=None, dweight_out=No
     if r is not None:
         return r
     torch, codes = _torch(), _codes()
+    _tensors(("h", h), ("dy", dy), ("weight", weight))
     _matrices(("h", h), ("dy", dy), ("dh", dh), ("dx_out", dx_out))
     rows, cols = h.shape
     f32 = torch.float32
@@ -1186,6 +1201,7 @@ def expert_sort(experts, groups, workspace=None, stream=None):
     if r is not None:
         return r
     torch = _torch()
+    _tensors(("experts", experts))
     _matrices(("experts", experts))
     _demand(("experts", experts, None, (torch.int32, torch.int64)))
     _here(experts)
@@ -1214,6 +1230,7 @@ def expert_dispatch(x, slots, scales=None, out=None, scales_out=None, stream=Non
         return r
     torch, codes = _torch(), _codes()
     fp8 = torch.float8_e4m3fn
+    _tensors(("x", x), ("slots", slots))
     _matrices(("x", x), ("slots", slots), ("out", out))
     tokens, cols = x.shape
     _demand(("x", x, None, {*codes, fp8}), ("slots", slots, (tokens, slots.shape[1]), torch.int32),
@@ -1252,6 +1269,7 @@ def expert_combine(rows, slots, weights=None, out=None, stream=None):
     if r is not None:
         return r
     torch, codes = _torch(), _codes()
+    _tensors(("rows", rows), ("slots", slots))
     _matrices(("rows", rows), ("slots", slots))
     (n, cols), (tokens, k) = rows.shape, slots.shape
     _demand(("rows", rows, None, set(codes)), ("slots", slots, None, torch.int32),
@@ -1280,6 +1298,7 @@ def expert_combine_grad(dy, rows, slots, weights, drows_out=None, dweights_out=N
     if r is not None:
         return r
     torch, codes = _torch(), _codes()
+    _tensors(("dy", dy), ("rows", rows), ("slots", slots), ("weights", weights))
     _matrices(("rows", rows), ("slots", slots))
     (n, cols), (tokens, k) = rows.shape, slots.shape
     _demand(("rows", rows, None, set(codes)), ("dy", dy, (tokens, cols), rows.dtype),
@@ -1322,8 +1341,7 @@ def _clip(grads, max_norm, eps, out, workspace, stream):
     for i, g in enumerate(grads):
         o = None if out is None else out[i]
         for name, t in ((f"grads[{i}]", g), (f"out[{i}]", o))[:1 if out is None else 2]:
-            if not hasattr(t, "data_ptr"):
-                raise TypeError(f"{name} must be a tensor")
+            _tensors((name, t))
             if not t.is_cuda:
                 raise ValueError(f"{name} must be a CUDA tensor")
             if t.dtype not in codes:
@@ -1356,9 +1374,13 @@ def _clip(grads, max_norm, eps, out, workspace, stream):
     return norm
 
 
-def _listed(tensors):
+def _listed(name, tensors):
     """A list of tensors: of one, of any iterable."""
-    return [tensors] if hasattr(tensors, "data_ptr") else list(tensors)
+    if hasattr(tensors, "data_ptr"):
+        return [tensors]
+    if not hasattr(tensors, "__iter__"):
+        raise TypeError(f"{name} must be tensors, not {type(tensors).__name__}")
+    return list(tensors)
 
 
 def grad_norm(grads, workspace=None, stream=None):
@@ -1366,7 +1388,7 @@ def grad_norm(grads, workspace=None, stream=None):
     gradients (fp16, bf16, fp32, mixed as they come; elements that lie together,
     in any order): an fp32 tensor without dimensions, which stays on the
     device."""
-    grads = _listed(grads)
+    grads = _listed("grads", grads)
     r = (_CALLS or _compiled()).clip_grads(grads, None, 0.0, None, workspace, stream)
     return _clip(grads, None, 0.0, None, workspace, stream) if r is None else r
 
@@ -1376,7 +1398,7 @@ def clip_grads(grads, max_norm, eps=1e-6, out=None, workspace=None, stream=None)
     grad_norm gives it, in place or into the tensors of out; returns the norm
     before.  Nothing waits for the device.  No tensor may come twice or overlap
     another.  An infinite norm leaves zeros and NaNs, a NaN leaves NaNs."""
-    grads, out = _listed(grads), None if out is None else _listed(out)
+    grads, out = _listed("grads", grads), None if out is None else _listed("out", out)
     if max_norm is None:
         raise TypeError("max_norm must be a number")
     r = (_CALLS or _compiled()).clip_grads(grads, max_norm, eps, out, workspace, stream)
